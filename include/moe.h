@@ -383,6 +383,126 @@ moe_status moe_forward_w8a8_blocks(const moe_shape *shape, const void *x, const 
                                    void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * ---- training the router -----------------------------------------------------
+ * What a router is trained with beside the forward pass above: the balance
+ * loss with its per-expert counts, dropout from a counter-based generator, and
+ * the backward passes of the combine and of the routing.  A step runs
+ *     moe_route -> moe_permute -> moe_expert_ffn* -> moe_combine_dropout,
+ *     moe_balance_loss,
+ *     moe_combine_backward (d_y -> d_topk_w), moe_route_backward (-> d_logits),
+ * and the caller's own product of d_logits with x is the gradient of w_g.
+ * The routed expert weights stay frozen unless the caller differentiates the
+ * expert FFN; d_y_perm of moe_combine_backward is what that would start from.
+ *
+ * `logits` [T][E] (fp32) are the scores whose softmax or sigmoid the router
+ * takes: s for MOE_ROUTER_SIGMOID, s + b for MOE_ROUTER_SOFTMAX (what
+ * moe_route's logits_out gives for that router).  They are finite, or -inf for
+ * an expert a token may not take (its probability and gradient are 0).
+ *
+ * token_mask [T] (bytes, may be NULL): a token with a 0 takes no part -- it is
+ * not counted, and its row of d_logits is 0; its logits are not used.
+ * seq_offsets [n_seq + 1] (int32, ascending, within [0, T]): sequence g is the
+ * tokens [seq_offsets[g], seq_offsets[g + 1]), possibly none; tokens before the
+ * first or after the last are as masked.  NULL stands for one sequence of all
+ * T tokens (n_seq = 1).  n_seq <= 2^20.
+ *
+ * Every result is the same bits on every run: sums go in a fixed order, and no
+ * floating-point atomic is used.
+ */
+
+/* Bytes of workspace for moe_balance_loss; 0 for an invalid shape or n_seq. */
+size_t moe_balance_workspace_bytes(const moe_shape *shape, int32_t n_seq);
+
+/*
+ * Balance loss and per-expert counts (auxiliary balance loss of the f_i P_i
+ * form [S section 2.1, its formula lost there]).  Over the n_g tokens of
+ * sequence g that take part, with p_te the softmax of a token's logits over all
+ * E experts, or sigmoid / (sum of the E sigmoids) for MOE_ROUTER_SIGMOID:
+ *   counts[g][e]     = number of slots with topk_idx == e       (int32)
+ *   mean_probs[g][e] = P_ge = sum_t p_te / n_g                   (fp32)
+ *   f_ge             = E counts[g][e] / (K n_g)
+ *   loss             = alpha / n_seq * sum_g sum_e f_ge P_ge     (fp32, one value)
+ * A sequence none of whose tokens take part has zeros and adds nothing.
+ * n_g is counted as (sum of counts[g]) / K.  An expert id outside [0, E) is
+ * recorded as MOE_ERR_BOUNDS and its slot dropped; so are offsets that do not
+ * ascend within [0, T], whose sequences' results are then unspecified.
+ * Shape fields used: T, E, K, router.
+ */
+moe_status moe_balance_loss(const moe_shape *shape, const float *logits,
+                            const int32_t *topk_idx, const uint8_t *token_mask,
+                            const int32_t *seq_offsets, int32_t n_seq, float alpha,
+                            int32_t *counts, float *mean_probs, float *loss,
+                            void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Gradient of the routing with respect to the logits, both parts in one pass:
+ *  - the balance loss's (counts non-NULL: as moe_balance_loss wrote them; they
+ *    are constants of the gradient), times *d_loss (a device value; NULL is 1):
+ *      a_ge = d_loss alpha E counts[g][e] / (n_seq K n_g^2)
+ *      softmax: p_te (a_ge - sum_i p_ti a_gi)
+ *      sigmoid: p_te (1 - sigmoid(z_te)) (a_ge - sum_i p_ti a_gi)
+ *  - the routing weights' (d_topk_w [T][K] non-NULL), at the K picked experts,
+ *    w the weights of moe_route:
+ *      softmax: w_k (dw_k - sum_j w_j dw_j)
+ *      sigmoid: a_k (1 - a_k) (dw_k - sum_j w_j dw_j) / (sum_j a_j + 1e-6)
+ * One of counts and d_topk_w must be given.  d_logits [T][E] (fp32) is written
+ * whole.  An expert id outside [0, E) adds nothing.
+ */
+moe_status moe_route_backward(const moe_shape *shape, const float *logits,
+                              const int32_t *topk_idx, const float *d_topk_w,
+                              const uint8_t *token_mask, const int32_t *seq_offsets,
+                              int32_t n_seq, float alpha, const int32_t *counts,
+                              const float *d_loss, float *d_logits, void *stream);
+
+/*
+ * Dropout with a mask that is never stored: y = residual + D(x) over n
+ * elements of `dtype` (residual may be NULL), added in fp32 and rounded once.
+ *   thr = round(65536 p);  D(x)_i = u_i >= thr ? x_i * 65536 / (65536 - thr) : 0
+ * with u_i 16 bits of Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel
+ * random numbers: as easy as 1, 2, 3", SC 2011): counter words (low and high
+ * half of i / 8, low and high half of rng[1]), key the halves of rng[0]; u_i is
+ * half i % 2 (low first) of output word (i % 8) / 2.
+ * rng: two device words {seed, offset} -- on the device so that a captured
+ * graph draws new masks when the caller changes them; a call consumes one
+ * offset.  D is its own transpose: the gradient of x is moe_dropout of the
+ * output's gradient with the same rng (residual NULL).
+ * p is in [0, 1]; with thr = 0 nothing is drawn and rng may be NULL; a dropped
+ * element is 0 whatever x holds.  y may be x or residual itself.
+ * n == 0 is a no-op.
+ */
+moe_status moe_dropout(int64_t n, int32_t dtype, const void *x, const void *residual,
+                       double p, const uint64_t *rng, void *y, void *stream);
+
+/*
+ * moe_combine with dropout on its sum and the residual stream:
+ *   y[t] = residual[t] + D(y_shared[t] + sum_j topk_w[t][j] * y_perm[inv_perm[t*K+j]])
+ * in fp32, rounded once; D and rng as in moe_dropout on the [T][d] sum.
+ * y_shared and residual may be NULL; y may be either of them.  Slots with
+ * inv_perm outside [0, T*K) add nothing, as in moe_combine.
+ */
+moe_status moe_combine_dropout(const moe_shape *shape, const void *y_perm,
+                               const int32_t *inv_perm, const float *topk_w,
+                               const void *y_shared, const void *residual, double p,
+                               const uint64_t *rng, void *y, void *stream);
+
+/*
+ * Backward pass of moe_combine_dropout (of moe_combine with p = 0), from the
+ * output's gradient d_y [T][d]; dz = D(d_y) with the forward call's p and rng:
+ *   d_topk_w[t][j]              = <dz[t], y_perm[inv_perm[t*K+j]]>     (fp32)
+ *   d_y_perm[inv_perm[t*K+j]]   = topk_w[t][j] * dz[t]                 [T*K][d]
+ *   d_shared[t]                 = dz[t]                                [T][d]
+ * each output may be NULL, not all three (the residual's gradient is d_y).
+ * y_perm may be NULL without d_topk_w, topk_w without d_y_perm.  d_y_perm may
+ * be y_perm itself and d_shared d_y.  A slot with inv_perm outside [0, T*K)
+ * has d_topk_w 0; rows of d_y_perm that no slot names are not written.
+ */
+moe_status moe_combine_backward(const moe_shape *shape, const void *d_y,
+                                const void *y_perm, const int32_t *inv_perm,
+                                const float *topk_w, double p, const uint64_t *rng,
+                                void *d_y_perm, float *d_topk_w, void *d_shared,
+                                void *stream);
+
+/*
  * Reads the device error word of `workspace` (a device pointer passed to a
  * previous call) into *code_out (a HOST pointer): MOE_OK, MOE_ERR_TIMEOUT or
  * MOE_ERR_BOUNDS.  Synchronous (one 16-byte device-to-host copy of the error

@@ -27,7 +27,9 @@ EXPORTED = ("moe_status_string", "moe_workspace_bytes", "moe_route", "moe_permut
             "moe_quantize_fp8_rows", "moe_expert_ffn_fp8", "moe_forward_fp8",
             "moe_quantize_fp8_blocks", "moe_expert_ffn_fp8_blocks", "moe_forward_fp8_blocks",
             "moe_expert_ffn_w8a8", "moe_forward_w8a8", "moe_expert_ffn_w8a8_blocks",
-            "moe_forward_w8a8_blocks", "moe_get_device_error")
+            "moe_forward_w8a8_blocks", "moe_balance_workspace_bytes", "moe_balance_loss",
+            "moe_route_backward", "moe_dropout", "moe_combine_dropout", "moe_combine_backward",
+            "moe_get_device_error")
 FP8_BLOCK = 128  # side of the square weight-scale blocks of the *_fp8_blocks calls
 
 
@@ -81,12 +83,21 @@ def _load_lib() -> ctypes.CDLL:
     lib.moe_forward_w8a8.argtypes = [sp, vp, vp, vp, fp, vp, vp, sz, vp]
     lib.moe_expert_ffn_w8a8_blocks.argtypes = lib.moe_expert_ffn_w8a8.argtypes
     lib.moe_forward_w8a8_blocks.argtypes = lib.moe_forward_w8a8.argtypes
+    f64, f32 = ctypes.c_double, ctypes.c_float
+    lib.moe_balance_workspace_bytes.argtypes = [sp, i32]
+    lib.moe_balance_workspace_bytes.restype = sz
+    lib.moe_balance_loss.argtypes = [sp, vp, vp, vp, vp, i32, f32, vp, vp, vp, vp, sz, vp]
+    lib.moe_route_backward.argtypes = [sp, vp, vp, vp, vp, vp, i32, f32, vp, vp, vp, vp]
+    lib.moe_dropout.argtypes = [ctypes.c_int64, i32, vp, vp, f64, vp, vp, vp]
+    lib.moe_combine_dropout.argtypes = [sp, vp, vp, vp, vp, vp, f64, vp, vp, vp]
+    lib.moe_combine_backward.argtypes = [sp, vp, vp, vp, vp, f64, vp, vp, vp, vp, vp]
     lib.moe_get_device_error.argtypes = [vp, ctypes.POINTER(i32)]
     for f in ("moe_route", "moe_permute", "moe_permute_noalloc", "moe_expert_ffn", "moe_combine",
               "moe_forward", "moe_quantize_fp8_rows", "moe_expert_ffn_fp8", "moe_forward_fp8",
               "moe_quantize_fp8_blocks", "moe_expert_ffn_fp8_blocks", "moe_forward_fp8_blocks",
               "moe_expert_ffn_w8a8", "moe_forward_w8a8", "moe_expert_ffn_w8a8_blocks",
-              "moe_forward_w8a8_blocks", "moe_get_device_error"):
+              "moe_forward_w8a8_blocks", "moe_balance_loss", "moe_route_backward", "moe_dropout",
+              "moe_combine_dropout", "moe_combine_backward", "moe_get_device_error"):
         getattr(lib, f).restype = i32
     return lib
 
@@ -280,6 +291,121 @@ def moe_forward_w8a8_blocks(shape, x, w_g, bias, w: moe_fp8_experts, y, workspac
     _check(_lib.moe_forward_w8a8_blocks(ctypes.byref(shape), _p(x), _p(w_g), _p(bias),
                                         ctypes.byref(w), _p(y), ws, nws, _stream(stream)),
            "moe_forward_w8a8_blocks")
+
+
+def _arg(t, name: str, dtype, n: int, optional: bool = False):
+    """Device pointer of a contiguous tensor of n elements of `dtype`."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if not t.is_cuda:
+        raise ValueError("libmoe takes device tensors only")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _row_dtype(shape: moe_shape):
+    return torch.bfloat16 if shape.dtype == MOE_BF16 else torch.float32
+
+
+def _seqs(seq_offsets):
+    """(pointer, number of sequences) of seq_offsets, an int32 [n_seq + 1] tensor or None."""
+    if seq_offsets is None:
+        return None, 1
+    n = seq_offsets.numel()
+    return _arg(seq_offsets, "seq_offsets", torch.int32, n), n - 1
+
+
+def _rng(rng):
+    """rng {seed, offset}: an int64 (or uint64) device tensor; None where nothing is drawn."""
+    if rng is None:
+        return None
+    return _arg(rng, "rng", torch.uint64 if rng.dtype == torch.uint64 else torch.int64, 2)
+
+
+def moe_balance_workspace_bytes(shape: moe_shape, n_seq: int = 1) -> int:
+    return int(_lib.moe_balance_workspace_bytes(ctypes.byref(shape), n_seq))
+
+
+def alloc_balance_workspace(shape: moe_shape, n_seq: int = 1, device=None) -> torch.Tensor:
+    n = moe_balance_workspace_bytes(shape, n_seq)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_balance_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def moe_balance_loss(shape, logits, topk_idx, token_mask, seq_offsets, alpha, counts, mean_probs,
+                     loss, workspace, stream=None):
+    """Balance loss [1] (fp32), per-expert counts [n_seq][E] (int32) and mean
+    probabilities [n_seq][E] (fp32) of the router's logits [T][E] and picks [T][K]."""
+    T, E, K = shape.T, shape.E, shape.K
+    seqs, n = _seqs(seq_offsets)
+    ws, nws = _ws(workspace)
+    _check(_lib.moe_balance_loss(
+        ctypes.byref(shape), _arg(logits, "logits", torch.float32, T * E),
+        _arg(topk_idx, "topk_idx", torch.int32, T * K),
+        _arg(token_mask, "token_mask", torch.uint8, T, True), seqs, n, alpha,
+        _arg(counts, "counts", torch.int32, n * E),
+        _arg(mean_probs, "mean_probs", torch.float32, n * E),
+        _arg(loss, "loss", torch.float32, 1), ws, nws, _stream(stream)), "moe_balance_loss")
+
+
+def moe_route_backward(shape, logits, topk_idx, d_topk_w, token_mask, seq_offsets, alpha, counts,
+                       d_loss, d_logits, stream=None):
+    """Gradient of the logits: the routing weights' (d_topk_w, or None) and the
+    balance loss's (counts as moe_balance_loss wrote them, or None) together."""
+    T, E, K = shape.T, shape.E, shape.K
+    seqs, n = _seqs(seq_offsets)
+    _check(_lib.moe_route_backward(
+        ctypes.byref(shape), _arg(logits, "logits", torch.float32, T * E),
+        _arg(topk_idx, "topk_idx", torch.int32, T * K, True),
+        _arg(d_topk_w, "d_topk_w", torch.float32, T * K, True),
+        _arg(token_mask, "token_mask", torch.uint8, T, True), seqs, n, alpha,
+        _arg(counts, "counts", torch.int32, n * E, True),
+        _arg(d_loss, "d_loss", torch.float32, 1, True),
+        _arg(d_logits, "d_logits", torch.float32, T * E), _stream(stream)), "moe_route_backward")
+
+
+def moe_dropout(x, residual, p, rng, y, stream=None):
+    """y = residual + dropout(x), x of any shape (bf16 or fp32); rng an int64
+    device tensor {seed, offset}.  The same call on the output's gradient, with
+    the same rng and no residual, gives x's gradient."""
+    dtype = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}[x.dtype]
+    n = x.numel()
+    _check(_lib.moe_dropout(n, dtype, _arg(x, "x", x.dtype, n),
+                            _arg(residual, "residual", x.dtype, n, True), p, _rng(rng),
+                            _arg(y, "y", x.dtype, n), _stream(stream)), "moe_dropout")
+
+
+def moe_combine_dropout(shape, y_perm, inv_perm, topk_w, y_shared, residual, p, rng, y,
+                        stream=None):
+    """moe_combine with dropout on its sum and the residual added."""
+    dt, n, row = _row_dtype(shape), shape.T * shape.K, shape.T * shape.d
+    _check(_lib.moe_combine_dropout(
+        ctypes.byref(shape), _arg(y_perm, "y_perm", dt, n * shape.d),
+        _arg(inv_perm, "inv_perm", torch.int32, n), _arg(topk_w, "topk_w", torch.float32, n),
+        _arg(y_shared, "y_shared", dt, row, True), _arg(residual, "residual", dt, row, True), p,
+        _rng(rng), _arg(y, "y", dt, row), _stream(stream)), "moe_combine_dropout")
+
+
+def moe_combine_backward(shape, d_y, y_perm, inv_perm, topk_w, p, rng, d_y_perm, d_topk_w,
+                         d_shared, stream=None):
+    """Gradients of moe_combine_dropout from d_y: of the expert rows (d_y_perm), the
+    routing weights (d_topk_w, fp32) and the shared expert's rows (d_shared), each or None."""
+    dt, n, row = _row_dtype(shape), shape.T * shape.K, shape.T * shape.d
+    _check(_lib.moe_combine_backward(
+        ctypes.byref(shape), _arg(d_y, "d_y", dt, row),
+        _arg(y_perm, "y_perm", dt, n * shape.d, True), _arg(inv_perm, "inv_perm", torch.int32, n),
+        _arg(topk_w, "topk_w", torch.float32, n, True), p, _rng(rng),
+        _arg(d_y_perm, "d_y_perm", dt, n * shape.d, True),
+        _arg(d_topk_w, "d_topk_w", torch.float32, n, True),
+        _arg(d_shared, "d_shared", dt, row, True), _stream(stream)), "moe_combine_backward")
 
 
 def moe_get_device_error(workspace) -> int:

@@ -232,6 +232,32 @@ cudaError_t launch_quantize_rows_known_amax(int64_t rows, int cols, const void* 
 cudaError_t launch_combine(const moe_shape& s, const void* y_perm, const int32_t* inv_perm,
                            const float* topk_w, const void* y_shared, void* y, cudaStream_t st);
 
+// ---- dropout.cu ----
+cudaError_t launch_dropout(int64_t n, int dtype, const void* x, const void* residual, double p,
+                           const uint64_t* rng, void* y, cudaStream_t st);
+cudaError_t launch_combine_dropout(const moe_shape& s, const void* y_perm, const int32_t* inv_perm,
+                                   const float* topk_w, const void* y_shared, const void* residual,
+                                   double p, const uint64_t* rng, void* y, cudaStream_t st);
+cudaError_t launch_combine_backward(const moe_shape& s, const void* d_y, const void* y_perm,
+                                    const int32_t* inv_perm, const float* topk_w, double p,
+                                    const uint64_t* rng, void* d_y_perm, float* d_topk_w,
+                                    void* d_shared, cudaStream_t st);
+
+// ---- balance.cu ----
+// rows of partial sums (of E values) that the loss of n_seq sequences needs
+int64_t balance_partials(const moe_shape& s, int n_seq);
+// cu: [n_seq + 1] first token of each sequence, or NULL (n_seq = 1, all tokens);
+// ticket: a zeroed counter
+cudaError_t launch_balance_loss(const moe_shape& s, const float* logits, const int32_t* topk_idx,
+                                const uint8_t* mask, const int32_t* cu, int n_seq, float alpha,
+                                int32_t* counts, float* mean_p, float* loss, float* part_p,
+                                int32_t* part_c, double* seq_loss, unsigned int* ticket,
+                                DevError* err, cudaStream_t st);
+cudaError_t launch_route_backward(const moe_shape& s, const float* logits, const int32_t* topk_idx,
+                                  const float* d_topk_w, const uint8_t* mask, const int32_t* cu,
+                                  int n_seq, float alpha, const int32_t* counts,
+                                  const float* d_loss, float* d_logits, cudaStream_t st);
+
 int device_sm_count();
 
 // Launches with programmatic stream serialisation (MOE_PDL=0 turns it off, read
