@@ -396,8 +396,9 @@ moe_status moe_forward_w8a8_blocks(const moe_shape *shape, const void *x, const 
  *
  * `logits` [T][E] (fp32) are the scores whose softmax or sigmoid the router
  * takes: s for MOE_ROUTER_SIGMOID, s + b for MOE_ROUTER_SOFTMAX (what
- * moe_route's logits_out gives for that router).  They are finite, or -inf for
- * an expert a token may not take (its probability and gradient are 0).
+ * moe_route's logits_out gives for that router).  They are finite (below 1e38
+ * in magnitude), or -inf for an expert that a token may not take (its
+ * probability and gradient are 0).
  *
  * token_mask [T] (bytes, may be NULL): a token with a 0 takes no part -- it is
  * not counted, and its row of d_logits is 0; its logits are not used.
@@ -446,7 +447,7 @@ moe_status moe_balance_loss(const moe_shape *shape, const float *logits,
  *      softmax: w_k (dw_k - sum_j w_j dw_j)
  *      sigmoid: a_k (1 - a_k) (dw_k - sum_j w_j dw_j) / (sum_j a_j + 1e-6)
  * One of counts and d_topk_w must be given.  d_logits [T][E] (fp32) is written
- * whole.  An expert id outside [0, E) adds nothing.
+ * whole; it may not overlap logits.  An expert id outside [0, E) adds nothing.
  */
 moe_status moe_route_backward(const moe_shape *shape, const float *logits,
                               const int32_t *topk_idx, const float *d_topk_w,

@@ -133,9 +133,15 @@ def _p(t):
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object (2.9 us -> 0.3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -299,15 +305,15 @@ def _arg(t, name: str, dtype, n: int, optional: bool = False):
         if optional:
             return None
         raise ValueError(f"{name} is missing")
+    if t.is_cuda and t.dtype == dtype and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError("libmoe takes device tensors only")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _row_dtype(shape: moe_shape):

@@ -244,19 +244,43 @@ cudaError_t launch_combine_backward(const moe_shape& s, const void* d_y, const v
                                     void* d_shared, cudaStream_t st);
 
 // ---- balance.cu ----
-// rows of partial sums (of E values) that the loss of n_seq sequences needs
-int64_t balance_partials(const moe_shape& s, int n_seq);
-// cu: [n_seq + 1] first token of each sequence, or NULL (n_seq = 1, all tokens);
-// ticket: a zeroed counter
-cudaError_t launch_balance_loss(const moe_shape& s, const float* logits, const int32_t* topk_idx,
-                                const uint8_t* mask, const int32_t* cu, int n_seq, float alpha,
-                                int32_t* counts, float* mean_p, float* loss, float* part_p,
-                                int32_t* part_c, double* seq_loss, unsigned int* ticket,
-                                DevError* err, cudaStream_t st);
-cudaError_t launch_route_backward(const moe_shape& s, const float* logits, const int32_t* topk_idx,
-                                  const float* d_topk_w, const uint8_t* mask, const int32_t* cu,
-                                  int n_seq, float alpha, const int32_t* counts,
-                                  const float* d_loss, float* d_logits, cudaStream_t st);
+struct BalanceArgs {
+    const float* logits;
+    const int32_t* topk_idx;
+    const uint8_t* mask;  // [T] or NULL
+    const int32_t* cu;    // [n_seq + 1] first token of each sequence, or NULL (n_seq = 1)
+    int n_seq;
+    float alpha;
+    int32_t* counts;      // [n_seq][E]
+    float* mean_p;        // [n_seq][E]
+    float* loss;          // [1]
+    // scratch: one partial row per (block, sequence) pair, balance_blocks + n_seq at most
+    float* part_p;        // [rows][E]
+    int32_t* part_c;      // [rows][E]
+    int32_t* part_n;      // [rows]
+    int32_t* part_bad;    // [balance_blocks]
+    float* shares;        // [n_seq * balance_slices]
+    unsigned int* ticket;
+    DevError* err;
+    int T, E, K, chunk, blocks;  // set by the launch
+};
+int64_t balance_blocks(const moe_shape& s);          // blocks of tokens
+int balance_slices(const moe_shape& s, int n_seq);   // blocks of columns a sequence
+cudaError_t launch_balance_loss(const moe_shape& s, BalanceArgs a, cudaStream_t st);
+struct RouteBackwardArgs {
+    const float* logits;
+    const int32_t* topk_idx;
+    const float* d_topk_w;  // [T][K] or NULL
+    const uint8_t* mask;    // [T] or NULL
+    const int32_t* cu;      // as in BalanceArgs
+    int n_seq;
+    float alpha;
+    const int32_t* counts;  // [n_seq][E] or NULL
+    const float* d_loss;    // [1] or NULL (1)
+    float* d_logits;        // [T][E]
+    int T, E, K, pw_log, chunk;  // set by the launch
+};
+cudaError_t launch_route_backward(const moe_shape& s, RouteBackwardArgs a, cudaStream_t st);
 
 int device_sm_count();
 

@@ -21,21 +21,24 @@ bool good(const void* p, uintptr_t to) { return p && aligned(p, to); }
 bool good_or_null(const void* p, uintptr_t to) { return aligned(p, to); }
 
 // Error block (the record at its start, the ticket of the last block at
-// kTicket), then one loss per sequence, the partial sums and partial counts.
+// kTicket), then the shares of the loss and the partial rows.
 constexpr size_t kErrBytes = 256, kTicket = 128;
 
 struct BalanceWs {
-    size_t seq_loss, part_p, part_c, total;
+    size_t shares, part_n, part_bad, part_p, part_c, total;
 };
 
 BalanceWs balance_ws(const moe_shape& s, int32_t n_seq) {
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    const size_t rows = (size_t)balance_partials(s, n_seq) * (size_t)s.E;
+    const size_t blocks = (size_t)balance_blocks(s), rows = blocks + (size_t)n_seq;
+    const size_t shares = (size_t)n_seq * (size_t)balance_slices(s, n_seq);
     BalanceWs w;
-    w.seq_loss = kErrBytes;
-    w.part_p = up(w.seq_loss + sizeof(double) * (size_t)n_seq);
-    w.part_c = up(w.part_p + sizeof(float) * rows);
-    w.total = up(w.part_c + sizeof(int32_t) * rows);
+    w.shares = kErrBytes;
+    w.part_n = up(w.shares + sizeof(float) * shares);
+    w.part_bad = up(w.part_n + sizeof(int32_t) * rows);
+    w.part_p = up(w.part_bad + sizeof(int32_t) * blocks);
+    w.part_c = up(w.part_p + sizeof(float) * rows * (size_t)s.E);
+    w.total = up(w.part_c + sizeof(int32_t) * rows * (size_t)s.E);
     return w;
 }
 
@@ -77,20 +80,32 @@ moe_status moe_balance_loss(const moe_shape* shape, const float* logits, const i
     if (ws_bytes < w.total) return MOE_ERR_WORKSPACE;
     cudaStream_t cs = (cudaStream_t)stream;
     uint8_t* base = static_cast<uint8_t*>(workspace);
-    cudaError_t e = cudaMemsetAsync(base, 0, kErrBytes, cs);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (s.T == 0) {
         const size_t n = sizeof(float) * (size_t)n_seq * (size_t)s.E;
-        e = cudaMemsetAsync(counts, 0, n, cs);
+        cudaError_t e = cudaMemsetAsync(base, 0, kErrBytes, cs);
+        if (e == cudaSuccess) e = cudaMemsetAsync(counts, 0, n, cs);
         if (e == cudaSuccess) e = cudaMemsetAsync(mean_probs, 0, n, cs);
         if (e == cudaSuccess) e = cudaMemsetAsync(loss, 0, sizeof(float), cs);
         return cuda_status(e);
     }
-    return cuda_status(launch_balance_loss(
-        s, logits, topk_idx, token_mask, seq_offsets, n_seq, alpha, counts, mean_probs, loss,
-        reinterpret_cast<float*>(base + w.part_p), reinterpret_cast<int32_t*>(base + w.part_c),
-        reinterpret_cast<double*>(base + w.seq_loss), reinterpret_cast<unsigned int*>(base + kTicket),
-        reinterpret_cast<DevError*>(base), cs));
+    BalanceArgs a{};
+    a.logits = logits;
+    a.topk_idx = topk_idx;
+    a.mask = token_mask;
+    a.cu = seq_offsets;
+    a.n_seq = n_seq;
+    a.alpha = alpha;
+    a.counts = counts;
+    a.mean_p = mean_probs;
+    a.loss = loss;
+    a.part_p = reinterpret_cast<float*>(base + w.part_p);
+    a.part_c = reinterpret_cast<int32_t*>(base + w.part_c);
+    a.part_n = reinterpret_cast<int32_t*>(base + w.part_n);
+    a.part_bad = reinterpret_cast<int32_t*>(base + w.part_bad);
+    a.shares = reinterpret_cast<float*>(base + w.shares);
+    a.ticket = reinterpret_cast<unsigned int*>(base + kTicket);
+    a.err = reinterpret_cast<DevError*>(base);
+    return cuda_status(launch_balance_loss(s, a, cs));
 }
 
 moe_status moe_route_backward(const moe_shape* shape, const float* logits, const int32_t* topk_idx,
@@ -108,9 +123,18 @@ moe_status moe_route_backward(const moe_shape* shape, const float* logits, const
     if (!good_or_null(counts, 4) || !good_or_null(d_topk_w, 4) || !good_or_null(d_loss, 4))
         return MOE_ERR_INVALID_ARG;
     if (d_topk_w ? !good(topk_idx, 4) : !good_or_null(topk_idx, 4)) return MOE_ERR_INVALID_ARG;
-    return cuda_status(launch_route_backward(s, logits, topk_idx, d_topk_w, token_mask, seq_offsets,
-                                             n_seq, alpha, counts, d_loss, d_logits,
-                                             (cudaStream_t)stream));
+    RouteBackwardArgs a{};
+    a.logits = logits;
+    a.topk_idx = topk_idx;
+    a.d_topk_w = d_topk_w;
+    a.mask = token_mask;
+    a.cu = seq_offsets;
+    a.n_seq = n_seq;
+    a.alpha = alpha;
+    a.counts = counts;
+    a.d_loss = d_loss;
+    a.d_logits = d_logits;
+    return cuda_status(launch_route_backward(s, a, (cudaStream_t)stream));
 }
 
 moe_status moe_dropout(int64_t n, int32_t dtype, const void* x, const void* residual, double p,
