@@ -17,6 +17,10 @@
 #include "internal.h"
 #include "philox.cuh"
 
+#ifndef CV
+#define CV 2
+#define CK 2
+#endif
 namespace moe {
 
 namespace {
@@ -33,10 +37,13 @@ dropout_kernel(const T* x, const T* residual, T* y, int64_t n, DropRule rule,
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
     for (int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g < groups; g += stride) {
         float f[8];
-        widen(load_unit(x + g * 8), f);
+        const Unit<T> v = load_unit(x + g * 8);
         Unit<T> r;
         if (residual) r = load_unit(residual + g * 8);
-        if (rule.thr) drop8(f, (uint64_t)g, st, rule);
+        Bits8 bits = {};
+        if (rule.thr) bits = draw8((uint64_t)g, st);
+        widen(v, f);
+        if (rule.thr) drop8(f, bits, rule);
         if (residual) {
             float rf[8];
             widen(r, rf);
@@ -53,7 +60,7 @@ dropout_kernel(const T* x, const T* residual, T* y, int64_t n, DropRule rule,
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if (k < m) f[k] = Elem<T>::to_f32(x[base + k]);
-        if (rule.thr) drop8(f, (uint64_t)groups, st, rule);
+        if (rule.thr) drop8(f, draw8((uint64_t)groups, st), rule);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             if (k >= m) continue;
@@ -63,95 +70,190 @@ dropout_kernel(const T* x, const T* residual, T* y, int64_t n, DropRule rule,
     }
 }
 
-// A thread owns one group of eight elements of an output row.
-template <typename T>
-__global__ void __launch_bounds__(256)
+// The routed rows of one token, as its warps see them (blockDim.x threads along
+// the row, blockDim.y tokens a block, whole warps on one token): lane j holds
+// slot j's row (-1: dropped) and weight.
+struct Slots {
+    int32_t p;
+    float w;
+};
+__device__ __forceinline__ Slots load_slots(const int32_t* __restrict__ inv_perm,
+                                            const float* __restrict__ topk_w, int64_t t, int K,
+                                            int64_t n_rows, bool on) {
+    const int lane = threadIdx.x & 31;
+    Slots s{-1, 0.f};
+    if (on && lane < K) {
+        s.p = __ldg(inv_perm + t * K + lane);
+        if (s.p >= n_rows) s.p = -1;
+        if (topk_w) s.w = __ldg(topk_w + t * K + lane);
+    }
+    return s;
+}
+
+// KB rows from slot j0 on, V groups of eight elements a thread; zeros for slots
+// that are dropped or beyond K
+template <typename T, int V, int KB>
+__device__ __forceinline__ void load_rows(Unit<T> (&row)[KB][V], const T* y_perm, const Slots& s,
+                                          int j0, int K, int d) {
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+        const int32_t p = __shfl_sync(0xffffffffu, s.p, (j0 + j) & 31);
+        const bool any = j0 + j < K && p >= 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int u = threadIdx.x + i * blockDim.x;
+            row[j][i] = Unit<T>{};
+            if (any && u < d / 8) row[j][i] = load_unit(y_perm + (int64_t)p * d + (int64_t)u * 8);
+        }
+    }
+}
+
+// A thread sums V groups of eight elements of an output row, KB slots at a time:
+// the loads of a step are all asked for before the first is used, and the mask
+// is drawn while the first step's are on their way.
+template <typename T, int V, int KB>
+__global__ void __launch_bounds__(1024)
 combine_dropout_kernel(const T* y_perm, const int32_t* __restrict__ inv_perm,
                        const float* __restrict__ topk_w, const T* y_shared, const T* residual,
-                       T* y, int d, int K, int64_t n_rows, DropRule rule,
+                       T* y, int n_tokens, int d, int K, int64_t n_rows, DropRule rule,
                        const uint64_t* __restrict__ rng) {
     pdl_wait();
     pdl_trigger();
     const int units = d / 8;
-    const int64_t t = blockIdx.x;
-    const int u = blockIdx.y * blockDim.x + threadIdx.x;
-    if (u >= units) return;
-    const int64_t at = t * d + (int64_t)u * 8;
-    float acc[8] = {};
-    if (y_shared) widen(load_unit(y_shared + at), acc);
-    for (int j = 0; j < K; ++j) {
-        const int32_t p = inv_perm[t * K + j];
-        if (p < 0 || p >= n_rows) continue;  // dropped slot
-        const float w = topk_w[t * K + j];
-        float f[8];
-        widen(load_unit(y_perm + (int64_t)p * d + (int64_t)u * 8), f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, f[k], acc[k]);
-    }
-    if (rule.thr) drop8(acc, (uint64_t)(at / 8), load_rng(rng), rule);
-    if (residual) {
-        float f[8];
-        widen(load_unit(residual + at), f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] += f[k];
-    }
-    store_unit(y + at, acc);
-}
-
-// One token per block: its threads hold dz in registers (V groups of eight
-// elements each) and walk the token's K rows; the K dot products are summed in
-// a fixed order (lanes, then warps).
-template <typename T, int V>
-__global__ void __launch_bounds__(512)
-combine_backward_kernel(const T* d_y, const T* y_perm, const int32_t* __restrict__ inv_perm,
-                        const float* __restrict__ topk_w, T* d_y_perm, float* d_topk_w, T* d_shared,
-                        int d, int K, int64_t n_rows, DropRule rule,
-                        const uint64_t* __restrict__ rng) {
-    __shared__ float red[16][32];  // [warp][slot]
-    pdl_wait();
-    pdl_trigger();
-    const int units = d / 8;
-    const int64_t t = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-    float dz[V][8];
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool on = t < n_tokens;
+    const Slots slots = load_slots(inv_perm, topk_w, t, K, n_rows, on);
+    Unit<T> sh[V], res[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int u = threadIdx.x + i * blockDim.x;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) dz[i][k] = 0.f;
-        if (u < units) widen(load_unit(d_y + t * d + (int64_t)u * 8), dz[i]);
+        const int64_t at = t * d + (int64_t)u * 8;
+        sh[i] = Unit<T>{};
+        if (y_shared && on && u < units) sh[i] = load_unit(y_shared + at);
     }
+    Unit<T> row[KB][V];
+    load_rows(row, y_perm, slots, 0, K, d);
+    Bits8 bits[V] = {};
     if (rule.thr) {
         const RngState st = load_rng(rng);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            drop8(dz[i], (uint64_t)(t * units + threadIdx.x + i * blockDim.x), st, rule);
+            bits[i] = draw8((uint64_t)(t * units + threadIdx.x + i * blockDim.x), st);
     }
-    if (d_shared) {
+    float acc[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) widen(sh[i], acc[i]);
+    for (int j0 = 0;;) {
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            const float w = __shfl_sync(0xffffffffu, slots.w, (j0 + j) & 31);
+            const bool any =
+                __shfl_sync(0xffffffffu, slots.p, (j0 + j) & 31) >= 0 && j0 + j < K;
+            if (!any) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float f[8];
+                widen(row[j][i], f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[i][k] = fmaf(w, f[k], acc[i][k]);
+            }
+        }
+        j0 += KB;
+        if (j0 >= K) break;
+        load_rows(row, y_perm, slots, j0, K, d);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int u = threadIdx.x + i * blockDim.x;
+        if (!on || u >= units) continue;
+        const int64_t at = t * d + (int64_t)u * 8;
+        if (residual) res[i] = load_unit(residual + at);
+        if (rule.thr) drop8(acc[i], bits[i], rule);
+        if (residual) {
+            float f[8];
+            widen(res[i], f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[i][k] += f[k];
+        }
+        store_unit(y + at, acc[i]);
+    }
+}
+
+// A token's threads (blockDim.x, blockDim.y tokens a block) hold dz in
+// registers, V groups of eight elements each, and walk the token's K rows, the
+// next row on its way while one is worked on.  The K dot products are summed in
+// a fixed order: a thread's elements, lanes, warps.
+template <typename T, int V, int KB>
+__global__ void __launch_bounds__(1024)
+combine_backward_kernel(const T* d_y, const T* y_perm, const int32_t* __restrict__ inv_perm,
+                        const float* __restrict__ topk_w, T* d_y_perm, float* d_topk_w, T* d_shared,
+                        int n_tokens, int d, int K, int64_t n_rows, DropRule rule,
+                        const uint64_t* __restrict__ rng) {
+    __shared__ float red[32][32];  // [warp of the block][slot]
+    pdl_wait();
+    pdl_trigger();
+    const int units = d / 8;
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
+    const int warp = threadIdx.y * nwarps + (threadIdx.x >> 5);
+    const bool on = t < n_tokens;
+    const Slots slots = load_slots(inv_perm, d_y_perm ? topk_w : nullptr, t, K, n_rows, on);
+    Unit<T> raw[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int u = threadIdx.x + i * blockDim.x;
+        raw[i] = Unit<T>{};
+        if (on && u < units) raw[i] = load_unit(d_y + t * d + (int64_t)u * 8);
+    }
+    Unit<T> row[KB][V];
+    if (d_topk_w) load_rows(row, y_perm, slots, 0, K, d);
+    float dz[V][8];
+    RngState st = {};
+    if (rule.thr) st = load_rng(rng);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        Bits8 bits = {};
+        if (rule.thr) bits = draw8((uint64_t)(t * units + threadIdx.x + i * blockDim.x), st);
+        widen(raw[i], dz[i]);
+        if (rule.thr) drop8(dz[i], bits, rule);
+    }
+    if (d_shared && on) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int u = threadIdx.x + i * blockDim.x;
             if (u < units) store_unit(d_shared + t * d + (int64_t)u * 8, dz[i]);
         }
     }
-    for (int j = 0; j < K; ++j) {
-        const int32_t p = inv_perm[t * K + j];
-        float dot = 0.f;
-        if (p >= 0 && p < n_rows) {
-            const int64_t row = (int64_t)p * d;
-            if (d_topk_w) {
+    for (int j0 = 0; j0 < K; j0 += KB) {
+        if (d_topk_w) {
+            float dot[KB];
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                dot[j] = 0.f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const int u = threadIdx.x + i * blockDim.x;
-                    if (u >= units) continue;
                     float f[8];
-                    widen(load_unit(y_perm + row + (int64_t)u * 8), f);
+                    widen(row[j][i], f);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) dot = fmaf(dz[i][k], f[k], dot);
+                    for (int k = 0; k < 8; ++k) dot[j] = fmaf(dz[i][k], f[k], dot[j]);
                 }
             }
-            if (d_y_perm) {
-                const float w = topk_w[t * K + j];
+            if (j0 + KB < K) load_rows(row, y_perm, slots, j0 + KB, K, d);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int j = 0; j < KB; ++j) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+                if (lane == 0 && j0 + j < K) red[warp][j0 + j] = dot[j];
+        }
+        if (d_y_perm) {
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                if (j0 + j >= K) break;
+                const int32_t p = __shfl_sync(0xffffffffu, slots.p, j0 + j);
+                const float w = __shfl_sync(0xffffffffu, slots.w, j0 + j);
+                if (p < 0) continue;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int u = threadIdx.x + i * blockDim.x;
@@ -159,17 +261,15 @@ combine_backward_kernel(const T* d_y, const T* y_perm, const int32_t* __restrict
                     float f[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) f[k] = w * dz[i][k];
-                    store_unit(d_y_perm + row + (int64_t)u * 8, f);
+                    store_unit(d_y_perm + (int64_t)p * d + (int64_t)u * 8, f);
                 }
             }
         }
-        dot = warp_sum(dot);
-        if (lane == 0) red[warp][j] = dot;
     }
     __syncthreads();
-    if (d_topk_w && threadIdx.x < K) {
+    if (d_topk_w && on && threadIdx.x < K) {
         float s = 0.f;
-        for (int w = 0; w < nwarps; ++w) s += red[w][threadIdx.x];
+        for (int w = 0; w < nwarps; ++w) s += red[threadIdx.y * nwarps + w][threadIdx.x];
         d_topk_w[t * K + threadIdx.x] = s;
     }
 }
@@ -183,33 +283,47 @@ cudaError_t dropout_t(int64_t n, const void* x, const void* residual, DropRule r
                       0, st, (const T*)x, (const T*)residual, (T*)y, n, rule, rng);
 }
 
-template <typename T>
-cudaError_t combine_dropout_t(const moe_shape& s, const void* y_perm, const int32_t* inv_perm,
-                              const float* topk_w, const void* y_shared, const void* residual,
-                              DropRule rule, const uint64_t* rng, void* y, cudaStream_t st) {
-    const dim3 grid((unsigned)s.T, (unsigned)ceil_div(s.d / 8, 256));
-    return launch_pdl(combine_dropout_kernel<T>, grid, dim3(256), 0, st, (const T*)y_perm, inv_perm,
-                      topk_w, (const T*)y_shared, (const T*)residual, (T*)y, s.d, s.K,
-                      (int64_t)s.T * s.K, rule, rng);
+// Threads along a row of d / 8 groups, V a thread, and tokens side by side: whole
+// warps, blocks of about 256 threads or one row.
+template <int V>
+dim3 row_block(int d) {
+    const int x = (int)ceil_div(d / 8, V * 32) * 32;
+    return dim3((unsigned)x, (unsigned)(256 / x > 0 ? 256 / x : 1));
 }
 
-template <typename T, int V>
+template <typename T, int V, int KB>
+cudaError_t combine_dropout_v(const moe_shape& s, const void* y_perm, const int32_t* inv_perm,
+                              const float* topk_w, const void* y_shared, const void* residual,
+                              DropRule rule, const uint64_t* rng, void* y, cudaStream_t st) {
+    const dim3 block = row_block<V>(s.d);
+    return launch_pdl(combine_dropout_kernel<T, V, KB>, dim3((unsigned)ceil_div(s.T, block.y)), block,
+                      0, st, (const T*)y_perm, inv_perm, topk_w, (const T*)y_shared,
+                      (const T*)residual, (T*)y, s.T, s.d, s.K, (int64_t)s.T * s.K, rule, rng);
+}
+
+template <typename T, typename... Args>
+cudaError_t combine_dropout_t(const moe_shape& s, Args... args) {
+    if (s.d / 8 > 32) return combine_dropout_v<T, CV, CK>(s, args...);
+    return combine_dropout_v<T, 1, CK>(s, args...);
+}
+
+template <typename T, int V, int KB>
 cudaError_t combine_backward_v(const moe_shape& s, const void* d_y, const void* y_perm,
                                const int32_t* inv_perm, const float* topk_w, DropRule rule,
                                const uint64_t* rng, void* d_y_perm, float* d_topk_w, void* d_shared,
                                cudaStream_t st) {
-    const int threads = (int)ceil_div(ceil_div(s.d / 8, V), 32) * 32;
-    return launch_pdl(combine_backward_kernel<T, V>, dim3((unsigned)s.T), dim3((unsigned)threads), 0,
-                      st, (const T*)d_y, (const T*)y_perm, inv_perm, topk_w, (T*)d_y_perm, d_topk_w,
-                      (T*)d_shared, s.d, s.K, (int64_t)s.T * s.K, rule, rng);
+    const dim3 block = row_block<V>(s.d);
+    return launch_pdl(combine_backward_kernel<T, V, KB>, dim3((unsigned)ceil_div(s.T, block.y)), block,
+                      0, st, (const T*)d_y, (const T*)y_perm, inv_perm, topk_w, (T*)d_y_perm,
+                      d_topk_w, (T*)d_shared, s.T, s.d, s.K, (int64_t)s.T * s.K, rule, rng);
 }
 
 template <typename T, typename... Args>
 cudaError_t combine_backward_t(const moe_shape& s, Args... args) {
-    const int units = s.d / 8;
-    if (units > 512) return combine_backward_v<T, 4>(s, args...);
-    if (units > 256) return combine_backward_v<T, 2>(s, args...);
-    return combine_backward_v<T, 1>(s, args...);
+    if (s.d / 8 <= 32) return combine_backward_v<T, 1, 1>(s, args...);
+    if constexpr (sizeof(T) == 2)
+        if (s.K > 2) return combine_backward_v<T, 2, 2>(s, args...);
+    return combine_backward_v<T, 2, 1>(s, args...);
 }
 
 }  // namespace
