@@ -845,13 +845,19 @@ int balance_chunk(const moe_shape& s) {
 
 int64_t balance_blocks(const moe_shape& s) { return ceil_div(s.T, balance_chunk(s)); }
 
-// Dynamic shared memory above the default limit.  The limit asked for is the
-// same for every call, so calls of several threads do not undo each other's.
+// Launches `kernel` with dynamic shared memory that may pass the default limit.
+// The limit asked for is the same for every call, so calls of several threads do
+// not undo each other's.
 constexpr int kMaxSmem = 108 * 1024;
-template <typename F>
-cudaError_t allow_smem(F kernel, size_t bytes) {
-    if (bytes <= 48 * 1024) return cudaSuccess;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+template <typename Args>
+cudaError_t launch_wide(void (*kernel)(Args), unsigned blocks, size_t smem, cudaStream_t st,
+                        const Args& args) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, st, args);
 }
 
 // slices of 32 columns, side by side while the sequences alone leave SMs idle
@@ -871,11 +877,9 @@ cudaError_t launch_balance_loss(const moe_shape& s, BalanceArgs a, cudaStream_t 
         using L = decltype(layout);
         const size_t smem = sizeof(float) * (size_t)s.E *
                             (kWarps * kStages * L::kTokens + kWarps + 1);
-        auto k = s.router == MOE_ROUTER_SIGMOID ? balance_partial_kernel<L, true>
-                                                : balance_partial_kernel<L, false>;
-        const cudaError_t err = allow_smem(k, smem);
-        if (err != cudaSuccess) return err;
-        return launch_pdl(k, dim3((unsigned)a.blocks), dim3(kThreads), smem, st, a);
+        return launch_wide(s.router == MOE_ROUTER_SIGMOID ? balance_partial_kernel<L, true>
+                                                          : balance_partial_kernel<L, false>,
+                           (unsigned)a.blocks, smem, st, a);
     });
     if (e != cudaSuccess) return e;
     // a block per sequence and slice of columns, a warp for every four of the
@@ -899,11 +903,9 @@ cudaError_t launch_route_backward(const moe_shape& s, RouteBackwardArgs a, cudaS
         a.chunk = (int)(ceil_div(ceil_div(s.T, wave(s) * kWarps), L::kRows) * L::kRows);
         const unsigned blocks = (unsigned)ceil_div(s.T, (int64_t)a.chunk * kWarps);
         const size_t smem = sizeof(float) * (size_t)s.E * (kWarps * (kStages * L::kTokens + 1));
-        auto k = s.router == MOE_ROUTER_SIGMOID ? route_backward_kernel<L, true>
-                                                : route_backward_kernel<L, false>;
-        const cudaError_t err = allow_smem(k, smem);
-        if (err != cudaSuccess) return err;
-        return launch_pdl(k, dim3(blocks), dim3(kThreads), smem, st, a);
+        return launch_wide(s.router == MOE_ROUTER_SIGMOID ? route_backward_kernel<L, true>
+                                                          : route_backward_kernel<L, false>,
+                           blocks, smem, st, a);
     });
 }
 

@@ -12,19 +12,18 @@
 // nothing is stored between the two.
 //
 // All three are bound by HBM: every row is read once and written once, in
-// 16-byte vectors, and the mask costs about 90 integer instructions per eight
-// elements.
+// 16-byte vectors.
 #include "internal.h"
 #include "philox.cuh"
 
-#ifndef CV
-#define CV 2
-#define CK 2
-#endif
 namespace moe {
 
 namespace {
 
+// A thread takes groups of eight elements, gridDim.x * 256 apart, and draws each
+// group's bits while its loads are on their way.  16384 x 7168 bf16 with residual
+// takes 108 us (704 MB, 6.5 TB/s); masks gathered into a byte before use took 156 us,
+// the integer work then bounding it.
 template <typename T>
 __global__ void __launch_bounds__(256)
 dropout_kernel(const T* x, const T* residual, T* y, int64_t n, DropRule rule,
@@ -70,9 +69,8 @@ dropout_kernel(const T* x, const T* residual, T* y, int64_t n, DropRule rule,
     }
 }
 
-// The routed rows of one token, as its warps see them (blockDim.x threads along
-// the row, blockDim.y tokens a block, whole warps on one token): lane j holds
-// slot j's row (-1: dropped) and weight.
+// The routed rows of one token, as each of its warps sees them (whole warps work
+// on one token): lane j holds slot j's row (-1: dropped) and weight.
 struct Slots {
     int32_t p;
     float w;
@@ -90,55 +88,62 @@ __device__ __forceinline__ Slots load_slots(const int32_t* __restrict__ inv_perm
     return s;
 }
 
-// KB rows from slot j0 on, V groups of eight elements a thread; zeros for slots
-// that are dropped or beyond K
+// KB rows from slot j0 on, V groups of eight elements a thread from group u0 on,
+// blockDim.x apart; zeros for slots that are dropped or beyond K
 template <typename T, int V, int KB>
 __device__ __forceinline__ void load_rows(Unit<T> (&row)[KB][V], const T* y_perm, const Slots& s,
-                                          int j0, int K, int d) {
+                                          int j0, int K, int d, int u0) {
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
         const int32_t p = __shfl_sync(0xffffffffu, s.p, (j0 + j) & 31);
         const bool any = j0 + j < K && p >= 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int u = threadIdx.x + i * blockDim.x;
+            const int u = u0 + i * blockDim.x;
             row[j][i] = Unit<T>{};
             if (any && u < d / 8) row[j][i] = load_unit(y_perm + (int64_t)p * d + (int64_t)u * 8);
         }
     }
 }
 
-// A thread sums V groups of eight elements of an output row, KB slots at a time:
-// the loads of a step are all asked for before the first is used, and the mask
-// is drawn while the first step's are on their way.
+// A warp sums V groups of eight elements a lane of one token's output row, KB
+// slots at a time, the next ones asked for as soon as those are used; the mask is
+// drawn while the first are on their way.  Bound by HBM.  Warps that depend on
+// nothing but themselves, two a block, keep the loads coming: T = 16384, d = 7168,
+// K = 8 bf16 with shared expert and residual takes 386 us (6.70 TB/s), blocks of 224
+// threads 418 us, four slots at a time 397 us, one group a lane 450 us.  A row of at
+// most 32 groups has one a lane, and there four slots at a time take 20 us against
+// 22 (T = 32768, d = 256, K = 4).
+// (The bound of 256 threads has the compiler spend few enough registers for 20
+// and more blocks of 64 an SM: with a bound of 64 the same call takes 400 us.)
 template <typename T, int V, int KB>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(256)
 combine_dropout_kernel(const T* y_perm, const int32_t* __restrict__ inv_perm,
                        const float* __restrict__ topk_w, const T* y_shared, const T* residual,
                        T* y, int n_tokens, int d, int K, int64_t n_rows, DropRule rule,
                        const uint64_t* __restrict__ rng) {
     pdl_wait();
     pdl_trigger();
-    const int units = d / 8;
+    const int units = d / 8, u0 = blockIdx.y * blockDim.x * V + threadIdx.x;
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool on = t < n_tokens;
     const Slots slots = load_slots(inv_perm, topk_w, t, K, n_rows, on);
-    Unit<T> sh[V], res[V];
+    Unit<T> sh[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int u = threadIdx.x + i * blockDim.x;
+        const int u = u0 + i * blockDim.x;
         const int64_t at = t * d + (int64_t)u * 8;
         sh[i] = Unit<T>{};
         if (y_shared && on && u < units) sh[i] = load_unit(y_shared + at);
     }
     Unit<T> row[KB][V];
-    load_rows(row, y_perm, slots, 0, K, d);
+    load_rows(row, y_perm, slots, 0, K, d, u0);
     Bits8 bits[V] = {};
     if (rule.thr) {
         const RngState st = load_rng(rng);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            bits[i] = draw8((uint64_t)(t * units + threadIdx.x + i * blockDim.x), st);
+            bits[i] = draw8((uint64_t)(t * units + u0 + i * blockDim.x), st);
     }
     float acc[V][8];
 #pragma unroll
@@ -160,18 +165,19 @@ combine_dropout_kernel(const T* y_perm, const int32_t* __restrict__ inv_perm,
         }
         j0 += KB;
         if (j0 >= K) break;
-        load_rows(row, y_perm, slots, j0, K, d);
+        load_rows(row, y_perm, slots, j0, K, d, u0);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int u = threadIdx.x + i * blockDim.x;
+        const int u = u0 + i * blockDim.x;
         if (!on || u >= units) continue;
         const int64_t at = t * d + (int64_t)u * 8;
-        if (residual) res[i] = load_unit(residual + at);
+        Unit<T> res;
+        if (residual) res = load_unit(residual + at);
         if (rule.thr) drop8(acc[i], bits[i], rule);
         if (residual) {
             float f[8];
-            widen(res[i], f);
+            widen(res, f);
 #pragma unroll
             for (int k = 0; k < 8; ++k) acc[i][k] += f[k];
         }
@@ -179,10 +185,13 @@ combine_dropout_kernel(const T* y_perm, const int32_t* __restrict__ inv_perm,
     }
 }
 
-// A token's threads (blockDim.x, blockDim.y tokens a block) hold dz in
-// registers, V groups of eight elements each, and walk the token's K rows, the
-// next row on its way while one is worked on.  The K dot products are summed in
-// a fixed order: a thread's elements, lanes, warps.
+// A token's threads (blockDim.x of them, blockDim.y tokens a block) hold dz in
+// registers, V groups of eight elements each, and walk the token's K rows, KB at a
+// time and the next ones on their way while the gradients of these are written.
+// The K dot products are summed in a fixed order: a thread's elements, lanes,
+// warps.  Bound by HBM: T = 16384, d = 7168, K = 8 bf16 takes 615 us for 4.23 GB
+// (6.88 TB/s, the measured copy's rate); four groups a thread without the
+// look-ahead took 774 us, one row at a time 698 us.
 template <typename T, int V, int KB>
 __global__ void __launch_bounds__(1024)
 combine_backward_kernel(const T* d_y, const T* y_perm, const int32_t* __restrict__ inv_perm,
@@ -206,7 +215,7 @@ combine_backward_kernel(const T* d_y, const T* y_perm, const int32_t* __restrict
         if (on && u < units) raw[i] = load_unit(d_y + t * d + (int64_t)u * 8);
     }
     Unit<T> row[KB][V];
-    if (d_topk_w) load_rows(row, y_perm, slots, 0, K, d);
+    if (d_topk_w) load_rows(row, y_perm, slots, 0, K, d, threadIdx.x);
     float dz[V][8];
     RngState st = {};
     if (rule.thr) st = load_rng(rng);
@@ -238,7 +247,7 @@ combine_backward_kernel(const T* d_y, const T* y_perm, const int32_t* __restrict
                     for (int k = 0; k < 8; ++k) dot[j] = fmaf(dz[i][k], f[k], dot[j]);
                 }
             }
-            if (j0 + KB < K) load_rows(row, y_perm, slots, j0 + KB, K, d);
+            if (j0 + KB < K) load_rows(row, y_perm, slots, j0 + KB, K, d, threadIdx.x);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -283,28 +292,21 @@ cudaError_t dropout_t(int64_t n, const void* x, const void* residual, DropRule r
                       0, st, (const T*)x, (const T*)residual, (T*)y, n, rule, rng);
 }
 
-// Threads along a row of d / 8 groups, V a thread, and tokens side by side: whole
-// warps, blocks of about 256 threads or one row.
-template <int V>
-dim3 row_block(int d) {
-    const int x = (int)ceil_div(d / 8, V * 32) * 32;
-    return dim3((unsigned)x, (unsigned)(256 / x > 0 ? 256 / x : 1));
-}
-
 template <typename T, int V, int KB>
 cudaError_t combine_dropout_v(const moe_shape& s, const void* y_perm, const int32_t* inv_perm,
                               const float* topk_w, const void* y_shared, const void* residual,
                               DropRule rule, const uint64_t* rng, void* y, cudaStream_t st) {
-    const dim3 block = row_block<V>(s.d);
-    return launch_pdl(combine_dropout_kernel<T, V, KB>, dim3((unsigned)ceil_div(s.T, block.y)), block,
-                      0, st, (const T*)y_perm, inv_perm, topk_w, (const T*)y_shared,
-                      (const T*)residual, (T*)y, s.T, s.d, s.K, (int64_t)s.T * s.K, rule, rng);
+    const dim3 block(32, 2);
+    const dim3 grid((unsigned)ceil_div(s.T, 2), (unsigned)ceil_div(s.d / 8, 32 * V));
+    return launch_pdl(combine_dropout_kernel<T, V, KB>, grid, block, 0, st, (const T*)y_perm, inv_perm,
+                      topk_w, (const T*)y_shared, (const T*)residual, (T*)y, s.T, s.d, s.K,
+                      (int64_t)s.T * s.K, rule, rng);
 }
 
 template <typename T, typename... Args>
 cudaError_t combine_dropout_t(const moe_shape& s, Args... args) {
-    if (s.d / 8 > 32) return combine_dropout_v<T, CV, CK>(s, args...);
-    return combine_dropout_v<T, 1, CK>(s, args...);
+    return s.d / 8 > 32 ? combine_dropout_v<T, 2, 1>(s, args...)
+                        : combine_dropout_v<T, 1, 4>(s, args...);
 }
 
 template <typename T, int V, int KB>
@@ -312,12 +314,17 @@ cudaError_t combine_backward_v(const moe_shape& s, const void* d_y, const void* 
                                const int32_t* inv_perm, const float* topk_w, DropRule rule,
                                const uint64_t* rng, void* d_y_perm, float* d_topk_w, void* d_shared,
                                cudaStream_t st) {
-    const dim3 block = row_block<V>(s.d);
+    // one token's row in whole warps; several tokens a block of 256 where it is short
+    const int x = (int)ceil_div(s.d / 8, V * 32) * 32;
+    const dim3 block((unsigned)x, (unsigned)(256 / x > 0 ? 256 / x : 1));
     return launch_pdl(combine_backward_kernel<T, V, KB>, dim3((unsigned)ceil_div(s.T, block.y)), block,
                       0, st, (const T*)d_y, (const T*)y_perm, inv_perm, topk_w, (T*)d_y_perm,
                       d_topk_w, (T*)d_shared, s.T, s.d, s.K, (int64_t)s.T * s.K, rule, rng);
 }
 
+// Two rows of two groups a thread, where they fit the registers of a whole-row
+// block (bf16) and a token has more than two: K = 2 took 33 us with two and 31 us
+// with one (T = 4096, d = 4096), and fp32 spilt (300 us against 198 us).
 template <typename T, typename... Args>
 cudaError_t combine_backward_t(const moe_shape& s, Args... args) {
     if (s.d / 8 <= 32) return combine_backward_v<T, 1, 1>(s, args...);
