@@ -517,3 +517,50 @@ def test_strided_and_wrong_tensors_are_refused(moe):
         call(out, idx.long(), out)
     with pytest.raises(moe.MoeError):  # rows go in 16-byte vectors
         call(torch.zeros(65, device="cuda")[1:], idx, out)
+
+
+# ---- the operators together -------------------------------------------------
+
+def test_router_step_gradient_is_the_losses(moe):
+    """One step of the example: d_scores through the library's calls against
+    differentiating the same step in 64 bits (experts' outputs as the library stored
+    them).  bf16 enters twice: y's rounding (2^-8 of |y|) in the error, and d_y's."""
+    from examples import train_router as ex
+    T, d, E, K = 64, 128, 8, 2
+    layer = ex.RouterTrainer(T, d, E, K, 128, sequences=2)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(T, d, generator=g, device="cuda").bfloat16()
+    target = torch.randn(T, d, generator=g, device="cuda").bfloat16()
+    w_g = (torch.randn(E, d, generator=g, device="cuda") * d ** -0.5).requires_grad_()
+    off = int(layer.rng[1])
+    scores = (x.float() @ w_g.t()).detach()
+    layer.step(x, target, w_g)
+
+    z = scores.cpu().double().requires_grad_()
+    idx, cu = layer.topk_idx.cpu(), layer.seq_offsets.tolist()
+    inv = layer.inv_perm.cpu().view(T, K)
+    w = ref.weights(z.gather(1, idx.long()), "softmax")
+    rows = layer.y_perm.cpu().double()[inv.long()]
+    keep, scale = ref.keep_and_scale((T, d), layer.p, 0, off)
+    y = x.cpu().double() + (w[:, :, None] * rows).sum(1) * keep * scale
+    task = (y - target.cpu().double()).square().mean()
+    total = task + ref.balance(z, idx, "softmax", layer.alpha, None, cu)[2]
+    want, = torch.autograd.grad(total, z)
+    # each element of err is off by 2^-8 |y|, d_y by another 2^-8 |d_y|; a score's
+    # gradient sums d of them over w (1 - w) <= 1/4 of a difference of two rows
+    off_y = 2.0 ** -8 * (y.detach().abs() + (y.detach() - target.cpu().double()).abs()) * 2 / y.numel()
+    size = (off_y[:, None] * rows.abs().sum(1, keepdim=True) * scale).sum(2)
+    got = layer.d_scores.cpu().double()
+    assert ((got - want).abs() <= size + 64 * U * want.abs() + TINY).all()
+    assert torch.allclose(w_g.grad.cpu().double(), want.t() @ x.cpu().double(),
+                          atol=(size.max() * x.float().abs().max().item() * T).item())
+
+
+def test_example_learns_and_balances(moe):
+    """The example's run: the student nears the teacher (the loss falls by far more
+    than its spread), and no expert is lost."""
+    from examples import train_router as ex
+    tasks, balances = ex.train(steps=60, T=1024, log=None)
+    assert np.isfinite(tasks).all() and np.isfinite(balances).all()
+    assert np.mean(tasks[-10:]) < 0.8 * np.mean(tasks[:5])
+    assert balances[-1] < 0.05 * 2  # alpha times 2: even use is alpha times 1
