@@ -36,6 +36,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr float kTinySum = 1e-30f;
+constexpr int kStages = 2;  // tiles a warp holds: one at hand, one on its way
 
 // ---- two fp32 values in a 64-bit register: one instruction works on both -----
 typedef uint64_t f2;
@@ -124,8 +125,6 @@ struct RowLayout {
     // column of value j of lane l
     __device__ static int col(int j, int l) { return (j / VEC * G + l) * VEC + j % VEC; }
 };
-
-constexpr int kStages = 2;  // tiles a warp holds: one at hand, one on its way
 
 // sums and maxima over the lanes of a group, of V rows side by side
 template <int G, int V>
@@ -392,7 +391,7 @@ struct SeqFinder {
 // or g grows from one such pair to the next, so the rows are its own): the sums
 // of the probabilities, the counts, and the number of slots counted.
 template <typename L, bool SIG>
-__global__ void __launch_bounds__(kThreads, L::kN <= 16 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
 balance_partial_kernel(BalanceArgs p) {
     extern __shared__ __align__(16) float sm[];  // rings, [kWarps][E] sums, [E] counts
     __shared__ int slots, bad;
@@ -409,13 +408,13 @@ balance_partial_kernel(BalanceArgs p) {
     pdl_wait();
     pdl_trigger();
     const SeqFinder seqs(p.cu, p.n_seq, p.T);
-    Ring<L> ring{p.logits, sm + warp * kStages * L::kTokens * E, w0, kStride, t1, E, lane, -1};
-    ring.start();
     // a lane's first pick of the tile that starts at token `next` (slot numbers
     // stay below 2^31)
     auto pick = [&](uint32_t f) { return f < t1 * K ? p.topk_idx[f] : -1; };
     uint32_t next = w0;
     int e_next = next < t1 ? pick(next * K + lane) : -1;
+    Ring<L> ring{p.logits, sm + warp * kStages * L::kTokens * E, w0, kStride, t1, E, lane, -1};
+    ring.start();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;  // for the kernel that adds the rows
     for (uint32_t t = t0; t < t1;) {
         uint32_t end;
@@ -610,7 +609,7 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(BalanceArgs p) {
 // holds K) and added to the tile's rows, which the gradient has replaced in
 // shared memory, before they are written out.
 template <typename L, bool SIG>
-__global__ void __launch_bounds__(kThreads, L::kN <= 16 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
 route_backward_kernel(RouteBackwardArgs p) {
     constexpr int V = L::kV;
     extern __shared__ __align__(16) float sm[];  // rings, [kWarps][E] coefficients
@@ -619,15 +618,14 @@ route_backward_kernel(RouteBackwardArgs p) {
     const int l = lane % L::kGroup, r = lane / L::kGroup;
     float* coef = sm + kWarps * kStages * L::kTokens * E + warp * E;
     const uint64_t w0 = ((uint64_t)blockIdx.x * kWarps + warp) * p.chunk;
-    if (w0 >= (uint64_t)p.T) return;
-    const uint32_t t0 = (uint32_t)w0, t1 = min(t0 + p.chunk, (uint32_t)p.T);
     pdl_wait();
     pdl_trigger();
+    if (w0 >= (uint64_t)p.T) return;
+    const uint32_t t0 = (uint32_t)w0, t1 = min(t0 + p.chunk, (uint32_t)p.T);
+    // What the first tile needs beside its scores is asked for before the ring's
+    // copies: behind those (30 MB over all SMs) each would wait 2 to 5 us.
     const SeqFinder seqs(p.cu, p.n_seq, p.T);
-    // without the balance loss no row is read: the ring's copies are empty
-    Ring<L> ring{p.logits, sm + warp * kStages * L::kTokens * E, t0, L::kTokens,
-                 p.counts ? t1 : t0, E, lane, -1};
-    ring.start();
+    const float up = p.counts ? p.alpha / (float)p.n_seq * (p.d_loss ? *p.d_loss : 1.f) : 0.f;
     // The picks, a lane each: a step takes the picks of `per` tokens.  At hand is
     // step `at` with its scores on their way, behind it the next one's experts.
     const int pw = 1 << p.pw_log, pick = lane & (pw - 1), of = lane >> p.pw_log;
@@ -650,30 +648,43 @@ route_backward_kernel(RouteBackwardArgs p) {
         z_at = e_at >= 0 ? __ldg(p.logits + (int64_t)(step + of) * E + e_at) : -INFINITY;
         load_next(step + per);
     };
-    if (p.d_topk_w) {
-        load_next(t0);
-        move_on(t0);
-    }
+    if (p.d_topk_w) load_next(t0);
+    // the counts of a sequence, a lane's columns: asked for, and made a_ge
+    constexpr int kC = (L::kN * L::kGroup + 31) / 32;
+    int32_t c_at[kC];
+    auto load_counts = [&](int g) {
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+            c_at[i] = lane + 32 * i < E ? p.counts[(int64_t)g * E + lane + 32 * i] : 0;
+    };
+    auto make_coef = [&]() {
+        int32_t total = 0;  // at most T * K
+#pragma unroll
+        for (int i = 0; i < kC; ++i) total += c_at[i];
+        total = __reduce_add_sync(0xffffffffu, total);
+        // a = alpha E c / (G K n^2) with n = total / K
+        const float n = (float)total, k = total > 0 ? up * (float)E / n * ((float)K / n) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+            if (lane + 32 * i < E) coef[lane + 32 * i] = (float)c_at[i] * k;
+        __syncwarp();
+    };
+    uint32_t end;
+    int g = seqs.find(t0, end);
+    if (p.counts && g >= 0) load_counts(g);
+    if (p.d_topk_w) move_on(t0);
+    // without the balance loss no row is read: the ring's copies are empty
+    Ring<L> ring{p.logits, sm + warp * kStages * L::kTokens * E, t0, L::kTokens,
+                 p.counts ? t1 : t0, E, lane, -1};
+    ring.start();
     for (uint32_t t = t0; t < t1;) {
-        uint32_t end;
-        const int g = seqs.find(t, end);
+        if (t != t0) {
+            g = seqs.find(t, end);
+            if (p.counts && g >= 0) load_counts(g);
+        }
         end = min(end, t1);
         const bool in_seq = g >= 0;
-        if (p.counts && in_seq) {
-            const int32_t* counts = p.counts + (int64_t)g * E;
-            float total = 0.f;
-            for (int e = lane; e < E; e += 32) {
-                const float c = (float)counts[e];
-                coef[e] = c;
-                total += c;
-            }
-            total = warp_sum(total);
-            // a = alpha E c / (G K n^2) with n = total / K
-            const float up = p.alpha / (float)p.n_seq * (p.d_loss ? *p.d_loss : 1.f);
-            const float k = total > 0.f ? up * (float)E / total * ((float)K / total) : 0.f;
-            for (int e = lane; e < E; e += 32) coef[e] *= k;
-            __syncwarp();
-        }
+        if (p.counts && in_seq) make_coef();
         int it = (int)((t - t0) / L::kTokens);
         for (uint32_t base = t0 + it * L::kTokens; base < end; base += L::kTokens, ++it) {
             float* tile = ring.get(it);
@@ -807,8 +818,8 @@ route_backward_kernel(RouteBackwardArgs p) {
 // Calls f with the row layout for E experts, 16 scores a lane where 32 lanes
 // allow it (8 and 32 where a row is shorter or longer): 16-byte vectors when rows
 // are multiples of 16 bytes.  Measured against 8 scores a lane on twice the lanes
-// (E = 256, 131072 tokens): the same 39 us for the loss, 56 us against 60 us for the
-// gradient.
+// (E = 256, 131072 tokens, before the blocks were two an SM): the same 39 us for the
+// loss, 56 us against 60 us for the gradient.
 template <int VEC, typename F>
 cudaError_t with_layout_of(int E, F&& f) {
     if (E <= 8) return f(RowLayout<VEC, 8, 1>{});
@@ -827,17 +838,19 @@ cudaError_t with_layout(int E, F&& f) {
 
 }  // namespace
 
-// Blocks an SM holds (registers and shared memory): the tokens are spread over
-// one wave of them, a second, part-filled wave being the dearest part of a small
-// kernel.
-int64_t wave(const moe_shape& s) { return (int64_t)152 * (s.E > 256 ? 2 : 3); }
+// The tokens are spread over one wave of blocks, two an SM.  A second, part-filled
+// wave is the dearest part of a small kernel; a third block an SM means 80 registers
+// a thread, which spill in the backward pass (E = 256, 131072 tokens: 52 us with two
+// blocks, 55 us with three; 16384 tokens: 12 us and 16 us), and three tiles a warp in
+// place of two gain nothing (52 us).
+constexpr int64_t kWave = 152 * 2;
 
 // tokens of a block of the forward pass: whole steps of its warps
 int balance_chunk(const moe_shape& s) {
     int chunk = 0;
     with_layout(s.E, [&](auto layout) {
         constexpr int step = decltype(layout)::kRows * kWarps;
-        chunk = (int)(ceil_div(ceil_div(s.T > 0 ? s.T : 1, wave(s)), step) * step);
+        chunk = (int)(ceil_div(ceil_div(s.T > 0 ? s.T : 1, kWave), step) * step);
         return cudaSuccess;
     });
     return chunk;
@@ -900,7 +913,7 @@ cudaError_t launch_route_backward(const moe_shape& s, RouteBackwardArgs a, cudaS
     while ((1 << a.pw_log) < s.K) ++a.pw_log;
     return with_layout(s.E, [&](auto layout) {
         using L = decltype(layout);
-        a.chunk = (int)(ceil_div(ceil_div(s.T, wave(s) * kWarps), L::kRows) * L::kRows);
+        a.chunk = (int)(ceil_div(ceil_div(s.T, kWave * kWarps), L::kRows) * L::kRows);
         const unsigned blocks = (unsigned)ceil_div(s.T, (int64_t)a.chunk * kWarps);
         const size_t smem = sizeof(float) * (size_t)s.E * (kWarps * (kStages * L::kTokens + 1));
         return launch_wide(s.router == MOE_ROUTER_SIGMOID ? route_backward_kernel<L, true>

@@ -124,7 +124,10 @@ def test_router_over_token_counts(moe, T, E, K, router):
 
 SEQS = {"ragged": [0, 5, 5, 6, 300, 301, 700], "gaps": [3, 40, 650], "all_empty": [9, 9, 9],
         "one_empty_first": [0, 0, 700], "single_tokens": list(range(0, 701)),
-        "many_empty": [0] * 40 + [350] * 40 + [700] * 40, "one": [0, 700]}
+        "many_empty": [0] * 40 + [350] * 40 + [700] * 40, "one": [0, 700],
+        # as many offsets as a warp holds in registers, and one more
+        "offsets_256": [min(700, 3 * i) for i in range(256)],
+        "offsets_257": [min(700, 3 * i) for i in range(257)]}
 
 
 @pytest.mark.parametrize("router", ROUTERS)
@@ -263,6 +266,43 @@ def test_router_is_the_same_on_every_run_and_stream(moe):
         gb = _route_backward(moe, z, idx, "sigmoid", 0.1, torch.ones(6000, 8), a[0].cpu(), None,
                              None, cu)
         assert torch.equal(ga, gb)
+
+
+def test_router_in_a_graph(moe):
+    """Loss and backward captured together follow their inputs at each replay."""
+    T, E, K, n = 300, 64, 4, 3
+    s = moe.make_shape(T, 64, E, K, 64, 0, "f32", "sigmoid")
+    ws = moe.alloc_balance_workspace(s, n)
+    cu = torch.tensor([0, 50, 120, 300], dtype=torch.int32).cuda()
+    z, idx = torch.empty(T, E, device="cuda"), torch.empty(T, K, dtype=torch.int32, device="cuda")
+    dw, out = torch.empty(T, K, device="cuda"), torch.empty(T, E, device="cuda")
+    counts = torch.empty(n, E, dtype=torch.int32, device="cuda")
+    mean, loss = torch.empty(n, E, device="cuda"), torch.empty(1, device="cuda")
+
+    def calls():
+        moe.moe_balance_loss(s, z, idx, None, cu, 0.1, counts, mean, loss, ws)
+        moe.moe_route_backward(s, z, idx, dw, None, cu, 0.1, counts, loss, out)
+
+    def fill(seed):
+        g, zz, ii = _scores(T, E, K, seed)
+        z.copy_(zz), idx.copy_(ii), dw.copy_(torch.randn(T, K, generator=g))
+
+    fill(1)
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for seed in (2, 3):
+        fill(seed)
+        graph.replay()
+        got = [t.clone() for t in (counts, mean, loss, out)]
+        calls()
+        for a, b in zip(got, (counts, mean, loss, out)):
+            assert torch.equal(a, b)
+        want, _, wl = ref.balance(z.cpu().double(), idx.cpu(), "sigmoid", 0.1, None, cu.tolist())
+        assert torch.equal(got[0].cpu().long(), want)
+        _near(got[2][0], wl, 404 * U * wl)
 
 
 def test_balance_of_the_library_s_own_routing(moe):
