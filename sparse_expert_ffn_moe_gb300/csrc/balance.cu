@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr float kTinySum = 1e-30f;
+constexpr float kTinySum = 1e-18f;
 constexpr int kStages = 2;  // tiles a warp holds: one at hand, one on its way
 
 // ---- two fp32 values in a 64-bit register: one instruction works on both -----
@@ -186,43 +186,58 @@ __device__ __forceinline__ void load_row(const float* row, int E, int l, bool li
 }
 
 // ---- a warp's ring of tiles in shared memory --------------------------------
-// Asynchronous copy of n floats by the lanes (16 bytes at a time where rows are
-// whole 16-byte vectors); one group per tile.
+// Asynchronous copy of the n floats at src + at to dst, by the lanes, as one
+// group.  16 bytes at a time: dst takes the place of the multiple of four floats at
+// or before src + at (which rows that are whole vectors always start at), and what
+// is left behind the last whole vector goes float by float.
 template <typename L>
-__device__ __forceinline__ void copy_tile(float* dst, const float* src, int n, int lane) {
-    constexpr int kB = L::kVec * 4;  // bytes of a copy
-    uint32_t d = ptx::smem_u32(dst) + lane * kB;
-    const char* g = reinterpret_cast<const char*>(src) + lane * kB;
-    int left = n / L::kVec - lane;  // copies from this lane's first on
+__device__ __forceinline__ void copy_tile(float* dst, const float* src, int64_t at, int n,
+                                          int lane) {
+    const int head = L::kVec == 4 ? 0 : (int)(at & 3);
+    const char* g = reinterpret_cast<const char*>(src + at - head);
+    const uint32_t d = ptx::smem_u32(dst);
+    const int whole = n > 0 ? (head + n) / 4 : 0;
     auto copy = [&](int i) {
-        if constexpr (kB == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i * 32 * kB),
-                         "l"(g + i * 32 * kB)
-                         : "memory");
-        else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d + i * 32 * kB),
-                         "l"(g + i * 32 * kB)
-                         : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i * 16), "l"(g + i * 16)
+                     : "memory");
     };
-    for (; left > 96; left -= 128, d += 128 * kB, g += 128 * kB) {
+    int i = lane;
+    for (; i + 96 < whole; i += 128) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) copy(i);
+        for (int k = 0; k < 4; ++k) copy(i + 32 * k);
     }
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-        if (left > i * 32) copy(i);
+    for (int k = 0; k < 3; ++k)
+        if (i + 32 * k < whole) copy(i + 32 * k);
+    if constexpr (L::kVec != 4) {
+        const int f = whole * 4 + lane;
+        if (n > 0 && f < head + n)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d + f * 4), "l"(g + f * 4)
+                         : "memory");
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// n floats of a tile to memory, by the lanes
+// n floats of a tile to dst + at, by the lanes; src is as far from a multiple of 16
+// bytes as dst + at is
 template <typename L>
-__device__ __forceinline__ void store_tile(float* dst, const float* src, int n, int lane) {
-    using W = typename std::conditional<L::kVec == 4, float4, float>::type;
-    W* d = reinterpret_cast<W*>(dst) + lane;
-    const W* q = reinterpret_cast<const W*>(src) + lane;
-    int left = n / L::kVec - lane;
+__device__ __forceinline__ void store_tile(float* dst, const float* src, int64_t at, int n,
+                                           int lane) {
+    float* out = dst + at;
+    if constexpr (L::kVec != 4) {
+        const int head = min(n, (int)(-at & 3));
+        if (lane < head) out[lane] = src[lane];
+        out += head;
+        src += head;
+        n -= head;
+        const int tail = n & 3;
+        if (lane < tail) out[n - tail + lane] = src[n - tail + lane];
+    }
+    float4* d = reinterpret_cast<float4*>(out) + lane;
+    const float4* q = reinterpret_cast<const float4*>(src) + lane;
+    int left = n / 4 - lane;
     for (; left > 96; left -= 128, d += 128, q += 128) {
-        W v[4];
+        float4 v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = q[i * 32];
 #pragma unroll
@@ -233,23 +248,30 @@ __device__ __forceinline__ void store_tile(float* dst, const float* src, int n, 
         if (left > i * 32) d[i * 32] = q[i * 32];
 }
 
+// floats of a tile's place in shared memory: its rows, and what lies beside them in
+// the vectors of its first and last float
+template <typename L>
+__host__ __device__ __forceinline__ int tile_floats(int E) {
+    return L::kVec == 4 ? L::kTokens * E : (L::kTokens * E + 6) / 4 * 4;
+}
+
 // Tile i of a warp holds tokens first + i * stride .. + kTokens - 1, up to
 // `last`.  (Tokens are unsigned 32-bit: one past a tile may pass 2^31.)
 template <typename L>
 struct Ring {
     const float* src;  // the scores, [T][E]
-    float* buf;        // [kStages][kTokens][E]
+    float* buf;        // kStages places of tile_floats
     uint32_t first, stride, last;
     int E, lane;
     int cur;  // the tile at hand (-1: none yet)
 
     __device__ __forceinline__ float* slot(int i) const {
-        return buf + (i & (kStages - 1)) * (L::kTokens * E);
+        return buf + (i & (kStages - 1)) * tile_floats<L>(E);
     }
     __device__ __forceinline__ void issue(int i) {
         const uint32_t tok = first + i * stride;
         const int n = tok >= last ? 0 : min(last - tok, (uint32_t)L::kTokens);
-        copy_tile<L>(slot(i), src + (int64_t)tok * E, n * E, lane);
+        copy_tile<L>(slot(i), src, (int64_t)tok * E, n * E, lane);
     }
     __device__ __forceinline__ void start() {
         cur = -1;
@@ -267,7 +289,7 @@ struct Ring {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
             __syncwarp();
         }
-        return slot(i);
+        return slot(i) + (L::kVec == 4 ? 0 : (int)((int64_t)(first + i * stride) * E & 3));
     }
 };
 
@@ -294,10 +316,10 @@ __device__ __forceinline__ void row_probs(f2 (&z)[V][L::kP], f2 (&s)[V][L::kP], 
     for (int v = 0; v < V; ++v) load_row<L>(row(v), E, l, live[v], z[v]);
     if constexpr (SIG) {
         // A row whose sigmoids sum to less than kTinySum has every score below
-        // -69, where sigmoid(z) is e^z to fp32's last bit and its share of the
+        // -41, where sigmoid(z) is e^z to fp32's last bit and its share of the
         // sum is the same for scores moved up together: such rows go round once
-        // more with their largest score at -18, so that they cannot underflow
-        // as a whole.
+        // more with their largest score at -18, so that neither they underflow as
+        // a whole nor 1 / sum, or its square, overflows.
         for (bool again = false;; again = true) {
             bool tiny = false;
 #pragma unroll
@@ -332,6 +354,42 @@ __device__ __forceinline__ void row_probs(f2 (&z)[V][L::kP], f2 (&s)[V][L::kP], 
 #pragma unroll
     for (int v = 0; v < V; ++v) inv[v] = inv[v] > 0.f ? rcp(inv[v]) : 0.f;
 }
+
+// Which of a tile's tokens take part: a bit a token, the mask's bytes asked for a
+// tile ahead.
+template <typename L>
+struct LiveBits {
+    using Bits = typename std::conditional<(L::kTokens > 32), uint64_t, uint32_t>::type;
+    static constexpr int kWords = (L::kTokens + 31) / 32;
+    const uint8_t* mask;
+    uint32_t last, at;
+    uint8_t held[kWords];
+
+    // asks for the bytes of the tile at token `base`
+    __device__ __forceinline__ void ask(uint32_t base) {
+        at = base;
+        if (mask == nullptr) return;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const uint32_t tok = base + w * 32 + (threadIdx.x & 31);
+            held[w] = tok < last ? mask[tok] : 0;
+        }
+    }
+    // the tokens [from, to) of the tile at `base` that are not masked
+    __device__ __forceinline__ Bits get(uint32_t base, uint32_t from, uint32_t to) {
+        Bits b = (Bits)~(Bits)0;
+        if (mask != nullptr) {
+            if (at != base) ask(base);
+            b = 0;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w)
+                b |= (Bits)__ballot_sync(0xffffffffu, held[w] != 0) << (w * 32 % (sizeof(Bits) * 8));
+        }
+        constexpr int kBits = sizeof(Bits) * 8;
+        b &= (Bits)~(Bits)0 << (from - base);
+        return b & (Bits)~(Bits)0 >> (kBits - (to - base));
+    }
+};
 
 // Finds the sequence of a token.  A warp holds up to kHeld * 32 of the n + 1
 // offsets in its registers, asked for before anything else is (behind a block's
@@ -398,7 +456,7 @@ balance_partial_kernel(BalanceArgs p) {
     constexpr int V = L::kV;
     constexpr uint32_t kStride = kWarps * L::kTokens;
     const int E = p.E, K = p.K;
-    float* sums = sm + kWarps * kStages * L::kTokens * E;
+    float* sums = sm + kWarps * kStages * tile_floats<L>(E);
     int32_t* hist = reinterpret_cast<int32_t*>(sums + kWarps * E);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane % L::kGroup, r = lane / L::kGroup;
@@ -413,7 +471,9 @@ balance_partial_kernel(BalanceArgs p) {
     auto pick = [&](uint32_t f) { return f < t1 * K ? p.topk_idx[f] : -1; };
     uint32_t next = w0;
     int e_next = next < t1 ? pick(next * K + lane) : -1;
-    Ring<L> ring{p.logits, sm + warp * kStages * L::kTokens * E, w0, kStride, t1, E, lane, -1};
+    LiveBits<L> alive{p.mask, t1, 0, {}};
+    alive.ask(w0);
+    Ring<L> ring{p.logits, sm + warp * kStages * tile_floats<L>(E), w0, kStride, t1, E, lane, -1};
     ring.start();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;  // for the kernel that adds the rows
     for (uint32_t t = t0; t < t1;) {
@@ -434,14 +494,13 @@ balance_partial_kernel(BalanceArgs p) {
             for (uint32_t base = w0 + i * kStride; base < end; base += kStride, ++i) {
                 const float* tile = ring.get(i);
                 const uint32_t from = max(t, base), to = min(end, base + L::kTokens);
+                const auto on = alive.get(base, from, to);
+                alive.ask(base + kStride);
                 const bool whole = to - from == L::kTokens && p.mask == nullptr;
                 if (next != base) e_next = pick(base * K + lane);
                 for (int j = lane; j < L::kTokens * K; j += 32) {
                     const int e = j < 32 ? e_next : pick(base * K + j);
-                    if (!whole) {
-                        const uint32_t tok = base + j / K;
-                        if (tok < from || tok >= to || (p.mask && p.mask[tok] == 0)) continue;
-                    }
+                    if (!whole && !(on >> j / K & 1)) continue;
                     if ((uint32_t)e < (uint32_t)E) {
                         atomicAdd(&hist[e], 1);
                         ++mine;
@@ -456,11 +515,7 @@ balance_partial_kernel(BalanceArgs p) {
                     if (base + h * L::kRows >= to) break;
                     bool live[V];
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const uint32_t tok = base + (h + v) * L::kRows + r;
-                        live[v] = whole || (tok >= from && tok < to &&
-                                            (p.mask == nullptr || p.mask[tok] != 0));
-                    }
+                    for (int v = 0; v < V; ++v) live[v] = on >> ((h + v) * L::kRows + r) & 1;
                     f2 z[V][L::kP], s[V][L::kP];
                     float inv[V];
                     auto row = [&](int v) { return tile + ((h + v) * L::kRows + r) * E; };
@@ -616,7 +671,7 @@ route_backward_kernel(RouteBackwardArgs p) {
     const int E = p.E, K = p.K;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane % L::kGroup, r = lane / L::kGroup;
-    float* coef = sm + kWarps * kStages * L::kTokens * E + warp * E;
+    float* coef = sm + kWarps * kStages * tile_floats<L>(E) + warp * E;
     const uint64_t w0 = ((uint64_t)blockIdx.x * kWarps + warp) * p.chunk;
     pdl_wait();
     pdl_trigger();
@@ -636,7 +691,7 @@ route_backward_kernel(RouteBackwardArgs p) {
     auto load_next = [&](uint32_t step) {
         const uint32_t tok = step + of;
         e_next = -1;
-        if (of < per && tok < t1 && pick < K && (p.mask == nullptr || p.mask[tok] != 0)) {
+        if (of < per && tok < t1 && pick < K) {
             e_next = p.topk_idx[tok * K + pick];  // T * K < 2^31
             dw_next = p.d_topk_w[tok * K + pick];
         }
@@ -649,6 +704,8 @@ route_backward_kernel(RouteBackwardArgs p) {
         load_next(step + per);
     };
     if (p.d_topk_w) load_next(t0);
+    LiveBits<L> alive{p.mask, t1, 0, {}};
+    alive.ask(t0);
     // the counts of a sequence, a lane's columns: asked for, and made a_ge
     constexpr int kC = (L::kN * L::kGroup + 31) / 32;
     int32_t c_at[kC];
@@ -674,7 +731,7 @@ route_backward_kernel(RouteBackwardArgs p) {
     if (p.counts && g >= 0) load_counts(g);
     if (p.d_topk_w) move_on(t0);
     // without the balance loss no row is read: the ring's copies are empty
-    Ring<L> ring{p.logits, sm + warp * kStages * L::kTokens * E, t0, L::kTokens,
+    Ring<L> ring{p.logits, sm + warp * kStages * tile_floats<L>(E), t0, L::kTokens,
                  p.counts ? t1 : t0, E, lane, -1};
     ring.start();
     for (uint32_t t = t0; t < t1;) {
@@ -690,7 +747,9 @@ route_backward_kernel(RouteBackwardArgs p) {
             float* tile = ring.get(it);
             const uint32_t from = max(t, base), to = min(end, base + L::kTokens);
             const bool inside = to - from == L::kTokens;
-            const bool whole = inside && in_seq && p.mask == nullptr;
+            auto on = alive.get(base, from, to);
+            alive.ask(base + L::kTokens);
+            if (!in_seq) on = 0;
 #pragma unroll
             for (int h = 0; h < L::kU; h += V) {
                 if (base + h * L::kRows >= to) break;
@@ -699,7 +758,7 @@ route_backward_kernel(RouteBackwardArgs p) {
                 for (int v = 0; v < V; ++v) {
                     const uint32_t tok = base + (h + v) * L::kRows + r;
                     in[v] = inside || (tok >= from && tok < to);
-                    live[v] = whole || (in[v] && in_seq && (p.mask == nullptr || p.mask[tok] != 0));
+                    live[v] = on >> (tok - base) & 1;
                 }
                 auto row = [&](int v) { return tile + ((h + v) * L::kRows + r) * E; };
                 f2 z[V][L::kP], s[V][L::kP];
@@ -721,7 +780,7 @@ route_backward_kernel(RouteBackwardArgs p) {
                     // p (a - sum p a) = z (inv a - inv^2 sum z a)
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        const f2 sub = both(-inv[v] * inv[v] * dot[v]);
+                        const f2 sub = both(-inv[v] * (inv[v] * dot[v]));
 #pragma unroll
                         for (int j = 0; j < L::kP; ++j) {
                             z[v][j] = mul2(z[v][j], fma2(c[j], both(inv[v]), sub));
@@ -762,8 +821,7 @@ route_backward_kernel(RouteBackwardArgs p) {
                         load_next(step);
                         move_on(step);
                     }
-                    const uint32_t tok = step + of;
-                    const int e = tok >= from && tok < to ? e_at : -1;
+                    const int e = of < per && (on >> (i0 + of) & 1) ? e_at : -1;
                     const float dw = dw_at;
                     float a = e >= 0 ? z_at : -INFINITY, b = 1.f;
                     move_on(step + per);
@@ -805,7 +863,7 @@ route_backward_kernel(RouteBackwardArgs p) {
                 __syncwarp();
             }
             // the rows of this sequence, contiguous in memory
-            store_tile<L>(p.d_logits + (int64_t)from * E, tile + (from - base) * E,
+            store_tile<L>(p.d_logits, tile + (from - base) * E, (int64_t)from * E,
                           (int)(to - from) * E, lane);
         }
         t = end;
@@ -888,8 +946,8 @@ cudaError_t launch_balance_loss(const moe_shape& s, BalanceArgs a, cudaStream_t 
     a.blocks = (int)balance_blocks(s);
     cudaError_t e = with_layout(s.E, [&](auto layout) {
         using L = decltype(layout);
-        const size_t smem = sizeof(float) * (size_t)s.E *
-                            (kWarps * kStages * L::kTokens + kWarps + 1);
+        const size_t smem = sizeof(float) * (size_t)(kWarps * kStages * tile_floats<L>(s.E) +
+                                                     (kWarps + 1) * s.E);
         return launch_wide(s.router == MOE_ROUTER_SIGMOID ? balance_partial_kernel<L, true>
                                                           : balance_partial_kernel<L, false>,
                            (unsigned)a.blocks, smem, st, a);
@@ -915,7 +973,8 @@ cudaError_t launch_route_backward(const moe_shape& s, RouteBackwardArgs a, cudaS
         using L = decltype(layout);
         a.chunk = (int)(ceil_div(ceil_div(s.T, kWave * kWarps), L::kRows) * L::kRows);
         const unsigned blocks = (unsigned)ceil_div(s.T, (int64_t)a.chunk * kWarps);
-        const size_t smem = sizeof(float) * (size_t)s.E * (kWarps * (kStages * L::kTokens + 1));
+        const size_t smem =
+            sizeof(float) * (size_t)(kWarps * (kStages * tile_floats<L>(s.E) + s.E));
         return launch_wide(s.router == MOE_ROUTER_SIGMOID ? route_backward_kernel<L, true>
                                                           : route_backward_kernel<L, false>,
                            blocks, smem, st, a);

@@ -167,7 +167,8 @@ def test_router_with_masked_tokens(moe, kind, router):
 
 
 @pytest.mark.parametrize("router", ROUTERS)
-@pytest.mark.parametrize("scale,shift", [(1, -200.0), (1, -80.0), (1, 80.0), (30, 0.0), (0, 0.0),
+@pytest.mark.parametrize("scale,shift", [(1, -200.0), (1, -80.0), (1, -65.0), (1, -55.0),
+                                         (1, -45.0), (1, -40.0), (1, -20.0), (1, 80.0), (30, 0.0), (0, 0.0),
                                          (1e-30, 0.0), (50, -300.0)])
 def test_router_with_far_scores(moe, scale, shift, router):
     """Scores where a sigmoid or an exponential under- or overflows on its own.  Tops
