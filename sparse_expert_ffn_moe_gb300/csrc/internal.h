@@ -262,7 +262,7 @@ struct BalanceArgs {
     float* shares;        // [n_seq * balance_slices]
     unsigned int* ticket;
     DevError* err;
-    int T, E, K, chunk, blocks;  // set by the launch
+    int T, E, K, chunk, blocks, solo;  // set by the launch
 };
 int64_t balance_blocks(const moe_shape& s);          // blocks of tokens
 int balance_slices(const moe_shape& s, int n_seq);   // blocks of columns a sequence
