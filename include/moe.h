@@ -1,6 +1,6 @@
 /*
  * moe.h -- C ABI of libmoe, the GB300 (sm_103a) forward pass of one sparse
- * Mixture-of-Experts FFN layer:
+ * Mixture-of-Experts FFN layer, and what its router is trained with:
  *
  *     y = SharedExpert(x) + sum_{i in TopK(x . W_g^T + b)} w_i * Expert_i(x),
  *     w = softmax over only the K selected scores,

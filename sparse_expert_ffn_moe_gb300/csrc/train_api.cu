@@ -119,6 +119,10 @@ moe_status moe_route_backward(const moe_shape* shape, const float* logits, const
     if ((st = check_seqs(seq_offsets, n_seq)) != MOE_OK) return st;
     if (s.T == 0) return MOE_OK;
     if (!good(logits, 16) || !good(d_logits, 16)) return MOE_ERR_INVALID_ARG;
+    // the copies of the scores run ahead of the gradient's rows
+    const uintptr_t in = (uintptr_t)logits, out = (uintptr_t)d_logits;
+    const uint64_t bytes = sizeof(float) * (uint64_t)s.T * (uint64_t)s.E;
+    if (in < out + bytes && out < in + bytes) return MOE_ERR_INVALID_ARG;
     if (!counts && !d_topk_w) return MOE_ERR_INVALID_ARG;
     if (!good_or_null(counts, 4) || !good_or_null(d_topk_w, 4) || !good_or_null(d_loss, 4))
         return MOE_ERR_INVALID_ARG;

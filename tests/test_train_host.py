@@ -135,8 +135,11 @@ def test_balance_loss_refusals(moe):
 def test_route_backward_refusals(moe):
     s = moe.make_shape(4, 64, 8, 2, 64, 0, "f32")
     good = dict(s=ctypes.byref(s), logits=FAKE, idx=FAKE, dw=FAKE, mask=None, cu=None, n=1,
-                alpha=0.1, counts=FAKE, d_loss=FAKE, out=FAKE, st=None)
+                alpha=0.1, counts=FAKE, d_loss=FAKE, out=2 * FAKE, st=None)
     bad = lambda **kw: _call(moe, "moe_route_backward", good, **kw)  # noqa: E731
+    size = 4 * 8 * 4  # bytes of the [T][E] scores: the gradient may not lie over them
+    for out in (FAKE, FAKE + size - 16, FAKE - size + 16):
+        assert bad(out=out) == moe.MOE_ERR_INVALID_ARG
     for name in ("logits", "out"):
         for p in (None, ODD, FAKE + 4):
             assert bad(**{name: p}) == moe.MOE_ERR_INVALID_ARG
