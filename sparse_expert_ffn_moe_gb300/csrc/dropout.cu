@@ -193,7 +193,7 @@ combine_dropout_kernel(const T* y_perm, const int32_t* __restrict__ inv_perm,
 // (6.88 TB/s, the measured copy's rate); four groups a thread without the
 // look-ahead took 774 us, one row at a time 698 us.
 template <typename T, int V, int KB>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(V == 1 ? 256 : 1024)
 combine_backward_kernel(const T* d_y, const T* y_perm, const int32_t* __restrict__ inv_perm,
                         const float* __restrict__ topk_w, T* d_y_perm, float* d_topk_w, T* d_shared,
                         int n_tokens, int d, int K, int64_t n_rows, DropRule rule,
@@ -322,14 +322,19 @@ cudaError_t combine_backward_v(const moe_shape& s, const void* d_y, const void* 
                       d_topk_w, (T*)d_shared, s.T, s.d, s.K, (int64_t)s.T * s.K, rule, rng);
 }
 
-// Two rows of two groups a thread, where they fit the registers of a whole-row
-// block (bf16) and a token has more than two: K = 2 took 33 us with two and 31 us
-// with one (T = 4096, d = 4096), and fp32 spilt (300 us against 198 us).
+// What a thread holds: in bf16 two rows of two groups each where a token has more
+// than two rows, else four groups of one row (K = 2, T = 4096, d = 4096: 28 us, two
+// groups 32 us; K = 1: 36 and 47 us); in fp32 two groups of one row (two rows spill:
+// 300 us against 198 us).  A row of at most 32 groups has one a thread, and two rows
+// (d = 256, K = 4: 28 us against 33 us with one).
 template <typename T, typename... Args>
 cudaError_t combine_backward_t(const moe_shape& s, Args... args) {
-    if (s.d / 8 <= 32) return combine_backward_v<T, 1, 1>(s, args...);
-    if constexpr (sizeof(T) == 2)
+    const int units = s.d / 8;
+    if (units <= 32) return combine_backward_v<T, 1, 2>(s, args...);
+    if constexpr (sizeof(T) == 2) {
         if (s.K > 2) return combine_backward_v<T, 2, 2>(s, args...);
+        if (units >= 128) return combine_backward_v<T, 4, 1>(s, args...);
+    }
     return combine_backward_v<T, 2, 1>(s, args...);
 }
 
