@@ -391,56 +391,69 @@ struct LiveBits {
     }
 };
 
-// Finds the sequence of a token.  A warp holds up to kHeld * 32 of the n + 1
-// offsets in its registers, asked for before anything else is (behind a block's
-// first copies they would wait as long as those); more are searched in memory, 32
-// ways at a time.
+// Finds the sequence of a token.  A warp holds a window of kHeld * 32 of the n + 1
+// offsets in its registers; all of them, if there are no more, asked for before
+// anything else is (behind a block's first copies they would wait as long as
+// those).  A token outside the window is searched for in memory, 32 ways at a time,
+// and the window moved there.
 constexpr int kHeld = 8;
 struct SeqFinder {
     const int32_t* cu;
     int n, T;
+    int base;  // offset of the window's first
     int32_t held[kHeld];
 
     __device__ __forceinline__ SeqFinder(const int32_t* __restrict__ cu_, int n_, int T_)
         : cu(cu_), n(n_), T(T_) {
-        if (cu == nullptr || n >= kHeld * 32) return;
-        const int lane = threadIdx.x & 31;
+        if (cu != nullptr && n < kHeld * 32) hold(0);
+        else base = -1;
+    }
+    __device__ __forceinline__ void hold(int first) {
+        base = first;
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-            held[i] = i * 32 + lane <= n ? cu[i * 32 + lane] : 0x7fffffff;
+        for (int i = 0; i < kHeld; ++i) {
+            const int k = first + i * 32 + (int)(threadIdx.x & 31);
+            held[i] = k <= n ? cu[k] : 0x7fffffff;
+        }
     }
     // The sequence of `token` (-1: none, before the first or after the last), and
     // in `end` the token up to which the answer holds.  Whatever the offsets are,
     // end > token and the answer is below n.
-    __device__ __forceinline__ int find(uint32_t token, uint32_t& end) const {
+    __device__ __forceinline__ int find(uint32_t token, uint32_t& end) {
         end = T;
         if (cu == nullptr) return 0;
         const int lane = threadIdx.x & 31, t = (int)token;
-        if (n < kHeld * 32) {
-            int before = 0, next = T;
+        for (bool moved = false;; moved = true) {
+            if (base >= 0) {
+                int before = 0, next = 0x7fffffff;
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
-                before += held[i] <= t;
-                if (held[i] > t) next = min(next, held[i]);
+                for (int i = 0; i < kHeld; ++i) {
+                    before += held[i] <= t;
+                    if (held[i] > t) next = min(next, held[i]);
+                }
+                before = __reduce_add_sync(0xffffffffu, before);
+                next = __reduce_min_sync(0xffffffffu, next);
+                // inside the window: an offset on either side, or none there is
+                if (moved || ((before > 0 || base == 0) &&
+                              (next != 0x7fffffff || base + kHeld * 32 > n))) {
+                    if (base + before > n) return -1;
+                    end = min(next, T);
+                    return base + before - 1;
+                }
             }
-            before = __reduce_add_sync(0xffffffffu, before);
-            end = __reduce_min_sync(0xffffffffu, next);
-            return before <= n ? before - 1 : -1;
+            int lo = 0, hi = n + 1;  // cu[lo - 1] <= t < cu[hi], where those exist
+            while (lo < hi) {
+                const int step = (hi - lo + 31) / 32;
+                const int i = lo + lane * step;
+                const int c = __ffs(~__ballot_sync(0xffffffffu, i < hi && cu[i] <= t)) - 1;
+                const int k = c < 0 ? 32 : c;  // lanes up to the first that says no
+                if (k == 0) break;
+                const int first = lo;
+                lo = first + (k - 1) * step + 1;
+                hi = min(hi, first + k * step);
+            }
+            hold(max(lo - 1, 0));
         }
-        int lo = 0, hi = n + 1;  // cu[lo - 1] <= t < cu[hi], where those exist
-        while (lo < hi) {
-            const int step = (hi - lo + 31) / 32;
-            const int i = lo + lane * step;
-            const int c = __ffs(~__ballot_sync(0xffffffffu, i < hi && cu[i] <= t)) - 1;
-            const int k = c < 0 ? 32 : c;  // lanes up to the first that says no
-            if (k == 0) break;
-            const int first = lo;
-            lo = first + (k - 1) * step + 1;
-            hi = min(hi, first + k * step);
-        }
-        if (lo > n) return -1;
-        end = min(cu[lo], T);
-        return lo - 1;
     }
 };
 
@@ -470,7 +483,7 @@ balance_partial_kernel(BalanceArgs p) {
     if (threadIdx.x == 0) bad = 0;
     pdl_wait();
     pdl_trigger();
-    const SeqFinder seqs(p.cu, p.n_seq, p.T);
+    SeqFinder seqs(p.cu, p.n_seq, p.T);
     // a lane's first pick of the tile that starts at token `next` (slot numbers
     // stay below 2^31)
     auto pick = [&](uint32_t f) { return f < t1 * K ? p.topk_idx[f] : -1; };
@@ -714,7 +727,7 @@ route_backward_kernel(RouteBackwardArgs p) {
     const uint32_t t0 = (uint32_t)w0, t1 = min(t0 + p.chunk, (uint32_t)p.T);
     // What the first tile needs beside its scores is asked for before the ring's
     // copies: behind those (30 MB over all SMs) each would wait 2 to 5 us.
-    const SeqFinder seqs(p.cu, p.n_seq, p.T);
+    SeqFinder seqs(p.cu, p.n_seq, p.T);
     const float up = p.counts ? p.alpha / (float)p.n_seq * (p.d_loss ? *p.d_loss : 1.f) : 0.f;
     // The picks, a lane each: a step takes the picks of `per` tokens.  At hand is
     // step `at` with its scores on their way, behind it the next one's experts.
@@ -966,10 +979,10 @@ cudaError_t launch_wide(void (*kernel)(Args), unsigned blocks, size_t smem, cuda
     return launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, st, args);
 }
 
-// slices of 32 columns, side by side while the sequences alone leave SMs idle
+// slices of 32 columns, side by side while that leaves at most eight blocks an SM
 int balance_slices(const moe_shape& s, int n_seq) {
     const int all = (int)ceil_div(s.E, 32);
-    const int fill = (int)ceil_div(304, n_seq);
+    const int fill = (int)ceil_div(152 * 8, n_seq);
     return all < fill ? all : fill;
 }
 
@@ -1000,11 +1013,12 @@ cudaError_t launch_balance_loss(const moe_shape& s, BalanceArgs a, cudaStream_t 
                            (unsigned)a.blocks, smem, st, a);
     });
     if (e != cudaSuccess || a.solo) return e;
-    // a block per sequence and slice of columns, a warp for every four of the
-    // partial rows that a sequence has on average
+    // A block per sequence and slice of columns, a warp for each of the partial rows
+    // that a sequence has on average: the longest of ragged ones has several times
+    // as many, and all wait for its block.
     const int64_t rows = ceil_div(a.blocks, a.n_seq) + 1;
-    int warps = 2;
-    while (warps < 32 && warps * 4 < rows) warps *= 2;
+    int warps = 4;
+    while (warps < 32 && warps < rows) warps *= 2;
     return launch_pdl(balance_final_kernel,
                       dim3((unsigned)a.n_seq, (unsigned)balance_slices(s, a.n_seq)),
                       dim3((unsigned)warps * 32), (size_t)warps * 32 * 8, st, a);
