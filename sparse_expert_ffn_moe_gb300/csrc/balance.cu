@@ -525,15 +525,25 @@ balance_partial_kernel(BalanceArgs p) {
                 alive.ask(base + kStride);
                 const bool whole = to - from == L::kTokens && p.mask == nullptr;
                 if (next != base) e_next = pick(base * K + lane);
-                for (int j = lane; j < L::kTokens * K; j += 32) {
-                    const int e = j < 32 ? e_next : pick(base * K + j);
-                    if (!whole && !(on >> j / K & 1)) continue;
+                const int picks = L::kTokens * K;
+                auto count = [&](int j, int e) {
+                    if (j >= picks || (!whole && !(on >> j / K & 1))) return;
                     if ((uint32_t)e < (uint32_t)E) {
                         atomicAdd(&hist[e], 1);
                         ++mine;
                     } else {
                         bad = 1;
                     }
+                };
+                count(lane, e_next);
+                // (a token has no more than 32) the rest, four asked for at once
+                for (int j = lane + 32; L::kTokens > 1 && j < picks; j += 128) {
+                    int e[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        e[q] = j + 32 * q < picks ? pick(base * K + j + 32 * q) : -1;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) count(j + 32 * q, e[q]);
                 }
                 next = base + kStride;
                 e_next = next < t1 ? pick(next * K + lane) : -1;
