@@ -279,7 +279,8 @@ combine_backward_kernel(const T* d_y, const T* y_perm, const int32_t* __restrict
     if (d_topk_w && on && threadIdx.x < K) {
         float s = 0.f;
         for (int w = 0; w < nwarps; ++w) s += red[threadIdx.y * nwarps + w][threadIdx.x];
-        d_topk_w[t * K + threadIdx.x] = s;
+        // this lane's slot; a dropped one has 0, whatever dz holds
+        d_topk_w[t * K + threadIdx.x] = slots.p >= 0 ? s : 0.f;
     }
 }
 

@@ -269,6 +269,40 @@ def test_router_is_the_same_on_every_run_and_stream(moe):
         assert torch.equal(ga, gb)
 
 
+@pytest.mark.parametrize("E", [1024, 1023])
+def test_router_past_two_to_the_31_scores(moe, E):
+    """Rows of scores and of their gradient that lie beyond 2^31 elements: all scores 0
+    but the last three rows', which are a sequence of their own."""
+    T, K = (1 << 21) + 4099, 2
+    z = torch.zeros(T, E, device="cuda")
+    idx = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda").repeat(T, 1)
+    _, last, picks = _scores(3, E, K, 21)
+    z[-3:], idx[-3:] = last.cuda(), picks.cuda()
+    cu = [0, T - 3, T]
+    s = moe.make_shape(T, 64, E, K, 64, 0, "f32")
+    ws = moe.alloc_balance_workspace(s, 2)
+    counts = torch.empty(2, E, dtype=torch.int32, device="cuda")
+    mean, loss, out = torch.empty(2, E, device="cuda"), torch.empty(1, device="cuda"), torch.empty_like(z)
+    cud = torch.tensor(cu, dtype=torch.int32).cuda()
+    moe.moe_balance_loss(s, z, idx, None, cud, 0.5, counts, mean, loss, ws)
+    moe.moe_route_backward(s, z, idx, None, None, cud, 0.5, counts, None, out)
+    assert moe.moe_get_device_error(ws) == 0
+    wc, wm, _ = ref.balance(last.double(), picks, "softmax", 0.5)
+    assert torch.equal(counts[1].cpu().long(), wc[0])
+    _near(mean[1], wm[0], 400 * U * wm[0])
+    assert counts[0].cpu().tolist()[:3] == [T - 3, T - 3, 0] and counts[0].sum() == 2 * (T - 3)
+    # two million equal terms in a tree of chains of at most 7000 adds
+    _near(mean[0], torch.full((E,), 1.0 / E, dtype=torch.float64), 7000 * U / E)
+    want, size = ref.route_grad(last, picks, "softmax", 0.25, None, wc)  # one of two sequences
+    _near(out[-3:], want, 64 * U * size + U * want.abs())
+    # a row of equal scores: a_e - mean(a), over E, at the picks and beside them
+    a = 0.25 * E * (T - 3) / (K * (T - 3.0) ** 2)
+    row = torch.full((E,), -2 * a / E / E, dtype=torch.float64)
+    row[:2] += a / E
+    for r in (0, T // 2, T - 4):
+        _near(out[r], row, 64 * U * (2 * a / E))
+
+
 def test_router_in_a_graph(moe):
     """Loss and backward captured together follow their inputs at each replay."""
     T, E, K, n = 300, 64, 4, 3
@@ -490,6 +524,24 @@ def test_combine_backward(moe, T, K, d, dtype, p):
     moe.moe_combine_backward(s, gy, over, dev["inv"], dev["w"], p, rng, over, w3, gy)
     assert torch.equal(w3, dw) and torch.equal(gy, dsh)
     assert torch.equal(over[named.cuda()], rows[named.cuda()])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 512])
+def test_dropped_slots_have_no_gradient(moe, d, dtype):
+    """inv_perm -1 gives d_topk_w 0 even where the output's gradient is not finite."""
+    T, K = 5, 3
+    c = _combine_inputs(T, K, d, dtype, 3)
+    c["inv"][2] = -1
+    c["inv"][4, 1] = T * K
+    c["d_y"][2], c["d_y"][4] = float("inf"), float("nan")
+    s = moe.make_shape(T, d, 4, K, 64, 0, dtype)
+    dw = torch.full((T, K), 7.0, device="cuda")
+    moe.moe_combine_backward(s, c["d_y"].cuda(), c["y_perm"].cuda(), c["inv"].cuda(), None, 0.0, None,
+                             None, dw, None)
+    got = dw.cpu()
+    assert (got[2] == 0).all() and got[4, 1] == 0 and torch.isnan(got[4, 0])
+    assert torch.isfinite(got[[0, 1, 3]]).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
