@@ -264,7 +264,7 @@ struct BalanceArgs {
     DevError* err;
     int T, E, K, chunk, blocks, solo;  // set by the launch
 };
-int64_t balance_blocks(const moe_shape& s);          // blocks of tokens
+int64_t balance_blocks(const moe_shape& s, int n_seq);  // blocks of tokens
 int balance_slices(const moe_shape& s, int n_seq);   // blocks of columns a sequence
 cudaError_t launch_balance_loss(const moe_shape& s, BalanceArgs a, cudaStream_t st);
 struct RouteBackwardArgs {

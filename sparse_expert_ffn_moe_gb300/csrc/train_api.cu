@@ -30,7 +30,7 @@ struct BalanceWs {
 
 BalanceWs balance_ws(const moe_shape& s, int32_t n_seq) {
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    const size_t blocks = (size_t)balance_blocks(s), rows = blocks + (size_t)n_seq;
+    const size_t blocks = (size_t)balance_blocks(s, n_seq), rows = blocks + (size_t)n_seq;
     const size_t shares = (size_t)n_seq * (size_t)balance_slices(s, n_seq);
     BalanceWs w;
     w.shares = kErrBytes;
