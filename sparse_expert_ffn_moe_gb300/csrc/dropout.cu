@@ -20,10 +20,14 @@ namespace moe {
 
 namespace {
 
-// A thread takes groups of eight elements, gridDim.x * 256 apart, and draws each
-// group's bits while its loads are on their way.  16384 x 7168 bf16 with residual
-// takes 108 us (704 MB, 6.5 TB/s); masks gathered into a byte before use took 156 us,
-// the integer work then bounding it.
+// A thread takes groups of eight elements, gridDim.x * 256 apart and two at a time,
+// and draws their bits while their loads are on their way.  16384 x 7168 bf16 with
+// residual takes 102 us (705 MB, 6.9 TB/s; one group at a time 108 us); masks
+// gathered into a byte before use took 156 us, the integer work then bounding it.
+// Without residual that work, about 140 instructions a group, weighs more: 15920 x
+// 3080 takes 35 us (5.5 TB/s; 41 us one at a time).  40 blocks an SM are
+// the best of both: 8 to 24 cost fp32 up to a fifth, 64 and more bf16 a tenth.
+constexpr int kGroups = 2, kDropoutBlocks = 40;
 template <typename T>
 __global__ void __launch_bounds__(256)
 dropout_kernel(const T* x, const T* residual, T* y, int64_t n, DropRule rule,
@@ -34,22 +38,36 @@ dropout_kernel(const T* x, const T* residual, T* y, int64_t n, DropRule rule,
     if (rule.thr) st = load_rng(rng);
     const int64_t groups = n / 8;
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g < groups; g += stride) {
-        float f[8];
-        const Unit<T> v = load_unit(x + g * 8);
-        Unit<T> r;
-        if (residual) r = load_unit(residual + g * 8);
-        Bits8 bits = {};
-        if (rule.thr) bits = draw8((uint64_t)g, st);
-        widen(v, f);
-        if (rule.thr) drop8(f, bits, rule);
-        if (residual) {
-            float rf[8];
-            widen(r, rf);
+    for (int64_t g0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g0 < groups;
+         g0 += kGroups * stride) {
+        Unit<T> v[kGroups], r[kGroups];
+        Bits8 bits[kGroups] = {};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] += rf[k];
+        for (int i = 0; i < kGroups; ++i) {
+            const int64_t g = g0 + i * stride;
+            if (g < groups) {
+                v[i] = load_unit(x + g * 8);
+                if (residual) r[i] = load_unit(residual + g * 8);
+            }
         }
-        store_unit(y + g * 8, f);
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+            if (rule.thr) bits[i] = draw8((uint64_t)(g0 + i * stride), st);
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int64_t g = g0 + i * stride;
+            if (g >= groups) break;
+            float f[8];
+            widen(v[i], f);
+            if (rule.thr) drop8(f, bits[i], rule);
+            if (residual) {
+                float rf[8];
+                widen(r[i], rf);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] += rf[k];
+            }
+            store_unit(y + g * 8, f);
+        }
     }
     // the last, partial group
     if (blockIdx.x == 0 && threadIdx.x == 0 && n % 8) {
@@ -288,7 +306,7 @@ template <typename T>
 cudaError_t dropout_t(int64_t n, const void* x, const void* residual, DropRule rule,
                       const uint64_t* rng, void* y, cudaStream_t st) {
     const int64_t blocks = ceil_div(n / 8 > 0 ? n / 8 : 1, 256);
-    const int64_t most = (int64_t)device_sm_count() * 64;
+    const int64_t most = (int64_t)device_sm_count() * kDropoutBlocks;
     return launch_pdl(dropout_kernel<T>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256),
                       0, st, (const T*)x, (const T*)residual, (T*)y, n, rule, rng);
 }

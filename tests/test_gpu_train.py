@@ -125,6 +125,7 @@ def test_router_over_token_counts(moe, T, E, K, router):
 SEQS = {"ragged": [0, 5, 5, 6, 300, 301, 700], "gaps": [3, 40, 650], "all_empty": [9, 9, 9],
         "one_empty_first": [0, 0, 700], "single_tokens": list(range(0, 701)),
         "many_empty": [0] * 40 + [350] * 40 + [700] * 40, "one": [0, 700],
+        "more_than_tokens": [i * 7 // 9 for i in range(901)],
         # as many offsets as a warp holds in registers, and one more
         "offsets_256": [min(700, 3 * i) for i in range(256)],
         "offsets_257": [min(700, 3 * i) for i in range(257)]}
@@ -132,10 +133,17 @@ SEQS = {"ragged": [0, 5, 5, 6, 300, 301, 700], "gaps": [3, 40, 650], "all_empty"
 
 @pytest.mark.parametrize("router", ROUTERS)
 @pytest.mark.parametrize("name", sorted(SEQS))
-@pytest.mark.parametrize("E,K", [(8, 2), (64, 6), (256, 8)])
+@pytest.mark.parametrize("E,K", [(6, 5), (8, 2), (64, 6), (256, 8)])
 def test_router_over_sequences(moe, name, E, K, router):
     _, z, idx = _scores(700, E, K, 5)
     _check_router(moe, z, idx, router, None, SEQS[name])
+
+
+@pytest.mark.parametrize("T", [1, 17, 32])
+def test_few_tokens_in_many_sequences(moe, T):
+    _, z, idx = _scores(T, 6, 5, T)
+    mask = (torch.arange(T) % 5 != 3).to(torch.uint8)
+    _check_router(moe, z, idx, "sigmoid", mask, [i * T // 383 for i in range(384)])
 
 
 @pytest.mark.parametrize("router", ROUTERS)
