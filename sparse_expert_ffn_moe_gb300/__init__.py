@@ -382,7 +382,9 @@ def moe_dropout(x, residual, p, rng, y, stream=None):
     """y = residual + dropout(x), x of any shape (bf16 or fp32); rng an int64
     device tensor {seed, offset}.  The same call on the output's gradient, with
     the same rng and no residual, gives x's gradient."""
-    dtype = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}[x.dtype]
+    dtype = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}.get(x.dtype)
+    if dtype is None:
+        raise ValueError(f"x must be torch.bfloat16 or torch.float32, not {x.dtype}")
     n = x.numel()
     _check(_lib.moe_dropout(n, dtype, _arg(x, "x", x.dtype, n),
                             _arg(residual, "residual", x.dtype, n, True), p, _rng(rng),

@@ -205,3 +205,10 @@ def test_binding_refuses_host_and_strided_tensors(moe):
     s = moe.make_shape(4, 64, 8, 2, 64, 0, "f32")
     with pytest.raises(ValueError, match="missing"):
         moe.moe_balance_loss(s, None, None, None, None, 0.1, None, None, None, None, stream=0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float64, torch.int32])
+def test_dropout_refuses_other_types(moe, dtype):
+    x = torch.zeros(4, 8, dtype=dtype)
+    with pytest.raises(ValueError, match="bfloat16 or torch.float32"):
+        moe.moe_dropout(x, None, 0.0, None, x, stream=0)
