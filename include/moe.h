@@ -458,7 +458,8 @@ moe_status moe_route_backward(const moe_shape *shape, const float *logits,
 /*
  * Dropout with a mask that is never stored: y = residual + D(x) over n
  * elements of `dtype` (residual may be NULL), added in fp32 and rounded once.
- *   thr = round(65536 p);  D(x)_i = u_i >= thr ? x_i * 65536 / (65536 - thr) : 0
+ *   thr = floor(65536 p + 1/2), in double
+ *   D(x)_i = u_i >= thr ? x_i * 65536 / (65536 - thr) : 0
  * with u_i 16 bits of Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel
  * random numbers: as easy as 1, 2, 3", SC 2011): counter words (low and high
  * half of i / 8, low and high half of rng[1]), key the halves of rng[0]; u_i is

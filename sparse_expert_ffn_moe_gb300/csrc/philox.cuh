@@ -27,7 +27,8 @@ struct DropRule {
     float scale;
 };
 
-// p in [0, 1]: rounded to the nearest multiple of 2^-16
+// p in [0, 1]: rounded to the nearest multiple of 2^-16 (the sum in double, so thr is 1
+// from the largest p below 2^-17 on)
 inline DropRule drop_rule(double p) {
     DropRule r;
     r.thr = (uint32_t)(p * 65536.0 + 0.5);

@@ -5,6 +5,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "philox.cuh"
 
 using namespace moe;
 
@@ -48,11 +49,11 @@ moe_status check_seqs(const int32_t* seq_offsets, int32_t n_seq) {
     return n_seq <= kMaxSeqs ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
-// p in [0, 1] (not NaN), and the generator's words where something is drawn
+// p in [0, 1] (not NaN), and the generator's words where something is drawn: where
+// the rule that the kernels get says so
 moe_status check_drop(double p, const uint64_t* rng) {
     if (!(p >= 0.0 && p <= 1.0)) return MOE_ERR_INVALID_ARG;
-    const bool draws = p * 65536.0 >= 0.5;
-    if ((draws && !rng) || !aligned(rng, 8)) return MOE_ERR_INVALID_ARG;
+    if ((drop_rule(p).thr && !rng) || !aligned(rng, 8)) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
 

@@ -212,3 +212,23 @@ def test_dropout_refuses_other_types(moe, dtype):
     x = torch.zeros(4, 8, dtype=dtype)
     with pytest.raises(ValueError, match="bfloat16 or torch.float32"):
         moe.moe_dropout(x, None, 0.0, None, x, stream=0)
+
+
+@pytest.mark.parametrize("name", ["moe_dropout", "moe_combine_dropout", "moe_combine_backward"])
+def test_generator_is_asked_for_wherever_something_is_drawn(moe, name):
+    """The threshold is 65536 p + 1/2 rounded down, in double: it is 1 from the largest
+    double below 2^-17 on (the sum rounds to 1), and there the generator's words are
+    read.  Asked of calls of no elements, which read nothing."""
+    s = moe.make_shape(0, 64, 8, 2, 64, 0, "bf16")
+    good = {"moe_dropout": dict(n=0, dtype=moe.MOE_BF16, x=None, res=None, p=0.0, rng=None, y=None,
+                                st=None),
+            "moe_combine_dropout": dict(s=ctypes.byref(s), y_perm=None, inv=None, w=None, sh=None,
+                                        res=None, p=0.0, rng=None, y=None, st=None),
+            "moe_combine_backward": dict(s=ctypes.byref(s), d_y=None, y_perm=None, inv=None, w=None,
+                                         p=0.0, rng=None, d_rows=None, d_w=None, d_sh=None,
+                                         st=None)}[name]
+    edge = np.nextafter(2.0 ** -17, 0.0)
+    for p in (0.0, 5e-324, 2.0 ** -18, np.nextafter(edge, 0.0), edge, 2.0 ** -17, 2.0 ** -16, 0.5, 1.0):
+        draws = int(float(p) * 65536 + 0.5) > 0
+        assert _call(moe, name, good, p=float(p)) == (moe.MOE_ERR_INVALID_ARG if draws else moe.MOE_OK)
+        assert _call(moe, name, good, p=float(p), rng=FAKE) == moe.MOE_OK
