@@ -712,6 +712,7 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(BalanceArgs p) {
                      : "memory");
     }
     if (__shfl_sync(0xffffffffu, done, 0) != blocks - 1u) return;
+    __syncwarp();  // the shuffle orders no memory: what lane 0 acquired, for the others too
     const float v =
         warp_sum_over<float>(0, blocks, [&](int64_t i) { return __ldcg(p.shares + i); });
     if (lane == 0) *p.loss = v * scale;
