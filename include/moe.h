@@ -398,7 +398,10 @@ moe_status moe_forward_w8a8_blocks(const moe_shape *shape, const void *x, const 
  * takes: s for MOE_ROUTER_SIGMOID, s + b for MOE_ROUTER_SOFTMAX (what
  * moe_route's logits_out gives for that router).  They are finite (below 1e38
  * in magnitude), or -inf for an expert that a token may not take (its
- * probability and gradient are 0).
+ * probability and gradient are 0).  A NaN or +inf is not passed over: the
+ * token's probabilities and their gradient are NaN, and so are its sequence's
+ * mean_probs and the loss; among a token's picked scores, the gradient at its
+ * picks is.  Other tokens and sequences keep their values.
  *
  * token_mask [T] (bytes, may be NULL): a token with a 0 takes no part -- it is
  * not counted, and its row of d_logits is 0; its logits are not used.

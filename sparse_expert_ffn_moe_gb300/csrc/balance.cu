@@ -75,6 +75,19 @@ __device__ __forceinline__ float rcp(float v) {
     return r;
 }
 
+// maximum and minimum that are NaN where either value is: a clamp must not turn a score
+// that is not a number into one (the same single instruction as without NaN)
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // e^x of two values whose exponentials stay finite (and |x| < 2e38).  t = x
 // log2(e) is rounded for the hardware's 2^t; what that took off, d = x - t ln 2
 // (ln 2 in two parts), comes back as a factor e^d = 1 + d, so the error stays at
@@ -102,7 +115,7 @@ constexpr float kOver = 88.7f;     // e^kOver is finite, and 1 / e^kOver rounds 
 __device__ __forceinline__ void sigmoid2(f2 z, f2& a, f2& b) {
     float z0, z1;
     unpack2(z, z0, z1);
-    const f2 e = exp2x(pack2(fminf(-z0, kOver), fminf(-z1, kOver)));
+    const f2 e = exp2x(pack2(min_nan(-z0, kOver), min_nan(-z1, kOver)));
     float d0, d1;
     unpack2(add2(e, both(1.f)), d0, d1);
     a = pack2(rcp(d0), rcp(d1));
@@ -300,7 +313,7 @@ __device__ __forceinline__ float exp_row(f2 (&z)[P], float m) {
     for (int i = 0; i < P; ++i) {
         float lo, hi;
         unpack2(add2(z[i], both(-m)), lo, hi);
-        z[i] = exp2x(pack2(fmaxf(lo, -kFar), fmaxf(hi, -kFar)));
+        z[i] = exp2x(pack2(max_nan(lo, -kFar), max_nan(hi, -kFar)));
     }
     return pair_sum(z);
 }
@@ -308,7 +321,7 @@ __device__ __forceinline__ float exp_row(f2 (&z)[P], float m) {
 // The router's probabilities of V rows, row(v) in shared memory (of none where
 // !live[v]), are z times inv; for the sigmoid router s = 1 - sigmoid, the backward
 // pass's factor.  Experts with a score of -inf get 0, and a row of them gets all
-// zeros.
+// zeros; a row with a NaN or +inf gets NaN, by its sum.
 template <typename L, bool SIG, int V, typename R>
 __device__ __forceinline__ void row_probs(f2 (&z)[V][L::kP], f2 (&s)[V][L::kP], float (&inv)[V],
                                           R&& row, int E, int l, const bool (&live)[V]) {
@@ -352,7 +365,7 @@ __device__ __forceinline__ void row_probs(f2 (&z)[V][L::kP], f2 (&s)[V][L::kP], 
         group_sum<L::kGroup>(inv);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) inv[v] = inv[v] > 0.f ? rcp(inv[v]) : 0.f;
+    for (int v = 0; v < V; ++v) inv[v] = inv[v] == 0.f ? 0.f : rcp(inv[v]);
 }
 
 // Which of a tile's tokens take part: a bit a token, the mask's bytes asked for a
@@ -897,14 +910,14 @@ route_backward_kernel(RouteBackwardArgs p) {
                         float m = a;
                         for (int o = pw / 2; o > 0; o >>= 1)
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        a = exp1(fmaxf(a - (m == -INFINITY ? 0.f : m), -kFar));
+                        a = exp1(max_nan(a - (m == -INFINITY ? 0.f : m), -kFar));
                     }
                     float sum = a, dot = e >= 0 ? a * dw : 0.f;
                     for (int o = pw / 2; o > 0; o >>= 1) {
                         sum += __shfl_xor_sync(0xffffffffu, sum, o);
                         dot += __shfl_xor_sync(0xffffffffu, dot, o);
                     }
-                    const float inv = SIG ? rcp(sum + 1e-6f) : sum > 0.f ? rcp(sum) : 0.f;
+                    const float inv = SIG ? rcp(sum + 1e-6f) : sum == 0.f ? 0.f : rcp(sum);
                     float v = a * inv * b * (dw - dot * inv);
                     // picks of the same expert (a top-K gives none) are added in
                     // slot order by the first of them

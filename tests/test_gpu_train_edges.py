@@ -39,3 +39,54 @@ def test_wrong_ids_take_no_part_in_the_gradient(moe, E, K, bal, router):  # noqa
     _near(got, want, 64 * U * size + U * want.abs())
     if not bal:
         assert (got[5] == 0).all() and (got[T - 1] == 0).all()
+
+
+@pytest.mark.parametrize("router", ROUTERS)
+@pytest.mark.parametrize("E,K", [(8, 2), (60, 6), (256, 8), (7, 5), (1000, 3)])
+@pytest.mark.parametrize("what", ["nan", "inf"])
+def test_scores_that_are_not_finite_show(moe, E, K, what, router):  # noqa: F811
+    """A NaN (or +inf) score of a token that takes part is not passed over: the token's
+    gradient is NaN, and so are its sequence's mean probabilities and the loss.  Counts,
+    the other tokens' gradients and the other sequences' means keep their bits."""
+    T, alpha, cu = 300, 0.2, [0, 90, 200, 300]
+    g, z, idx = _scores(T, E, K, 41)
+    mask = torch.ones(T, dtype=torch.uint8)
+    mask[7] = 0
+    dw = torch.randn(T, K, generator=g)
+    spoilt = z.clone()
+    value = float(what)
+    spoilt[120, idx[120, K - 1].long()] = value  # a picked expert's
+    last = next(e for e in range(E) if e not in idx[133].tolist())
+    spoilt[133, last] = value                    # one that was not picked
+    spoilt[7, 0] = value                         # of a masked token
+    hit = torch.zeros(T, dtype=torch.bool)
+    hit[120] = hit[133] = True
+
+    clean = _balance(moe, z, idx, router, alpha, mask, cu)
+    counts, mean, loss, err = _balance(moe, spoilt, idx, router, alpha, mask, cu)
+    assert err == 0 and torch.equal(counts, clean[0])
+    assert torch.isnan(mean[1]).all() and torch.isnan(loss).all()
+    assert torch.equal(mean[[0, 2]], clean[1][[0, 2]])
+
+    for d, c in ((None, counts), (dw, counts)):
+        want = _route_backward(moe, z, idx, router, alpha, d, c, None, mask, cu).cpu()
+        got = _route_backward(moe, spoilt, idx, router, alpha, d, c, None, mask, cu).cpu()
+        assert torch.isnan(got[hit]).all()
+        assert torch.equal(got[~hit], want[~hit])
+    # without the balance loss only the picked scores are read
+    want = _route_backward(moe, z, idx, router, alpha, dw, None, None, mask, cu).cpu()
+    got = _route_backward(moe, spoilt, idx, router, alpha, dw, None, None, mask, cu).cpu()
+    assert torch.isnan(got[120][idx[120].long()]).all() and torch.isnan(got[120]).sum() == K
+    hit[133] = False
+    assert torch.equal(got[~hit], want[~hit])
+
+
+@pytest.mark.parametrize("router", ROUTERS)
+def test_not_finite_in_one_block(moe, router):  # noqa: F811
+    """The same where one block has every token."""
+    T, E, K = 20, 8, 2
+    _, z, idx = _scores(T, E, K, 42)
+    z[11, 2] = float("nan")
+    counts, mean, loss, err = _balance(moe, z, idx, router, 0.1)
+    assert err == 0 and torch.isnan(mean).all() and torch.isnan(loss).all()
+    assert counts.sum() == T * K
