@@ -404,7 +404,8 @@ moe_status moe_forward_w8a8_blocks(const moe_shape *shape, const void *x, const 
  * picks is.  Other tokens and sequences keep their values.
  *
  * token_mask [T] (bytes, may be NULL): a token with a 0 takes no part -- it is
- * not counted, and its row of d_logits is 0; its logits are not used.
+ * not counted, and its row of d_logits is 0, whatever *d_loss holds; its logits
+ * are not used.
  * seq_offsets [n_seq + 1] (int32, ascending, within [0, T]): sequence g is the
  * tokens [seq_offsets[g], seq_offsets[g + 1]), possibly none; tokens before the
  * first or after the last are as masked.  NULL stands for one sequence of all

@@ -860,6 +860,10 @@ route_backward_kernel(RouteBackwardArgs p) {
                             z[v][j] = mul2(z[v][j], fma2(c[j], both(inv[v]), sub));
                             if constexpr (SIG) z[v][j] = mul2(z[v][j], s[v][j]);
                         }
+                        if (!live[v]) {  // 0 also where a (by d_loss) is not finite
+#pragma unroll
+                            for (int j = 0; j < L::kP; ++j) z[v][j] = both(0.f);
+                        }
                     }
                 } else {
 #pragma unroll

@@ -90,3 +90,23 @@ def test_not_finite_in_one_block(moe, router):  # noqa: F811
     counts, mean, loss, err = _balance(moe, z, idx, router, 0.1)
     assert err == 0 and torch.isnan(mean).all() and torch.isnan(loss).all()
     assert counts.sum() == T * K
+
+
+@pytest.mark.parametrize("router", ROUTERS)
+@pytest.mark.parametrize("E,K", [(8, 2), (60, 6), (256, 8), (7, 5), (1000, 3)])
+@pytest.mark.parametrize("d_loss", ["nan", "inf", "-inf"])
+def test_masked_rows_are_zero_whatever_the_loss_gradient(moe, E, K, d_loss, router):  # noqa: F811
+    """A loss scaled past fp32's range gives d_loss that is not finite: tokens that take part
+    get NaN or infinities, masked ones and those outside every sequence zeros all the same."""
+    T, cu = 300, [4, 90, 200, 290]
+    g, z, idx = _scores(T, E, K, 43)
+    mask = (torch.rand(T, generator=g) > 0.3).to(torch.uint8)
+    dead = mask == 0
+    dead[:4] = dead[290:] = True
+    wild = z.clone()
+    wild[mask == 0] = float("nan")
+    counts, _, _, _ = _balance(moe, z, idx, router, 0.2, mask, cu)
+    for dw in (None, torch.randn(T, K, generator=g)):
+        got = _route_backward(moe, wild, idx, router, 0.2, dw, counts, float(d_loss), mask, cu).cpu()
+        assert (got[dead] == 0).all()
+        assert not torch.isfinite(got[~dead]).all(1).any()
