@@ -328,6 +328,12 @@ def _seqs(seq_offsets):
     return _arg(seq_offsets, "seq_offsets", torch.int32, n), n - 1
 
 
+def _mask(token_mask, T):
+    """token_mask: a byte a token, or truth values (torch.bool, the same bytes); or None."""
+    truth = token_mask is not None and token_mask.dtype == torch.bool
+    return _arg(token_mask, "token_mask", torch.bool if truth else torch.uint8, T, True)
+
+
 def _rng(rng):
     """rng {seed, offset}: an int64 (or uint64) device tensor; None where nothing is drawn."""
     if rng is None:
@@ -356,7 +362,7 @@ def moe_balance_loss(shape, logits, topk_idx, token_mask, seq_offsets, alpha, co
     _check(_lib.moe_balance_loss(
         ctypes.byref(shape), _arg(logits, "logits", torch.float32, T * E),
         _arg(topk_idx, "topk_idx", torch.int32, T * K),
-        _arg(token_mask, "token_mask", torch.uint8, T, True), seqs, n, alpha,
+        _mask(token_mask, T), seqs, n, alpha,
         _arg(counts, "counts", torch.int32, n * E),
         _arg(mean_probs, "mean_probs", torch.float32, n * E),
         _arg(loss, "loss", torch.float32, 1), ws, nws, _stream(stream)), "moe_balance_loss")
@@ -372,7 +378,7 @@ def moe_route_backward(shape, logits, topk_idx, d_topk_w, token_mask, seq_offset
         ctypes.byref(shape), _arg(logits, "logits", torch.float32, T * E),
         _arg(topk_idx, "topk_idx", torch.int32, T * K, True),
         _arg(d_topk_w, "d_topk_w", torch.float32, T * K, True),
-        _arg(token_mask, "token_mask", torch.uint8, T, True), seqs, n, alpha,
+        _mask(token_mask, T), seqs, n, alpha,
         _arg(counts, "counts", torch.int32, n * E, True),
         _arg(d_loss, "d_loss", torch.float32, 1, True),
         _arg(d_logits, "d_logits", torch.float32, T * E), _stream(stream)), "moe_route_backward")

@@ -110,3 +110,19 @@ def test_masked_rows_are_zero_whatever_the_loss_gradient(moe, E, K, d_loss, rout
         got = _route_backward(moe, wild, idx, router, 0.2, dw, counts, float(d_loss), mask, cu).cpu()
         assert (got[dead] == 0).all()
         assert not torch.isfinite(got[~dead]).all(1).any()
+
+
+@pytest.mark.parametrize("router", ROUTERS)
+def test_masks_of_truth_values(moe, router):  # noqa: F811
+    """token_mask as a comparison gives it (torch.bool) is the same mask as in bytes."""
+    T, E, K = 200, 16, 3
+    g, z, idx = _scores(T, E, K, 51)
+    keep = torch.rand(T, generator=g) > 0.3
+    dw = torch.randn(T, K, generator=g)
+    a = _balance(moe, z, idx, router, 0.1, keep.to(torch.uint8))
+    b = _balance(moe, z, idx, router, 0.1, keep)
+    assert all(torch.equal(x, y) for x, y in zip(a[:3], b[:3]))
+    assert torch.equal(_route_backward(moe, z, idx, router, 0.1, dw, a[0], None, keep.to(torch.uint8)),
+                       _route_backward(moe, z, idx, router, 0.1, dw, a[0], None, keep))
+    with pytest.raises(ValueError, match="token_mask must be"):
+        _balance(moe, z, idx, router, 0.1, keep.int())
