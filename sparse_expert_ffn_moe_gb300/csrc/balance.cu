@@ -90,7 +90,8 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 
 // e^x of two values whose exponentials stay finite (and |x| < 2e38).  t = x
 // log2(e) is rounded for the hardware's 2^t; what that took off, d = x - t ln 2
-// (ln 2 in two parts), comes back as a factor e^d = 1 + d, so the error stays at
+// (ln 2 in two parts: Cody and Waite, "Software Manual for the Elementary Functions",
+// 1980), comes back as a factor e^d = 1 + d, so the error stays at
 // the hardware's two steps for large |x| too.  Below -87.3 it is 0.
 __device__ __forceinline__ f2 exp2x(f2 x) {
     const f2 nt = mul2(x, both(-1.44269504f));  // -t
@@ -979,7 +980,11 @@ cudaError_t with_layout(int E, F&& f) {
 // wave is the dearest part of a small kernel; a third block an SM means 80 registers
 // a thread, which spill in the backward pass (E = 256, 131072 tokens: 52 us with two
 // blocks, 55 us with three; 16384 tokens: 12 us and 16 us), and three tiles a warp in
-// place of two gain nothing (52 us).
+// place of two gain nothing (52 us).  Above 512 experts the gradient's kernels spill at
+// two blocks too, the sigmoid router's 330 to 390 bytes (E = 1024, 32768 tokens: 67 us,
+// softmax with 80 to 112 bytes 50 us).
+// The SMs are a constant, not the device's: the workspace query needs no device, and the
+// order of the sums does not depend on the part of a GPU that a process sees.
 constexpr int64_t kWave = 152 * 2;
 
 // Tokens of a block of the forward pass: its share of one wave, in whole steps of

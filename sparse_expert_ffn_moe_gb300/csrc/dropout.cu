@@ -209,7 +209,8 @@ combine_dropout_kernel(const T* y_perm, const int32_t* __restrict__ inv_perm,
 // The K dot products are summed in a fixed order: a thread's elements, lanes,
 // warps.  Bound by HBM: T = 16384, d = 7168, K = 8 bf16 takes 615 us for 4.23 GB
 // (6.88 TB/s, the measured copy's rate); four groups a thread without the
-// look-ahead took 774 us, one row at a time 698 us.
+// look-ahead took 774 us, one row at a time 698 us.  (Four groups a thread, K <= 2, spill 64
+// bytes at the 64 registers that the bound of 1024 threads leaves.)
 template <typename T, int V, int KB>
 __global__ void __launch_bounds__(V == 1 ? 256 : 1024)
 combine_backward_kernel(const T* d_y, const T* y_perm, const int32_t* __restrict__ inv_perm,
@@ -346,8 +347,8 @@ cudaError_t combine_backward_v(const moe_shape& s, const void* d_y, const void* 
 
 // What a thread holds: in bf16 two rows of two groups each where a token has more
 // than two rows, else four groups of one row (K = 2, T = 4096, d = 4096: 28 us, two
-// groups 32 us; K = 1: 36 and 47 us); in fp32 two groups of one row (two rows spill:
-// 300 us against 198 us).  A row of at most 32 groups has one a thread, and two rows
+// groups 32 us; K = 1: 36 and 47 us); in fp32 two groups of one row (two rows spill
+// 292 bytes: T = 8192, d = 4096, K = 4 with d_shared 290 us against 201 us).  A row of at most 32 groups has one a thread, and two rows
 // (d = 256, K = 4: 28 us against 33 us with one).
 template <typename T, typename... Args>
 cudaError_t combine_backward_t(const moe_shape& s, Args... args) {
