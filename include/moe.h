@@ -509,6 +509,50 @@ moe_status moe_combine_backward(const moe_shape *shape, const void *d_y,
                                 void *stream);
 
 /*
+ * ---- the norm in front of the experts ----------------------------------------
+ * Root-mean-square norm of `rows` rows of `cols` elements (dtype MOE_F32 or
+ * MOE_BF16), with the residual's addition:
+ *   s      = x + residual (fp32 sum, rounded to dtype: the row as the residual
+ *            stream holds it; x itself without a residual)
+ *   r      = 1 / sqrt(mean of s^2 + eps)                      (fp32)
+ *   y      = s * r * weight                                   (fp32, rounded once)
+ *   scales = max|y| / 448 of the row before its rounding (1 for a row of zeros),
+ *   codes  = E4M3 nearest to y / scale -- the row format of the W8A8 calls
+ * weight [cols] has the rows' dtype.  residual, s, y and codes may be NULL, not
+ * both y and codes; codes and scales [rows] (fp32) go together.  s may be x or
+ * residual itself, and y may be x; other overlaps are not allowed.  All
+ * pointers 16-byte aligned.  The squares are summed in fp32: rows whose mean
+ * square plus eps is a normal fp32 number.  eps is finite and not negative.
+ * A row with a NaN or an infinity spoils no other row.
+ * Limits: rows < 2^31, 1 <= cols <= 16384 (any width; multiples of 16 bytes are
+ * fastest).  rows == 0 is a no-op.  No workspace.
+ */
+moe_status moe_rmsnorm(int64_t rows, int64_t cols, int32_t dtype, const void *x,
+                       const void *residual, const void *weight, float eps, void *s,
+                       void *y, uint8_t *codes, float *scales, void *stream);
+
+/* Bytes of workspace for moe_rmsnorm_backward; 0 for sizes outside the limits. */
+size_t moe_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Backward pass of moe_rmsnorm from y's gradient d_y, on the rows s that the
+ * forward pass normalised (its s, or x where it had no residual):
+ *   g = d_y * weight,  h = s * r
+ *   d_x      = d_s + r * (g - h * mean(g * h))     rounded once to dtype
+ *   d_weight = sum over the rows of d_y * h        [cols] fp32
+ * d_s (may be NULL) is the gradient that reaches s by the residual stream; d_x
+ * is then the gradient of x and of the residual alike.  d_x or d_weight may be
+ * NULL, not both; the workspace is needed for d_weight alone.  d_x may be d_y,
+ * d_s or s itself.  Sums go in a fixed order (no atomics): the same bits on
+ * every run.  Limits and alignment as in moe_rmsnorm; with rows == 0 d_weight
+ * is zeroed.
+ */
+moe_status moe_rmsnorm_backward(int64_t rows, int64_t cols, int32_t dtype, const void *d_y,
+                                const void *s, const void *weight, float eps,
+                                const void *d_s, void *d_x, float *d_weight,
+                                void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * Reads the device error word of `workspace` (a device pointer passed to a
  * previous call) into *code_out (a HOST pointer): MOE_OK, MOE_ERR_TIMEOUT or
  * MOE_ERR_BOUNDS.  Synchronous (one 16-byte device-to-host copy of the error

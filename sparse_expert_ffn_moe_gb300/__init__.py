@@ -29,6 +29,7 @@ EXPORTED = ("moe_status_string", "moe_workspace_bytes", "moe_route", "moe_permut
             "moe_expert_ffn_w8a8", "moe_forward_w8a8", "moe_expert_ffn_w8a8_blocks",
             "moe_forward_w8a8_blocks", "moe_balance_workspace_bytes", "moe_balance_loss",
             "moe_route_backward", "moe_dropout", "moe_combine_dropout", "moe_combine_backward",
+            "moe_rmsnorm", "moe_rmsnorm_workspace_bytes", "moe_rmsnorm_backward",
             "moe_get_device_error")
 FP8_BLOCK = 128  # side of the square weight-scale blocks of the *_fp8_blocks calls
 
@@ -91,13 +92,19 @@ def _load_lib() -> ctypes.CDLL:
     lib.moe_dropout.argtypes = [ctypes.c_int64, i32, vp, vp, f64, vp, vp, vp]
     lib.moe_combine_dropout.argtypes = [sp, vp, vp, vp, vp, vp, f64, vp, vp, vp]
     lib.moe_combine_backward.argtypes = [sp, vp, vp, vp, vp, f64, vp, vp, vp, vp, vp]
+    i64 = ctypes.c_int64
+    lib.moe_rmsnorm.argtypes = [i64, i64, i32, vp, vp, vp, f32, vp, vp, vp, vp, vp]
+    lib.moe_rmsnorm_workspace_bytes.argtypes = [i64, i64]
+    lib.moe_rmsnorm_workspace_bytes.restype = sz
+    lib.moe_rmsnorm_backward.argtypes = [i64, i64, i32, vp, vp, vp, f32, vp, vp, vp, vp, sz, vp]
     lib.moe_get_device_error.argtypes = [vp, ctypes.POINTER(i32)]
     for f in ("moe_route", "moe_permute", "moe_permute_noalloc", "moe_expert_ffn", "moe_combine",
               "moe_forward", "moe_quantize_fp8_rows", "moe_expert_ffn_fp8", "moe_forward_fp8",
               "moe_quantize_fp8_blocks", "moe_expert_ffn_fp8_blocks", "moe_forward_fp8_blocks",
               "moe_expert_ffn_w8a8", "moe_forward_w8a8", "moe_expert_ffn_w8a8_blocks",
               "moe_forward_w8a8_blocks", "moe_balance_loss", "moe_route_backward", "moe_dropout",
-              "moe_combine_dropout", "moe_combine_backward", "moe_get_device_error"):
+              "moe_combine_dropout", "moe_combine_backward", "moe_rmsnorm", "moe_rmsnorm_backward",
+              "moe_get_device_error"):
         getattr(lib, f).restype = i32
     return lib
 
@@ -420,6 +427,53 @@ def moe_combine_backward(shape, d_y, y_perm, inv_perm, topk_w, p, rng, d_y_perm,
         _arg(d_y_perm, "d_y_perm", dt, n * shape.d, True),
         _arg(d_topk_w, "d_topk_w", torch.float32, n, True),
         _arg(d_shared, "d_shared", dt, row, True), _stream(stream)), "moe_combine_backward")
+
+
+def _norm_dtype(x, name: str):
+    dtype = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}.get(x.dtype)
+    if dtype is None:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, not {x.dtype}")
+    return dtype
+
+
+def moe_rmsnorm(x, residual, weight, eps, s, y, codes, scales, stream=None):
+    """RMS norm of the rows of x (bf16 or fp32, the last dimension) after the residual's
+    addition: the sum s, the normalised rows y, and y as E4M3 codes (uint8, x's shape)
+    with a scale a row (fp32); residual, s, y and (codes, scales) may each be None."""
+    dtype = _norm_dtype(x, "x")
+    t, n, cols = x.dtype, x.numel(), x.shape[-1]
+    rows = n // cols if cols else 0
+    _check(_lib.moe_rmsnorm(
+        rows, cols, dtype, _arg(x, "x", t, n), _arg(residual, "residual", t, n, True),
+        _arg(weight, "weight", t, cols), eps, _arg(s, "s", t, n, True), _arg(y, "y", t, n, True),
+        _arg(codes, "codes", torch.uint8, n, True),
+        _arg(scales, "scales", torch.float32, rows, True), _stream(stream)), "moe_rmsnorm")
+
+
+def moe_rmsnorm_workspace_bytes(rows: int, cols: int) -> int:
+    return int(_lib.moe_rmsnorm_workspace_bytes(rows, cols))
+
+
+def alloc_rmsnorm_workspace(rows: int, cols: int, device=None) -> torch.Tensor:
+    n = moe_rmsnorm_workspace_bytes(rows, cols)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_rmsnorm_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def moe_rmsnorm_backward(d_y, s, weight, eps, d_s, d_x, d_weight, workspace, stream=None):
+    """Gradients of moe_rmsnorm from y's gradient d_y, on the rows s that it normalised:
+    d_x (with d_s, the residual stream's own gradient, added; or None) and d_weight
+    (fp32, or None; it alone needs the workspace)."""
+    dtype = _norm_dtype(s, "s")
+    t, n, cols = s.dtype, s.numel(), s.shape[-1]
+    rows = n // cols if cols else 0
+    ws, nws = _ws(workspace)
+    _check(_lib.moe_rmsnorm_backward(
+        rows, cols, dtype, _arg(d_y, "d_y", t, n), _arg(s, "s", t, n),
+        _arg(weight, "weight", t, cols), eps, _arg(d_s, "d_s", t, n, True),
+        _arg(d_x, "d_x", t, n, True), _arg(d_weight, "d_weight", torch.float32, cols, True),
+        ws, nws, _stream(stream)), "moe_rmsnorm_backward")
 
 
 def moe_get_device_error(workspace) -> int:

@@ -284,6 +284,24 @@ cudaError_t launch_route_backward(const moe_shape& s, RouteBackwardArgs a, cudaS
 
 int device_sm_count();
 
+// norm.cu: RMS norm (x, residual -> s, y, codes and scales) and its backward pass
+// (d_y, x = s, d_s -> d_x, d_weight by way of part [rmsnorm_backward_blocks][d])
+struct NormArgs {
+    int64_t rows;
+    int d, dtype;
+    float eps;
+    const void *x, *residual, *weight;
+    void *s, *y;
+    uint8_t* codes;
+    float* scales;
+    const void *d_y, *d_s;
+    void* d_x;
+    float *d_weight, *part;
+};
+cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t st);
+int rmsnorm_backward_blocks(int64_t rows, int d);
+cudaError_t launch_rmsnorm_backward(const NormArgs& a, cudaStream_t st);
+
 // Launches with programmatic stream serialisation (MOE_PDL=0 turns it off, read
 // per call): the kernel may start while the previous kernel of the stream
 // finishes, and orders itself with pdl_wait().
