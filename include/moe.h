@@ -509,6 +509,41 @@ moe_status moe_combine_backward(const moe_shape *shape, const void *d_y,
                                 void *stream);
 
 /*
+ * ---- the layer for a few tokens ------------------------------------------------
+ * moe_forward for T <= 16 tokens in two launches, with the residual stream:
+ *   y = residual + SharedExpert(x) + sum_j w_j Expert_{i_j}(x)     (fp32, rounded once)
+ * The first launch scores, the second chooses the experts, streams every picked
+ * expert's weights once and joins.  Arguments, router rules and layouts are those
+ * of moe_forward, moe_forward_fp8 and moe_forward_fp8_blocks; shape->dtype must be
+ * MOE_BF16 (and d, inter, inter_shared multiples of 128 for 8-bit weights), T at
+ * most 16, else MOE_ERR_UNSUPPORTED.  residual [T][d] may be NULL; y may be the
+ * residual itself, not x.  The intermediates are finer than moe_forward's: sums,
+ * expert outputs and the combine stay in fp32, h is read as planes of 16 (bf16
+ * weights) or 12 bits (8-bit weights), x exactly -- with 8-bit weights down to
+ * 2^-23 of the token's largest value.
+ * The same bits on every run.  No call waits for a part of the grid that is not
+ * running, so calls on several streams (each with its own workspace) may overlap.
+ * A token whose row is not finite spoils no other token.  Graph capturable.
+ * Workspace: moe_few_workspace_bytes (0 for an invalid shape or T > 16); its error
+ * word is cleared first, a wait that ran out is recorded there (MOE_ERR_TIMEOUT).
+ */
+size_t moe_few_workspace_bytes(const moe_shape *shape);
+
+moe_status moe_forward_few(const moe_shape *shape, const void *x, const void *w_g,
+                           const float *bias, const void *w_gate, const void *w_up,
+                           const void *w_down, const void *ws_gate, const void *ws_up,
+                           const void *ws_down, const void *residual, void *y,
+                           void *workspace, size_t ws_bytes, void *stream);
+moe_status moe_forward_few_fp8(const moe_shape *shape, const void *x, const void *w_g,
+                               const float *bias, const moe_fp8_experts *w,
+                               const void *residual, void *y, void *workspace,
+                               size_t ws_bytes, void *stream);
+moe_status moe_forward_few_fp8_blocks(const moe_shape *shape, const void *x, const void *w_g,
+                                      const float *bias, const moe_fp8_experts *w,
+                                      const void *residual, void *y, void *workspace,
+                                      size_t ws_bytes, void *stream);
+
+/*
  * ---- the norm in front of the experts ----------------------------------------
  * Root-mean-square norm of `rows` rows of `cols` elements (dtype MOE_F32 or
  * MOE_BF16), with the residual's addition:

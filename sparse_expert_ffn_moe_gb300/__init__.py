@@ -29,6 +29,8 @@ EXPORTED = ("moe_status_string", "moe_workspace_bytes", "moe_route", "moe_permut
             "moe_expert_ffn_w8a8", "moe_forward_w8a8", "moe_expert_ffn_w8a8_blocks",
             "moe_forward_w8a8_blocks", "moe_balance_workspace_bytes", "moe_balance_loss",
             "moe_route_backward", "moe_dropout", "moe_combine_dropout", "moe_combine_backward",
+            "moe_few_workspace_bytes", "moe_forward_few", "moe_forward_few_fp8",
+            "moe_forward_few_fp8_blocks",
             "moe_rmsnorm", "moe_rmsnorm_workspace_bytes", "moe_rmsnorm_backward",
             "moe_get_device_error")
 FP8_BLOCK = 128  # side of the square weight-scale blocks of the *_fp8_blocks calls
@@ -92,6 +94,11 @@ def _load_lib() -> ctypes.CDLL:
     lib.moe_dropout.argtypes = [ctypes.c_int64, i32, vp, vp, f64, vp, vp, vp]
     lib.moe_combine_dropout.argtypes = [sp, vp, vp, vp, vp, vp, f64, vp, vp, vp]
     lib.moe_combine_backward.argtypes = [sp, vp, vp, vp, vp, f64, vp, vp, vp, vp, vp]
+    lib.moe_few_workspace_bytes.argtypes = [sp]
+    lib.moe_few_workspace_bytes.restype = sz
+    lib.moe_forward_few.argtypes = [sp] + [vp] * 12 + [sz, vp]
+    lib.moe_forward_few_fp8.argtypes = [sp, vp, vp, vp, fp, vp, vp, vp, sz, vp]
+    lib.moe_forward_few_fp8_blocks.argtypes = lib.moe_forward_few_fp8.argtypes
     i64 = ctypes.c_int64
     lib.moe_rmsnorm.argtypes = [i64, i64, i32, vp, vp, vp, f32, vp, vp, vp, vp, vp]
     lib.moe_rmsnorm_workspace_bytes.argtypes = [i64, i64]
@@ -103,7 +110,8 @@ def _load_lib() -> ctypes.CDLL:
               "moe_quantize_fp8_blocks", "moe_expert_ffn_fp8_blocks", "moe_forward_fp8_blocks",
               "moe_expert_ffn_w8a8", "moe_forward_w8a8", "moe_expert_ffn_w8a8_blocks",
               "moe_forward_w8a8_blocks", "moe_balance_loss", "moe_route_backward", "moe_dropout",
-              "moe_combine_dropout", "moe_combine_backward", "moe_rmsnorm", "moe_rmsnorm_backward",
+              "moe_combine_dropout", "moe_combine_backward", "moe_forward_few",
+              "moe_forward_few_fp8", "moe_forward_few_fp8_blocks", "moe_rmsnorm", "moe_rmsnorm_backward",
               "moe_get_device_error"):
         getattr(lib, f).restype = i32
     return lib
@@ -427,6 +435,56 @@ def moe_combine_backward(shape, d_y, y_perm, inv_perm, topk_w, p, rng, d_y_perm,
         _arg(d_y_perm, "d_y_perm", dt, n * shape.d, True),
         _arg(d_topk_w, "d_topk_w", torch.float32, n, True),
         _arg(d_shared, "d_shared", dt, row, True), _stream(stream)), "moe_combine_backward")
+
+
+def moe_few_workspace_bytes(shape: moe_shape) -> int:
+    return int(_lib.moe_few_workspace_bytes(ctypes.byref(shape)))
+
+
+def alloc_few_workspace(shape: moe_shape, device=None) -> torch.Tensor:
+    n = moe_few_workspace_bytes(shape)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_few_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def moe_forward_few(shape, x, w_g, bias, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, residual,
+                    y, workspace, stream=None):
+    """moe_forward for at most 16 tokens in two launches, y = residual + layer(x) (residual or
+    None); bf16 weights, workspace from alloc_few_workspace."""
+    s, bf = shape, torch.bfloat16
+    ws, nws = _ws(workspace)
+    one, sh = s.E * s.inter * s.d, s.inter_shared * s.d
+    _check(_lib.moe_forward_few(
+        ctypes.byref(s), _arg(x, "x", bf, s.T * s.d), _arg(w_g, "w_g", bf, s.E * s.d),
+        _arg(bias, "bias", torch.float32, s.E, True), _arg(w_gate, "w_gate", bf, one),
+        _arg(w_up, "w_up", bf, one), _arg(w_down, "w_down", bf, one),
+        _arg(ws_gate, "ws_gate", bf, sh, True), _arg(ws_up, "ws_up", bf, sh, True),
+        _arg(ws_down, "ws_down", bf, sh, True), _arg(residual, "residual", bf, s.T * s.d, True),
+        _arg(y, "y", bf, s.T * s.d), ws, nws, _stream(stream)), "moe_forward_few")
+
+
+def _few_fp8(call, name, s, x, w_g, bias, w, residual, y, workspace, stream):
+    bf = torch.bfloat16
+    ws, nws = _ws(workspace)
+    _check(call(ctypes.byref(s), _arg(x, "x", bf, s.T * s.d), _arg(w_g, "w_g", bf, s.E * s.d),
+                _arg(bias, "bias", torch.float32, s.E, True), ctypes.byref(w),
+                _arg(residual, "residual", bf, s.T * s.d, True), _arg(y, "y", bf, s.T * s.d), ws,
+                nws, _stream(stream)), name)
+
+
+def moe_forward_few_fp8(shape, x, w_g, bias, w: moe_fp8_experts, residual, y, workspace,
+                        stream=None):
+    """moe_forward_fp8 for at most 16 tokens in two launches, y = residual + layer(x)."""
+    _few_fp8(_lib.moe_forward_few_fp8, "moe_forward_few_fp8", shape, x, w_g, bias, w, residual, y,
+             workspace, stream)
+
+
+def moe_forward_few_fp8_blocks(shape, x, w_g, bias, w: moe_fp8_experts, residual, y, workspace,
+                               stream=None):
+    """moe_forward_fp8_blocks for at most 16 tokens in two launches, y = residual + layer(x)."""
+    _few_fp8(_lib.moe_forward_few_fp8_blocks, "moe_forward_few_fp8_blocks", shape, x, w_g, bias, w,
+             residual, y, workspace, stream)
 
 
 def _norm_dtype(x, name: str):

@@ -1596,6 +1596,10 @@ bool tc_available() {
     return major == 10 && minor == 3 && encode_fn() != nullptr;
 }
 
+void* tensor_map_encoder() { return (void*)encode_fn(); }
+unsigned long long tc_timeout_ns() { return timeout_ns(); }
+int tc_test_stall() { return test_stall(); }
+
 int tc_tile_rows(bool pair) { return pair ? Shape<true>::kTileRows : Shape<false>::kTileRows; }
 
 // Read on every call: MOE_GATHER_MAX_ROWS (0 disables the in-GEMM gather;

@@ -302,6 +302,30 @@ cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t st);
 int rmsnorm_backward_blocks(int64_t rows, int d);
 cudaError_t launch_rmsnorm_backward(const NormArgs& a, cudaStream_t st);
 
+// few.cu: the whole layer for at most kFewMaxTokens tokens
+constexpr int kFewMaxTokens = 16;
+struct FewWs {
+    int splits, max_parts, counters;
+    size_t claim, part, xq, xs, gpart, h, h_s, hs, hs_s, yp, total;
+};
+FewWs few_ws(const moe_shape& s, int fmt);
+struct FewCall {
+    const void *x, *w_g, *residual;
+    const float* bias;
+    const void *w_gate, *w_up, *w_down, *ws_gate, *ws_up, *ws_down;
+    const float *s_gate, *s_up, *s_down, *ss_gate, *ss_up, *ss_down;
+    void* y;
+};
+// fmt 0: bf16 weights; 1, 2: E4M3 with a scale a row, per 128 x 128 block
+cudaError_t launch_few(const moe_shape& s, int fmt, const FewCall& c, void* workspace,
+                       cudaStream_t st);
+
+// ffn_tc.cu: the driver's tensor-map encoder (NULL if it cannot be found), the bound on
+// device waits and the switch of the tests that makes one run out
+void* tensor_map_encoder();
+unsigned long long tc_timeout_ns();
+int tc_test_stall();
+
 // Launches with programmatic stream serialisation (MOE_PDL=0 turns it off, read
 // per call): the kernel may start while the previous kernel of the stream
 // finishes, and orders itself with pdl_wait().
