@@ -22,7 +22,8 @@
 // In a block, roles pass work through shared memory as the tensor-core GEMM's do:
 // warp 0 takes units and streams weight tiles (TMA, 128-byte swizzle), warp 1 the
 // rows that multiply them, warp 2 issues tcgen05 products with the weights as the
-// 128-row operand and the tokens as its few columns, warps 4-7 empty the accumulators.
+// 128-row operand and the tokens as its few columns, warps 4-7 empty the accumulators,
+// warps 8-11 count finished parts and join them.
 // Warp 0 runs ahead by the ring's depth (160 KB and more an SM) without waiting for h,
 // so the weights of the next part are on their way while h is still being finished.
 //
@@ -56,31 +57,34 @@ constexpr int kMaxSlots = kMaxT * 32;      // T * K
 constexpr int kMaxGroups = kMaxSlots + 1;  // and the shared expert
 constexpr int kScoreWarps = 8;
 constexpr int kScoreSplits = 8;
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
 constexpr int kBufs = 4;       // accumulator buffers of 128 tensor-memory columns
-constexpr int kQueue = 4;      // units between the roles
-constexpr int kMaxUnit = 32;   // most stages of a unit
-constexpr int kABytes = 32768; // weights of a stage: two tiles of 128 rows x 128 bytes
-constexpr uint32_t kAcc1 = 64; // columns from a buffer's first accumulator to its second
+constexpr int kQueue = 8;      // units between the roles
+constexpr int kABytes = 32768; // weights of a stage
+constexpr int kBBytes = 16384; // the rows beside them
+constexpr int kStage = kABytes + kBBytes;
+constexpr int kStages = 4;
 
 // FMT: 0 bf16 weights, 1 E4M3 with a scale a row, 2 E4M3 with a scale per 128 x 128 block.
 // NT: columns that tokens take (8 or 16).
 template <int FMT, int NT>
 struct Cfg {
-    static constexpr int kElems = FMT ? 128 : 64;    // K of a tile: 128 bytes
-    static constexpr int kHPlanes = FMT ? 3 : 2;     // of h
-    static constexpr int kHCols = FMT ? 4 : 2;       // the same as columns (a multiple of 16 in all)
-    static constexpr int kHTile = kHCols * NT * 128; // bytes of h beside one weight tile
-    static constexpr int kXBytes = FMT ? 2 * NT * 128 : 16 * 128;
-    static constexpr int kStage = kABytes + 2 * kHTile;
-    static constexpr int kStages = kStage > 45000 ? 4 : 5;
+    static constexpr int kElems = FMT ? 128 : 64;  // K of a tile: 128 bytes
+    static constexpr int kHPlanes = FMT ? 3 : 2;   // of h
+    // Columns of a product: whole 16s.  Those past the planes multiply whatever follows them
+    // in shared memory and are not read.
+    static constexpr int kXCols = FMT ? 2 * NT : 16, kHCols = FMT ? 4 : 2;
+    static constexpr int kXTile = kXCols * 128;    // bytes beside one weight tile
 };
 
-enum { kMapGate, kMapUp, kMapDown, kMapSGate, kMapSUp, kMapSDown, kMapX, kMapH, kMapHS, kMaps };
+enum { kMapGate, kMapUp, kMapDown, kMapSGate, kMapSUp, kMapSDown, kMapX, kMapH8, kMapHS8, kMapH16,
+       kMapHS16, kMaps };
 
 struct FewArgs {
     CUtensorMap maps[kMaps];
-    int T, d, E, K, I, Is, sigmoid, splits, max_parts, test_stall;
+    int T, d, E, K, I, Is, sigmoid, splits, test_stall;
+    int rg, rd;  // rows of a gate/up unit (of each of the two) and of a down unit
+    int qg, qd;  // K tiles of a stage
     unsigned long long timeout_ns;
     const float* bias;
     const bf16* residual;
@@ -93,99 +97,61 @@ struct FewArgs {
 };
 
 struct Ctl {
-    uint64_t full[5], empty[5], tfull[kBufs], tempty[kBufs], qfull[kQueue], qempty[kQueue];
+    uint64_t full[kStages], empty[kStages], tfull[kBufs], tempty[kBufs];
+    uint64_t qfull[kQueue], qempty[kQueue], summed[kQueue];
     uint32_t tmem;
     int abort_flag;
     int queue[kQueue];
     int last;
     int groups;                   // with the shared expert
     uint32_t present[32];         // experts that a token picked
-    uint16_t before[33];          // how many of them before a word of `present`
     uint16_t expert[kMaxGroups];  // of a group
     alignas(4) uint16_t mask[kMaxGroups + 1];  // tokens of a group (set by 32-bit atomics)
     uint16_t row0[kMaxGroups + 1];
     uint16_t pick[kMaxSlots];     // expert, then row, of a slot
     float weight[kMaxSlots];
+    float xs[kMaxT];              // scales of x
     float top[4][kMaxT];
-    float hscale[2 * kMaxUnit * kMaxT];
-    float wscale[2][2 * kMaxUnit];
-    alignas(16) float strand[4][128];  // read and written as float4
+    float hscale[2][4 * kMaxT];   // of a stage of h: [K tile][token], two in turn
+    alignas(16) float strand[512];  // read and written as float4
 };
 
 struct Unit {
-    int down, group, tile, part, s0, ns;
+    int down, group, tile, n;  // n: K tiles
 };
 
-// Cut of the work into units, the same in every block: a function of the sizes and of the
-// number of groups.
+// The work as units, the same in every block.
 struct Sched {
-    int nk, nks, nkr;          // stages over K: gate/up, shared and routed down
-    int tiles_s, tiles_r, tiles_d;
-    int gp, gc, dps, dcs, dpr, dcr;  // parts of a tile and stages of a part
-    int u1, u2, u3, u4;        // ends of: shared gate/up, routed, shared down, routed down
+    int nk, nks, nkr;   // K tiles: gate/up, shared and routed down
+    int gs, gr, td;     // units of a group: shared and routed gate/up, down
+    int u1, u2, u3, u4; // ends of: shared gate/up, routed, shared down, routed down
 };
 
-__device__ __forceinline__ void cut(int n, int want, int most, int& parts, int& stages) {
-    parts = min(most, (n + want - 1) / want);
-    stages = (n + parts - 1) / parts;
-    parts = (n + stages - 1) / stages;
-}
-
-__device__ Sched make_sched(const FewArgs& a, int groups, int elems, int blocks) {
+__device__ __forceinline__ Sched make_sched(const FewArgs& a, int groups, int elems) {
     Sched s;
     const int shared = a.Is > 0, routed = groups - shared;
-    const auto up = [](int n, int d) { return (n + d - 1) / d; };
-    s.nk = up(a.d, elems);
-    s.nks = up(a.Is, 2 * elems);
-    s.nkr = up(a.I, 2 * elems);
-    s.tiles_s = up(a.Is, 128);
-    s.tiles_r = up(a.I, 128);
-    s.tiles_d = up(a.d, 128);
-    const int64_t all = (int64_t)s.nk * (s.tiles_s + routed * s.tiles_r) +
-                        (int64_t)s.tiles_d * (s.nks + (int64_t)routed * s.nkr);
-    // a block's share in about 16 units, so that the last ones end near each other
-    const int want = (int)max((int64_t)1, min((int64_t)kMaxUnit, all / (16 * (int64_t)blocks)));
-    cut(s.nk, want, a.max_parts, s.gp, s.gc);
-    cut(s.nks > 0 ? s.nks : 1, want, a.max_parts, s.dps, s.dcs);
-    cut(s.nkr, want, a.max_parts, s.dpr, s.dcr);
-    s.u1 = s.tiles_s * s.gp;
-    s.u2 = s.u1 + routed * s.tiles_r * s.gp;
-    s.u3 = s.u2 + (shared ? s.tiles_d * s.dps : 0);
-    s.u4 = s.u3 + routed * s.tiles_d * s.dpr;
+    s.nk = a.d / elems;
+    s.nks = a.Is / elems;
+    s.nkr = a.I / elems;
+    s.gs = a.Is / a.rg;
+    s.gr = a.I / a.rg;
+    s.td = (a.d + a.rd - 1) / a.rd;
+    s.u1 = s.gs;
+    s.u2 = s.u1 + routed * s.gr;
+    s.u3 = s.u2 + shared * s.td;
+    s.u4 = s.u3 + routed * s.td;
     return s;
 }
 
 __device__ __forceinline__ Unit unit_at(const Sched& s, int u, int shared) {
-    Unit t;
-    int tiles, parts, stages, n;
-    if (u < s.u1) {
-        t.down = 0; t.group = 0; tiles = s.tiles_s; parts = s.gp; stages = s.gc; n = s.nk;
-    } else if (u < s.u2) {
+    if (u < s.u1) return {0, 0, u, s.nk};
+    if (u < s.u2) {
         u -= s.u1;
-        t.down = 0; tiles = s.tiles_r; parts = s.gp; stages = s.gc; n = s.nk;
-        t.group = shared + u / (tiles * parts);
-        u %= tiles * parts;
-    } else if (u < s.u3) {
-        u -= s.u2;
-        t.down = 1; t.group = 0; tiles = s.tiles_d; parts = s.dps; stages = s.dcs; n = s.nks;
-    } else {
-        u -= s.u3;
-        t.down = 1; tiles = s.tiles_d; parts = s.dpr; stages = s.dcr; n = s.nkr;
-        t.group = shared + u / (tiles * parts);
-        u %= tiles * parts;
+        return {0, shared + u / s.gr, u % s.gr, s.nk};
     }
-    t.tile = u / parts;
-    t.part = u % parts;
-    t.s0 = t.part * stages;
-    t.ns = min(stages, n - t.s0);
-    return t;
-}
-
-// 128 down rows of a K run with an odd number of tiles: the last stage has one tile
-template <int FMT>
-__device__ __forceinline__ int tiles_of_stage(const FewArgs& a, const Unit& u, int shared, int i) {
-    const int n = (u.group < shared ? a.Is : a.I) / Cfg<FMT, 8>::kElems;
-    return min(2, n - 2 * (u.s0 + i));
+    if (u < s.u3) return {1, 0, u - s.u2, s.nks};
+    u -= s.u3;
+    return {1, shared + u / s.td, u % s.td, s.nkr};
 }
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, Ctl* ctl,
@@ -213,6 +179,14 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
     asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_t* bar, int32_t c0,
+                                            int32_t c1, int32_t c2, int32_t c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(ptx::smem_u32(dst)),
+        "l"(tmap), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int32_t c0,
                                             int32_t c1, int32_t c2) {
     asm volatile(
@@ -221,8 +195,8 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_
         "l"(tmap), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
-// barrier of the four accumulator warps
-__device__ __forceinline__ void drain_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// barrier of the four finishing warps
+__device__ __forceinline__ void finish_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
 // The least power of two s with amax / s <= 448 (to fp32 rounding), and 1 / s; 1 where
 // amax is not positive.
@@ -335,55 +309,59 @@ __device__ __forceinline__ float score_of(const FewArgs& a, int t, int e) {
     return s;
 }
 
+// A key as an integer of the same order: -0 as +0, NaN above all numbers or below them by
+// its sign, so that every pick is one of the experts and none is picked twice.
+__device__ __forceinline__ uint32_t ordered(float key) {
+    const uint32_t b = __float_as_uint(key + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
 // The whole block chooses every token's experts (the rule of moe_route: the K largest keys,
-// ties to the lower expert) and lists the groups.  `keys`: T * E floats of shared memory.
-__device__ void choose(const FewArgs& a, Ctl* ctl, float* keys) {
+// ties to the lower expert) and lists the groups.  `keys`, `scores`: T * E words each.
+__device__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* keys, float* scores) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int shared = a.Is > 0;
+    const int shared = a.Is > 0, slots = a.T * a.K;
     if (threadIdx.x < 32) ctl->present[threadIdx.x] = 0u;
     for (int i = threadIdx.x; i <= kMaxGroups; i += kThreads) ctl->mask[i] = 0;
+    for (int i = threadIdx.x; i < a.T * a.E; i += kThreads) {
+        const int e = i % a.E;
+        const float s = score_of(a, i / a.E, e), b = a.bias ? __ldg(a.bias + e) : 0.0f;
+        scores[i] = s;
+        keys[i] = ordered(a.sigmoid ? 1.0f / (1.0f + expf(-s)) + b : s + b);
+    }
     __syncthreads();
     for (int t = warp; t < a.T; t += kThreads / 32) {
-        float* key = keys + t * a.E;
-#pragma unroll 2
-        for (int e = lane; e < a.E; e += 32) {
-            const float s = score_of(a, t, e), b = a.bias ? a.bias[e] : 0.0f;
-            key[e] = a.sigmoid ? 1.0f / (1.0f + expf(-s)) + b : s + b;
-        }
-        __syncwarp();
-        uint32_t taken = 0;  // of this lane's experts lane, lane + 32, ...
-        int mine = 0;        // lane j: the j-th pick
-        float first = 0.0f, mykey = 0.0f;
+        uint32_t* key = keys + t * a.E;
+        // a lane's best among its experts lane, lane + 32, ... that are not taken (0: none;
+        // no key is 0, which would be a NaN of all ones: it is read as 1)
+        uint32_t best = 0u, taken = 0u;
+        int at = 0;
+        const auto rescan = [&]() {
+            best = 0u;
+            for (int e = lane, m = 0; e < a.E; e += 32, ++m) {
+                const uint32_t k = max(key[e], 1u);
+                if (!(taken >> m & 1u) && k > best) {
+                    best = k;
+                    at = e;
+                }
+            }
+        };
+        rescan();
+        int mine = 0;  // lane j: the j-th pick
         for (int j = 0; j < a.K; ++j) {
-            float bk = 0.0f;
-            int be = -1;
-            for (int e = lane, m = 0; e < a.E; e += 32, ++m)
-                if (!(taken >> m & 1u) && (be < 0 || key[e] > bk)) {
-                    bk = key[e];
-                    be = e;
-                }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const float k2 = __shfl_xor_sync(0xffffffffu, bk, o);
-                const int e2 = __shfl_xor_sync(0xffffffffu, be, o);
-                if (e2 >= 0 && (be < 0 || k2 > bk || (k2 == bk && e2 < be))) {
-                    bk = k2;
-                    be = e2;
-                }
+            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+            const int e = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7fffffff);
+            if (lane == j) mine = e;
+            if ((e & 31) == lane) {
+                taken |= 1u << (e >> 5);
+                rescan();
             }
-            // with NaN keys the lanes may differ: the first one's pick holds
-            be = __shfl_sync(0xffffffffu, be, 0);
-            bk = __shfl_sync(0xffffffffu, bk, 0);
-            if ((be & 31) == lane) taken |= 1u << (be >> 5);
-            if (lane == j) {
-                mine = be;
-                mykey = bk;
-            }
-            if (j == 0) first = bk;
         }
+        // weights: a / (sum + 1e-6) or softmax over the picked keys
+        const float s = scores[t * a.E + mine], b = a.bias ? __ldg(a.bias + mine) : 0.0f;
+        const float first = __shfl_sync(0xffffffffu, s + b, 0);
         float w = 0.0f;
-        if (lane < a.K)
-            w = a.sigmoid ? 1.0f / (1.0f + expf(-score_of(a, t, mine))) : expf(mykey - first);
+        if (lane < a.K) w = a.sigmoid ? 1.0f / (1.0f + expf(-s)) : expf(s + b - first);
         const float sum = warp_sum(w) + (a.sigmoid ? 1e-6f : 0.0f);
         if (lane < a.K) {
             ctl->pick[t * a.K + lane] = (uint16_t)mine;
@@ -392,109 +370,113 @@ __device__ void choose(const FewArgs& a, Ctl* ctl, float* keys) {
         }
     }
     __syncthreads();
-    if (warp == 0) {
-        int n = __popc(ctl->present[lane]);
-        const int own = n;
+    // picked experts before each 32, in every warp's lanes
+    const uint32_t word = ctl->present[lane];
+    int before = __popc(word);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, n, o);
-            if (lane >= o) n += v;
-        }
-        ctl->before[lane] = (uint16_t)(n - own);
-        if (lane == 31) ctl->groups = n + shared;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
     }
-    __syncthreads();
-    const int slots = a.T * a.K;
-    const auto group_of = [&](int e) {
-        return shared + ctl->before[e >> 5] +
-               __popc(ctl->present[e >> 5] & ((1u << (e & 31)) - 1u));
+    const int groups = shared + __shfl_sync(0xffffffffu, before, 31);
+    before -= __popc(word);
+    const auto group_of = [&](int e) {  // by whole warps
+        const int w = e >> 5;
+        return shared + __shfl_sync(0xffffffffu, before, w) +
+               __popc(__shfl_sync(0xffffffffu, word, w) & ((1u << (e & 31)) - 1u));
     };
     // masks are 16-bit halves of words: set with 32-bit atomics
     uint32_t* words = reinterpret_cast<uint32_t*>(ctl->mask);
-    for (int f = threadIdx.x; f < slots; f += kThreads) {
-        const int e = ctl->pick[f], g = group_of(e), t = f / a.K;
-        ctl->expert[g] = (uint16_t)e;
-        atomicOr(&words[g >> 1], 1u << (t + 16 * (g & 1)));
+    if (threadIdx.x == 0) {
+        ctl->groups = groups;
+        if (shared) {
+            ctl->expert[0] = 0;
+            atomicOr(&words[0], (1u << a.T) - 1u);
+        }
     }
-    if (shared && threadIdx.x == 0) {
-        ctl->expert[0] = 0;
-        atomicOr(&words[0], (1u << a.T) - 1u);
+    for (int f0 = warp * 32; f0 < slots; f0 += kThreads) {
+        const int f = f0 + lane, e = f < slots ? ctl->pick[f] : 0, g = group_of(e);
+        if (f < slots) {
+            ctl->expert[g] = (uint16_t)e;
+            atomicOr(&words[g >> 1], 1u << (f / a.K + 16 * (g & 1)));
+        }
     }
     __syncthreads();
     if (warp == 0) {
         int base = 0;
-        for (int g0 = 0; g0 < ctl->groups; g0 += 32) {
+        for (int g0 = 0; g0 < groups; g0 += 32) {
             const int g = g0 + lane;
-            const int own = g < ctl->groups ? __popc((uint32_t)ctl->mask[g]) : 0;
+            const int own = g < groups ? __popc((uint32_t)ctl->mask[g]) : 0;
             int n = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, n, o);
                 if (lane >= o) n += v;
             }
-            if (g < ctl->groups) ctl->row0[g] = (uint16_t)(base + n - own);
+            if (g < groups) ctl->row0[g] = (uint16_t)(base + n - own);
             base += __shfl_sync(0xffffffffu, n, 31);
         }
-        if (lane == 0) ctl->row0[ctl->groups] = (uint16_t)base;
     }
     __syncthreads();
-    for (int f = threadIdx.x; f < slots; f += kThreads) {
-        const int g = group_of(ctl->pick[f]), t = f / a.K;
-        ctl->pick[f] =
-            (uint16_t)(ctl->row0[g] + __popc((uint32_t)ctl->mask[g] & ((1u << t) - 1u)));
+    for (int f0 = warp * 32; f0 < slots; f0 += kThreads) {
+        const int f = f0 + lane, g = group_of(f < slots ? ctl->pick[f] : 0);
+        if (f < slots)
+            ctl->pick[f] = (uint16_t)(ctl->row0[g] + __popc((uint32_t)ctl->mask[g] &
+                                                            ((1u << (f / a.K)) - 1u)));
     }
-    __syncthreads();
+    if (a.xs && threadIdx.x < a.T) ctl->xs[threadIdx.x] = __ldcg(a.xs + threadIdx.x);
 }
 
-// y of 128 columns (tile m) from every part of every row: the shared expert first, then a
-// token's picks in their order.  The four warps take tokens, or strands of a token's rows
-// where there are fewer than four.
-__device__ void join_tile(const FewArgs& a, const Sched& sc, Ctl* ctl, int m, int warp, int lane) {
+// y of a tile of rd columns from every group's part of every row: the shared expert first,
+// then a token's picks in their order.  A set of rd / 4 threads takes a token, or a strand of
+// its rows where there are fewer tokens than sets.
+__device__ void join_tile(const FewArgs& a, Ctl* ctl, int m, int r) {
     const int shared = a.Is > 0;
-    const int c = m * 128 + lane * 4;
+    const int lanes = a.rd / 4, sets = 128 / lanes, set = r / lanes;
+    const int cl = (r % lanes) * 4, c = m * a.rd + cl;
     const bool in = c < a.d;
-    const int strands = a.T == 1 ? 4 : a.T == 2 ? 2 : 1;
-    const int ns = shared ? sc.dps : 0, n = ns + a.K * sc.dpr;
-    for (int item = warp; item < a.T * strands; item += 4) {
-        const int t = item / strands, q = item % strands;
+    int strands = 1;
+    while (2 * strands * a.T <= sets) strands *= 2;
+    const int n = shared + a.K;
+    for (int item0 = 0; item0 < a.T * strands; item0 += sets) {
+        const int item = item0 + set, t = item / strands, q = item % strands;
+        const bool on = in && item < a.T * strands;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (in) {
+        if (on) {
 #pragma unroll 8
             for (int i = q; i < n; i += strands) {
-                const bool sh = i < ns;
-                const int j = sh ? 0 : (i - ns) / sc.dpr, p = sh ? i : (i - ns) % sc.dpr;
-                const int row = sh ? t : ctl->pick[t * a.K + j];
-                const float w = sh ? 1.0f : ctl->weight[t * a.K + j];
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                    a.yp + ((int64_t)row * a.max_parts + p) * a.d + c));
+                const int j = i - shared;
+                const int row = j < 0 ? t : ctl->pick[t * a.K + j];
+                const float w = j < 0 ? 1.0f : ctl->weight[t * a.K + j];
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.yp + (int64_t)row * a.d + c));
                 s.x = fmaf(w, v.x, s.x);
                 s.y = fmaf(w, v.y, s.y);
                 s.z = fmaf(w, v.z, s.z);
                 s.w = fmaf(w, v.w, s.w);
             }
         }
-        if (strands > 1) {
-            *reinterpret_cast<float4*>(&ctl->strand[item][lane * 4]) = s;
-            drain_sync();
-            for (int k = 1; k < strands; ++k) {
-                const float4 v = *reinterpret_cast<const float4*>(
-                    &ctl->strand[(t * strands + k) & 3][lane * 4]);
-                if (q == 0) {
+        if (strands > 1) {  // then all items are in one turn
+            *reinterpret_cast<float4*>(&ctl->strand[set * a.rd + cl]) = s;
+            finish_sync();
+            if (on && q == 0)
+                for (int k = 1; k < strands; ++k) {
+                    const float4 v =
+                        *reinterpret_cast<const float4*>(&ctl->strand[(set + k) * a.rd + cl]);
                     s.x += v.x;
                     s.y += v.y;
                     s.z += v.z;
                     s.w += v.w;
                 }
-            }
         }
-        if (q != 0 || !in) continue;
+        if (!on || q != 0) continue;
         const int64_t at = (int64_t)t * a.d + c;
         if (a.residual) {
-            const uint2 r = __ldg(reinterpret_cast<const uint2*>(a.residual + at));
-            s.x += __uint_as_float(r.x << 16);
-            s.y += __uint_as_float(r.x & 0xffff0000u);
-            s.z += __uint_as_float(r.y << 16);
-            s.w += __uint_as_float(r.y & 0xffff0000u);
+            // not through the read-only path: y may be the residual itself
+            const uint2 v = *reinterpret_cast<const uint2*>(a.residual + at);
+            s.x += __uint_as_float(v.x << 16);
+            s.y += __uint_as_float(v.x & 0xffff0000u);
+            s.z += __uint_as_float(v.y << 16);
+            s.w += __uint_as_float(v.y & 0xffff0000u);
         }
         const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
         *reinterpret_cast<uint2*>(a.y + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
@@ -502,84 +484,96 @@ __device__ void join_tile(const FewArgs& a, const Sched& sc, Ctl* ctl, int m, in
     }
 }
 
-// Thread 0 of the accumulator warps counts the tile's finished parts; true in all four
-// warps for the block that finished the last one.  What every part wrote is then visible.
+// Counts a tile's finished part; true in the four warps of the block that finished the last
+// one, which then sees what every part wrote.  The block's own part was written by its sums'
+// warps, whose arrival the finishing warps waited for: one thread's fence orders all of it.
 __device__ __forceinline__ bool last_part(Ctl* ctl, int* counter, int parts, int tid) {
-    __threadfence();
-    drain_sync();
-    if (tid == 0) ctl->last = atomicAdd(counter, 1) == parts - 1;
-    drain_sync();
-    const bool last = ctl->last != 0;
-    if (last) __threadfence();
-    return last;
+    if (parts == 1) return true;
+    finish_sync();
+    if (tid == 0) {
+        int old;
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                     : "=r"(old)
+                     : "l"(counter)
+                     : "memory");
+        ctl->last = old == parts - 1;
+    }
+    finish_sync();
+    return ctl->last != 0;
 }
 
-// h of one finished gate/up tile (thread r: row r), stored as planes; then the group's
-// count of finished tiles.
+// Gate and up sums of a row: [unit of the group][gate rg, up rg]
+__device__ __forceinline__ float* gate_row(const FewArgs& a, int row, bool sh, int shared) {
+    const int64_t at = sh ? (int64_t)row * a.Is
+                          : (int64_t)(shared ? a.T : 0) * a.Is + (int64_t)(row - (shared ? a.T : 0)) * a.I;
+    return a.gpart + 2 * at;
+}
+
+// h of a finished gate/up unit (bf16) or of 128 rows of finished units (8-bit: a scale per
+// token and 128 values), stored as planes; then the group's count of finished ones.
 template <int FMT, int NT>
-__device__ __forceinline__ void store_h(const FewArgs& a, const Sched& sc, Ctl* ctl, const Unit& u,
-                                        float (&h)[NT], int r, int shared) {
+__device__ __forceinline__ void finish_h(const FewArgs& a, Ctl* ctl, const Unit& u, int r, int shared) {
     using C = Cfg<FMT, NT>;
     const bool sh = u.group < shared;
     const int I = sh ? a.Is : a.I, rows = sh ? a.T : a.T * a.K;
-    const int row0 = ctl->row0[u.group] - (sh || !shared ? 0 : a.T);
-    const uint32_t mask = ctl->mask[u.group];
-    const int i = u.tile * 128 + r;
-    uint8_t* base = (uint8_t*)(sh ? a.h_s : a.h);
+    const int grow0 = ctl->row0[u.group], row0 = grow0 - (sh || !shared ? 0 : a.T);
+    const int tokens = __popc((uint32_t)ctl->mask[u.group]);
     if constexpr (FMT == 0) {
-        int c = 0;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (!(mask >> t & 1u)) continue;
-            if (i < I) {
-                bf16* hp = reinterpret_cast<bf16*>(base) + (int64_t)(row0 + c) * I + i;
-                const bf16 hi = __float2bfloat16_rn(h[t]);
-                hp[0] = hi;
-                hp[(int64_t)rows * I] = __float2bfloat16_rn(h[t] - __bfloat162float(hi));
-            }
-            ++c;
+        // rg threads a token
+        const int i = r % a.rg;
+        bf16* base = reinterpret_cast<bf16*>(sh ? a.h_s : a.h);
+        for (int c = r / a.rg; c < tokens; c += 128 / a.rg) {
+            const float* p = gate_row(a, grow0 + c, sh, shared) + u.tile * 2 * a.rg + i;
+            const float h = silu_mul(__ldcg(p), __ldcg(p + a.rg));
+            bf16* hp = base + (int64_t)(row0 + c) * I + u.tile * a.rg + i;
+            const bf16 hi = __float2bfloat16_rn(h);
+            hp[0] = hi;
+            hp[(int64_t)rows * I] = __float2bfloat16_rn(h - __bfloat162float(hi));
         }
     } else {
-        // a scale per token and 128 values: the largest magnitude over the four warps
-        const int warp = r >> 5;
+        const int block = u.tile * a.rg / 128, i = block * 128 + r;
+        const int at = i / a.rg * 2 * a.rg + i % a.rg;
+        uint8_t* base = reinterpret_cast<uint8_t*>(sh ? a.h_s : a.h);
+        float* hs = sh ? a.hs_s : a.hs;
+        float h[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (!(mask >> t & 1u)) continue;
-            float m = fabsf(h[t]);
+        for (int c = 0; c < NT; ++c) {
+            h[c] = 0.0f;
+            if (c >= tokens) continue;
+            const float* p = gate_row(a, grow0 + c, sh, shared) + at;
+            h[c] = silu_mul(__ldcg(p), __ldcg(p + a.rg));
+        }
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            if (c >= tokens) continue;
+            float m = fabsf(h[c]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if ((r & 31) == 0) ctl->top[warp][t] = m;
+            if ((r & 31) == 0) ctl->top[r >> 5][c] = m;
         }
-        drain_sync();
-        float* hs = sh ? a.hs_s : a.hs;
-        int c = 0;
+        finish_sync();
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (!(mask >> t & 1u)) continue;
-            const float m = fmaxf(fmaxf(ctl->top[0][t], ctl->top[1][t]),
-                                  fmaxf(ctl->top[2][t], ctl->top[3][t]));
+        for (int c = 0; c < NT; ++c) {
+            if (c >= tokens) continue;
             float s, inv;
-            plane_scale(m, s, inv);
-            if (r == 0) hs[(int64_t)(row0 + c) * (I / 128) + u.tile] = s;
+            plane_scale(fmaxf(fmaxf(ctl->top[0][c], ctl->top[1][c]),
+                              fmaxf(ctl->top[2][c], ctl->top[3][c])), s, inv);
+            if (r == 0) hs[(int64_t)(row0 + c) * (I / 128) + block] = s;
             uint8_t* hp = base + (int64_t)(row0 + c) * I + i;
-            float q = h[t] * inv;
+            float q = h[c] * inv;
 #pragma unroll
             for (int p = 0; p < C::kHPlanes; ++p) {
                 const uint8_t code = to_code(q);
                 hp[(int64_t)p * rows * I] = code;
                 q = (q - of_code(code)) * 16.0f;
             }
-            ++c;
         }
     }
     // the copies that read h are of the asynchronous proxy
     fence_proxy_async_all();
-    __threadfence();
-    drain_sync();
-    if (r == 0) {
-        __threadfence();
-        atomicAdd(a.ready + u.group, 1);
-    }
+    finish_sync();
+    if (r == 0)
+        asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(a.ready + u.group) : "memory");
 }
 
 template <int FMT, int NT>
@@ -588,11 +582,11 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
     using C = Cfg<FMT, NT>;
     extern __shared__ uint8_t raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    Ctl* ctl = reinterpret_cast<Ctl*>(ring + C::kStages * C::kStage);
+    Ctl* ctl = reinterpret_cast<Ctl*>(ring + kStages * kStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int shared = a.Is > 0;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             ptx::mbar_init(&ctl->full[i], 2);
             ptx::mbar_init(&ctl->empty[i], 1);
         }
@@ -602,26 +596,30 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
         }
         for (int i = 0; i < kQueue; ++i) {
             ptx::mbar_init(&ctl->qfull[i], 1);
-            ptx::mbar_init(&ctl->qempty[i], 6);
+            ptx::mbar_init(&ctl->qempty[i], 10);
+            ptx::mbar_init(&ctl->summed[i], 4);
         }
         ctl->abort_flag = 0;
         ptx::fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == 3) {
         ptx::tmem_alloc(&ctl->tmem, 512);
         ptx::tmem_relinquish();
     }
-    if (warp == 2 && lane < 9) ptx::prefetch_tmap(&a.maps[lane]);
+    if (warp == 2 && lane < kMaps) ptx::prefetch_tmap(&a.maps[lane]);
     pdl_wait();
     pdl_trigger();
-    choose(a, ctl, reinterpret_cast<float*>(ring));
+    // thread 0's first claim: asked for here, answered while the experts are chosen
+    int claim = threadIdx.x == 0 ? atomicAdd(a.claim, 1) : 0;
+    choose(a, ctl, reinterpret_cast<uint32_t*>(ring),
+           reinterpret_cast<float*>(ring) + a.T * a.E);
     // the ring held keys: order them before the copies that overwrite them
     ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = ctl->tmem;
-    const Sched sc = make_sched(a, ctl->groups, C::kElems, gridDim.x);
+    const Sched sc = make_sched(a, ctl->groups, C::kElems);
 
     if (warp == 0) {
         // -------------------------------------------------- units and their weights
@@ -629,99 +627,99 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
             int stage = 0, slot = 0;
             uint32_t phase = 0, qphase = 0;
             bool ok = true;
-            int next = atomicAdd(a.claim, 1);
-            while (ok) {
-                const int u = next < sc.u4 ? next : -1;
-                if (!wait_bounded(&ctl->qempty[slot], qphase ^ 1u, ctl, a, 10)) break;
+            const auto post = [&](int u) {
+                if (!wait_bounded(&ctl->qempty[slot], qphase ^ 1u, ctl, a, 10)) return false;
                 ctl->queue[slot] = u;
                 ptx::mbar_arrive(&ctl->qfull[slot]);
                 if (++slot == kQueue) { slot = 0; qphase ^= 1u; }
-                if (u < 0) break;
-                next = atomicAdd(a.claim, 1);  // answered while this unit's copies go out
+                return true;
+            };
+            while (ok && claim < sc.u4) {
+                const int u = claim;
+                claim = atomicAdd(a.claim, 1);  // answered while this unit's copies go out
+                if (!post(u)) { ok = false; break; }
                 const Unit un = unit_at(sc, u, shared);
                 const bool sh = un.group < shared;
-                const int e = sh ? 0 : ctl->expert[un.group], row = un.tile * 128;
-                for (int i = 0; i < un.ns; ++i) {
+                const int e = sh ? 0 : ctl->expert[un.group];
+                const int row = un.tile * (un.down ? a.rd : a.rg), q = un.down ? a.qd : a.qg;
+                for (int k = 0; k < un.n; k += q) {
                     if (!wait_bounded(&ctl->empty[stage], phase ^ 1u, ctl, a, 11)) { ok = false; break; }
-                    uint8_t* dst = ring + stage * C::kStage;
+                    uint8_t* dst = ring + stage * kStage;
+                    uint64_t* bar = &ctl->full[stage];
                     if (!un.down) {
-                        const int k = (un.s0 + i) * C::kElems;
-                        ptx::mbar_arrive_expect_tx(&ctl->full[stage], kABytes);
-                        tma_load_3d(dst, &a.maps[sh ? kMapSGate : kMapGate], &ctl->full[stage], k, row, e);
-                        tma_load_3d(dst + kABytes / 2, &a.maps[sh ? kMapSUp : kMapUp],
-                                    &ctl->full[stage], k, row, e);
+                        // a K tile's gate rows, then its up rows
+                        const int nk = min(q, un.n - k), tile = a.rg * 128;
+                        ptx::mbar_arrive_expect_tx(bar, nk * 2 * tile);
+                        for (int i = 0; i < nk; ++i) {
+                            const int c = (k + i) * C::kElems;
+                            tma_load_3d(dst, &a.maps[sh ? kMapSGate : kMapGate], bar, c, row, e);
+                            tma_load_3d(dst + tile, &a.maps[sh ? kMapSUp : kMapUp], bar, c, row, e);
+                            dst += 2 * tile;
+                        }
                     } else {
-                        const int nt = tiles_of_stage<FMT>(a, un, shared, i);
-                        const int k = 2 * (un.s0 + i) * C::kElems;
-                        ptx::mbar_arrive_expect_tx(&ctl->full[stage], nt * (kABytes / 2));
-                        for (int q = 0; q < nt; ++q)
-                            tma_load_3d(dst + q * (kABytes / 2), &a.maps[sh ? kMapSDown : kMapDown],
-                                        &ctl->full[stage], k + q * C::kElems, row, e);
+                        // K tiles past the end are zero-filled and counted all the same
+                        ptx::mbar_arrive_expect_tx(bar, q * a.rd * 128);
+                        tma_load_4d(dst, &a.maps[sh ? kMapSDown : kMapDown], bar, 0, row, k, e);
                     }
-                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
                 }
             }
+            if (ok) post(-1);
         }
     } else if (warp == 1) {
         // -------------------------------------------------- the rows beside the weights
         if (lane == 0 && !a.test_stall) {
-            int stage = 0, slot = 0;
-            uint32_t phase = 0, qphase = 0;
-            bool ok = true;
-            while (ok) {
-                if (!wait_bounded(&ctl->qfull[slot], qphase, ctl, a, 20)) break;
-                const int u = ctl->queue[slot];
-                ptx::mbar_arrive(&ctl->qempty[slot]);
-                if (++slot == kQueue) { slot = 0; qphase ^= 1u; }
-                if (u < 0) break;
-                const Unit un = unit_at(sc, u, shared);
-                const bool sh = un.group < shared;
-                const int tokens = __popc((uint32_t)ctl->mask[un.group]);
-                const int w = NT == 8 || tokens <= 8 ? 8 : 16;
-                const int rows = sh ? a.T : a.T * a.K;
-                const int row0 = ctl->row0[un.group] - (sh || !shared ? 0 : a.T);
-                if (un.down) {
-                    // the group's h: finished tiles are counted by whoever finishes them
-                    const int tiles = sh ? sc.tiles_s : sc.tiles_r;
-                    if (ld_acquire(a.ready + un.group) < tiles) {
-                        const uint64_t t0 = ptx::globaltimer_ns();
-                        while (ld_acquire(a.ready + un.group) < tiles) {
-                            __nanosleep(32);
-                            if (*(volatile int*)&ctl->abort_flag) { ok = false; break; }
-                            if (ptx::globaltimer_ns() - t0 > a.timeout_ns) {
-                                record_error(a.err, MOE_ERR_TIMEOUT, 21);
-                                *(volatile int*)&ctl->abort_flag = 1;
-                                ok = false;
-                                break;
-                            }
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, qphase = 0;
+        bool ok = true;
+        while (ok) {
+            if (!wait_bounded(&ctl->qfull[slot], qphase, ctl, a, 20)) break;
+            const int u = ctl->queue[slot];
+            ptx::mbar_arrive(&ctl->qempty[slot]);
+            if (++slot == kQueue) { slot = 0; qphase ^= 1u; }
+            if (u < 0) break;
+            const Unit un = unit_at(sc, u, shared);
+            const bool sh = un.group < shared;
+            const int tokens = __popc((uint32_t)ctl->mask[un.group]);
+            const int w = NT == 8 || tokens <= 8 ? 8 : 16;
+            const int row0 = ctl->row0[un.group] - (sh || !shared ? 0 : a.T);
+            if (un.down) {
+                // the group's h: finished tiles are counted by whoever finishes them
+                const int tiles = FMT ? (sh ? a.Is : a.I) / 128 : sh ? sc.gs : sc.gr;
+                if (ld_acquire(a.ready + un.group) < tiles) {
+                    const uint64_t t0 = ptx::globaltimer_ns();
+                    while (ld_acquire(a.ready + un.group) < tiles) {
+                        __nanosleep(32);
+                        if (*(volatile int*)&ctl->abort_flag) { ok = false; break; }
+                        if (ptx::globaltimer_ns() - t0 > a.timeout_ns) {
+                            record_error(a.err, MOE_ERR_TIMEOUT, 21);
+                            *(volatile int*)&ctl->abort_flag = 1;
+                            ok = false;
+                            break;
                         }
-                        if (!ok) break;
                     }
-                    fence_proxy_async_all();
+                    if (!ok) break;
                 }
-                for (int i = 0; i < un.ns; ++i) {
-                    if (!wait_bounded(&ctl->empty[stage], phase ^ 1u, ctl, a, 22)) { ok = false; break; }
-                    uint8_t* dst = ring + stage * C::kStage + kABytes;
-                    uint64_t* bar = &ctl->full[stage];
-                    if (!un.down) {
-                        const int k = (un.s0 + i) * C::kElems;
-                        ptx::mbar_arrive_expect_tx(bar, C::kXBytes);
-                        ptx::tma_load_2d(dst, &a.maps[kMapX], bar, k, 0);
-                        if (FMT) ptx::tma_load_2d(dst + NT * 128, &a.maps[kMapX], bar, k, a.T);
-                    } else {
-                        const int nt = tiles_of_stage<FMT>(a, un, shared, i);
-                        const CUtensorMap* map = &a.maps[sh ? kMapHS : kMapH];
-                        ptx::mbar_arrive_expect_tx(bar, nt * C::kHPlanes * w * 128);
-                        for (int q = 0; q < nt; ++q)
-                            for (int p = 0; p < C::kHPlanes; ++p)
-                                for (int b = 0; b < w; b += 8)
-                                    ptx::tma_load_2d(dst + q * C::kHTile + (p * w + b) * 128, map, bar,
-                                                     (2 * (un.s0 + i) + q) * C::kElems,
-                                                     p * rows + row0 + b);
-                    }
-                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
-                }
+                fence_proxy_async_all();
             }
+            const int q = un.down ? a.qd : a.qg;
+            const CUtensorMap* map =
+                &a.maps[w == 8 ? (sh ? kMapHS8 : kMapH8) : (sh ? kMapHS16 : kMapH16)];
+            for (int k = 0; k < un.n; k += q) {
+                if (!wait_bounded(&ctl->empty[stage], phase ^ 1u, ctl, a, 22)) { ok = false; break; }
+                uint8_t* dst = ring + stage * kStage + kABytes;
+                uint64_t* bar = &ctl->full[stage];
+                if (!un.down) {
+                    ptx::mbar_arrive_expect_tx(bar, q * C::kXTile);
+                    if (FMT) tma_load_4d(dst, &a.maps[kMapX], bar, 0, 0, 0, k);
+                    else tma_load_3d(dst, &a.maps[kMapX], bar, 0, 0, k);
+                } else {
+                    ptx::mbar_arrive_expect_tx(bar, q * C::kHPlanes * w * 128);
+                    tma_load_4d(dst, map, bar, 0, row0, 0, k);
+                }
+                if (++stage == kStages) { stage = 0; phase ^= 1u; }
+            }
+        }
         }
     } else if (warp == 2) {
         // -------------------------------------------------- products
@@ -737,39 +735,39 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                 if (u < 0) break;
                 const Unit un = unit_at(sc, u, shared);
                 const int w = NT == 8 || __popc((uint32_t)ctl->mask[un.group]) <= 8 ? 8 : 16;
-                const int n = un.down ? C::kHCols * w : (FMT ? 2 * NT : 16);
+                const int n = un.down ? C::kHCols * w : C::kXCols;
                 const uint32_t idesc = FMT ? ptx::idesc_e4m3_f32(128, n) : ptx::idesc_bf16_f32(128, n);
-                // accumulators emptied every stage where the scales change along K
+                const int q = un.down ? a.qd : a.qg;
+                // weight tiles of fewer than 128 rows: the products' other rows are whatever
+                // follows in shared memory, and are not read
+                const uint32_t wtile = (un.down ? a.rd : 2 * a.rg) * 128;
+                const uint32_t btile = un.down ? C::kHPlanes * w * 128 : C::kXTile;
+                // an accumulator a K tile, emptied every stage, where the scales change along K
                 const bool each = un.down ? FMT != 0 : FMT == 2;
-                for (int i = 0; i < un.ns; ++i) {
-                    if (each || i == 0) {
+                for (int k = 0; k < un.n; k += q) {
+                    if (each || k == 0) {
                         if (!wait_bounded(&ctl->tempty[buf], bphase ^ 1u, ctl, a, 31)) { ok = false; break; }
                     }
                     if (!wait_bounded(&ctl->full[stage], phase, ctl, a, 32)) { ok = false; break; }
                     ptx::tc_fence_after();
-                    const uint32_t w0 = ptx::smem_u32(ring + stage * C::kStage);
-                    const uint32_t b0 = w0 + kABytes;
+                    const uint32_t w0 = ptx::smem_u32(ring + stage * kStage), b0 = w0 + kABytes;
                     const uint32_t d0 = tmem + buf * 128;
-                    const int nt = un.down ? tiles_of_stage<FMT>(a, un, shared, i) : 2;
-                    for (int q = 0; q < nt; ++q) {
-                        // gate and up rows: two accumulators over the same x; down rows: two K
-                        // tiles, into one accumulator or (8-bit h, scaled per 128) two
-                        const uint32_t acc = q && (!un.down || FMT) ? d0 + kAcc1 : d0;
-                        const uint32_t bq = un.down ? b0 + q * C::kHTile : b0;
+                    const int nk = min(q, un.n - k);
+                    for (int i = 0; i < nk; ++i) {
+                        const uint32_t acc = each ? d0 + i * n : d0;
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            const uint64_t wd = ptx::sw128_kmajor_desc(w0 + q * (kABytes / 2) + kk * 32);
-                            const uint64_t bd = ptx::sw128_kmajor_desc(bq + kk * 32);
-                            const bool fresh = kk == 0 && (each || i == 0) &&
-                                               !(q && un.down && FMT == 0);
+                            const uint64_t wd = ptx::sw128_kmajor_desc(w0 + i * wtile + kk * 32);
+                            const uint64_t bd = ptx::sw128_kmajor_desc(b0 + i * btile + kk * 32);
+                            const bool fresh = kk == 0 && (each || (k == 0 && i == 0));
                             if constexpr (FMT) ptx::tc_mma_f8(acc, wd, bd, idesc, fresh ? 0u : 1u);
                             else ptx::tc_mma_f16(acc, wd, bd, idesc, fresh ? 0u : 1u);
                         }
                     }
                     any = true;
                     ptx::tc_commit(&ctl->empty[stage]);
-                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
-                    if (each || i == un.ns - 1) {
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    if (each || k + q >= un.n) {
                         ptx::tc_commit(&ctl->tfull[buf]);
                         if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
                     }
@@ -784,210 +782,222 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
             }
         }
     } else if (warp >= 4) {
-        // -------------------------------------------------- sums
-        const int r = (warp - 4) * 32 + lane;  // weight row of the tile
-        const uint32_t lanes = (uint32_t)((warp - 4) * 32) << 16;
-        int slot = 0, buf = 0;
-        uint32_t qphase = 0, bphase = 0;
-        bool ok = true;
+        const bool sums = warp < 8;            // warps 4-7; 8-11 finish
+        const int r = (warp & 3) * 32 + lane;  // weight row of the tile
+        int slot = 0;
+        uint32_t qphase = 0;
+        // the four warps of a role stop together: they meet at barriers
         const auto pass = [&](uint64_t* bar, uint32_t parity, int where) {
             const int good = lane == 0 ? (int)wait_bounded(bar, parity, ctl, a, where) : 0;
-            // the four warps stop together: they meet at barriers
-            return ptx::named_bar_and(1, 128, __shfl_sync(0xffffffffu, good, 0) != 0);
+            return ptx::named_bar_and(sums ? 1 : 2, 128, __shfl_sync(0xffffffffu, good, 0) != 0);
         };
         const auto release = [&](uint64_t* bar) {
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar);
         };
-        while (ok) {
-            if (!pass(&ctl->qfull[slot], qphase, 40)) break;
-            const int uid = ctl->queue[slot];
-            release(&ctl->qempty[slot]);
-            if (++slot == kQueue) { slot = 0; qphase ^= 1u; }
-            if (uid < 0) break;
-            const Unit un = unit_at(sc, uid, shared);
-            const bool sh = un.group < shared;
-            const int e = sh ? 0 : ctl->expert[un.group];
-            const uint32_t mask = ctl->mask[un.group];
-            const int row0 = ctl->row0[un.group];
-            if (!un.down) {
-                float sg[NT], su[NT];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) sg[t] = su[t] = 0.0f;
-                const int drains = FMT == 2 ? un.ns : 1;
-                const int I = sh ? a.Is : a.I;
-                float rg = 1.0f, ru = 1.0f;
-                if constexpr (FMT == 1) {
-                    const int64_t at = (int64_t)e * I + un.tile * 128 + r;  // I a multiple of 128
-                    rg = __ldg((sh ? a.ss_gate : a.s_gate) + at);
-                    ru = __ldg((sh ? a.ss_up : a.s_up) + at);
+        if (sums) {
+            // ---------------------------------------------- sums
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            int buf = 0;
+            uint32_t bphase = 0;
+            bool ok = true;
+            while (ok) {
+                if (!pass(&ctl->qfull[slot], qphase, 40)) break;
+                const int uid = ctl->queue[slot], mine = slot;
+                if (++slot == kQueue) { slot = 0; qphase ^= 1u; }
+                if (uid < 0) {
+                    release(&ctl->summed[mine]);
+                    break;
                 }
-                const int64_t blk = ((int64_t)e * (I / 128) + un.tile) * (a.d / 128) + un.s0;
-                for (int k = 0; k < drains; ++k) {
-                    if constexpr (FMT == 2) {
-                        rg = __ldg((sh ? a.ss_gate : a.s_gate) + blk + k);
-                        ru = __ldg((sh ? a.ss_up : a.s_up) + blk + k);
-                    }
-                    if (!pass(&ctl->tfull[buf], bphase, 41)) { ok = false; break; }
-                    ptx::tc_fence_after();
-                    const uint32_t at = tmem + lanes + buf * 128;
+                const Unit un = unit_at(sc, uid, shared);
+                const bool sh = un.group < shared;
+                const int e = sh ? 0 : ctl->expert[un.group];
+                const uint32_t mask = ctl->mask[un.group];
+                const int row0 = ctl->row0[un.group];
+                const int I = sh ? a.Is : a.I;
+                if (!un.down) {
+                    float s[NT];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float (&s)[NT] = half ? su : sg;
-                        const float w = half ? ru : rg;
-                        uint32_t v[16], lo[16];
-                        ptx::tmem_ld16(at + half * kAcc1, v);
-                        if constexpr (FMT && NT == 16) ptx::tmem_ld16(at + half * kAcc1 + 16, lo);
-                        ptx::tmem_ld_wait();
+                    for (int t = 0; t < NT; ++t) s[t] = 0.0f;
+                    const bool up = r >= a.rg;
+                    const int q = FMT == 2 ? a.qg : un.n;
+                    // the thread's row scale, or its blocks' scales along K (asked for a stage ahead)
+                    const float* sp = FMT ? (up ? (sh ? a.ss_up : a.s_up) : (sh ? a.ss_gate : a.s_gate))
+                                          : nullptr;
+                    float rs = 1.0f, bs[8];
+                    if constexpr (FMT == 1)
+                        if (r < 2 * a.rg)
+                            rs = __ldg(sp + (int64_t)e * I + un.tile * a.rg + (up ? r - a.rg : r));
+                    if constexpr (FMT == 2)
+                        sp += ((int64_t)e * (I / 128) + un.tile * a.rg / 128) * (a.d / 128);
+                    const auto ask = [&](int k) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) bs[i] = i < q && k + i < un.n ? __ldg(sp + k + i) : 0.0f;
+                    };
+                    if constexpr (FMT == 2) ask(0);
+                    for (int k = 0; k < un.n; k += q) {
+                        if (!pass(&ctl->tfull[buf], bphase, 41)) { ok = false; break; }
+                        ptx::tc_fence_after();
+                        const uint32_t at = tmem + lanes + buf * 128;
+#pragma unroll
+                        for (int i = 0; i < (FMT == 2 ? 8 : 1); ++i) {
+                            if (FMT == 2 && (i >= q || k + i >= un.n)) continue;
+                            uint32_t v[16], lo[16];
+                            ptx::tmem_ld16(at + i * C::kXCols, v);
+                            if constexpr (FMT && NT == 16) ptx::tmem_ld16(at + i * C::kXCols + 16, lo);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                float x = __uint_as_float(v[t]);
+                                if constexpr (FMT)
+                                    x = fmaf(__uint_as_float(NT == 16 ? lo[t] : v[8 + (t & 7)]),
+                                             0.0625f, x);
+                                s[t] = FMT == 2 ? fmaf(x, bs[i], s[t]) : x;
+                            }
+                        }
+                        ptx::tc_fence_before();
+                        release(&ctl->tempty[buf]);
+                        if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
+                        if constexpr (FMT == 2) ask(k + q);
+                    }
+                    if (!ok) break;
+                    if (r < 2 * a.rg) {
+                        int c = 0;
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            float x = __uint_as_float(v[t]);
-                            if constexpr (FMT)
-                                x = fmaf(__uint_as_float(NT == 16 ? lo[t] : v[8 + (t & 7)]), 0.0625f, x);
-                            s[t] = FMT == 0 ? x : fmaf(x, w, s[t]);
+                            if (!(mask >> t & 1u)) continue;
+                            const float x = FMT ? ctl->xs[t] * rs : 1.0f;
+                            __stcg(gate_row(a, row0 + c, sh, shared) + un.tile * 2 * a.rg + r, s[t] * x);
+                            ++c;
                         }
                     }
-                    ptx::tc_fence_before();
-                    release(&ctl->tempty[buf]);
-                    if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
-                }
-                if (!ok) break;
-                if constexpr (FMT) {
+                } else {
+                    const int tokens = __popc(mask);
+                    const int w = NT == 8 || tokens <= 8 ? 8 : 16;
+                    const int col = un.tile * a.rd + r;
+                    const bool mine_row = r < a.rd && col < a.d;
+                    float s[NT];
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const float x = t < a.T ? __ldcg(a.xs + t) : 0.0f;
-                        sg[t] *= x;
-                        su[t] *= x;
-                    }
-                }
-                if (sc.gp > 1) {
-                    // parts of a tile: [row][tile][part][gate 128, up 128]
-                    const int tiles = sh ? sc.tiles_s : sc.tiles_r;
-                    const int64_t first = sh || !shared
-                                              ? (int64_t)row0 * tiles
-                                              : (int64_t)a.T * sc.tiles_s + (int64_t)(row0 - a.T) * tiles;
-                    float* gp = a.gpart + ((first + un.tile) * a.max_parts) * 256 + r;
-                    const int64_t step = (int64_t)tiles * a.max_parts * 256;
-                    int c = 0;
+                    for (int t = 0; t < NT; ++t) s[t] = 0.0f;
+                    const int q = FMT ? a.qd : un.n;
+                    float rs = 1.0f, bs[4], hv = 0.0f;
+                    const float* sp = FMT ? (sh ? a.ss_down : a.s_down) : nullptr;
+                    if constexpr (FMT == 1)
+                        if (mine_row) rs = __ldg(sp + (int64_t)e * a.d + col);
+                    if constexpr (FMT == 2)
+                        sp += ((int64_t)e * (a.d / 128) + un.tile * a.rd / 128) * (I / 128);
+                    // scales of the stage from K tile k: h's go through shared memory (thread
+                    // 16 i + c: tile k + i, token c), asked for a stage ahead
+                    const float* hs = FMT ? (sh ? a.hs_s : a.hs) +
+                                                (int64_t)(row0 - (sh || !shared ? 0 : a.T)) * (I / 128)
+                                          : nullptr;
+                    const auto ask = [&](int k) {
+                        const int i = r >> 4, c = r & 15;
+                        hv = i < q && k + i < un.n && c < tokens
+                                 ? __ldcg(hs + (int64_t)c * (I / 128) + k + i) : 0.0f;
+                        if constexpr (FMT == 2)
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        if (!(mask >> t & 1u)) continue;
-                        float* p = gp + c * step + un.part * 256;
-                        __stcg(p, sg[t]);
-                        __stcg(p + 128, su[t]);
-                        ++c;
-                    }
-                    int* counter = a.gticket + un.group * max(sc.tiles_s, sc.tiles_r) + un.tile;
-                    if (!last_part(ctl, counter, sc.gp, r)) continue;
-                    c = 0;
+                            for (int i2 = 0; i2 < 4; ++i2)
+                                bs[i2] = i2 < q && k + i2 < un.n ? __ldg(sp + k + i2) : 0.0f;
+                    };
+                    int turn = 0;
+                    for (int k = 0; k < un.n; k += q, turn ^= 1) {
+                        if (FMT && k > 0 && r < 64) ctl->hscale[turn][r] = hv;
+                        if (!pass(&ctl->tfull[buf], bphase, 42)) { ok = false; break; }
+                        ptx::tc_fence_after();
+                        float bsn[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+                        if constexpr (FMT) {
+                            if (k == 0) {
+                                // h is done: a product with it is
+                                ask(0);
+                                if (r < 64) ctl->hscale[turn][r] = hv;
+                                asm volatile("bar.sync 1, 128;" ::: "memory");
+                            }
+                            if constexpr (FMT == 2)
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        if (!(mask >> t & 1u)) continue;
-                        const float* p = gp + c * step;
-                        float g = 0.0f, w = 0.0f;
-#pragma unroll 4
-                        for (int q = 0; q < sc.gp; ++q) {
-                            g += __ldcg(p + q * 256);
-                            w += __ldcg(p + q * 256 + 128);
+                                for (int i = 0; i < 4; ++i) bsn[i] = bs[i];
+                            ask(k + q);
                         }
-                        sg[t] = g;
-                        su[t] = w;
-                        ++c;
+                        const uint32_t at = tmem + lanes + buf * 128;
+#pragma unroll
+                        for (int i = 0; i < (FMT ? 4 : 1); ++i) {
+                            if (FMT && (i >= q || k + i >= un.n)) continue;
+                            const uint32_t ai = at + i * C::kHCols * w;
+                            float v[NT];
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) v[t] = 0.0f;
+                            if (w == 8) {
+                                uint32_t p01[16], p23[16];
+                                ptx::tmem_ld16(ai, p01);
+                                if constexpr (FMT) ptx::tmem_ld16(ai + 16, p23);
+                                ptx::tmem_ld_wait();
+#pragma unroll
+                                for (int t = 0; t < 8; ++t) {
+                                    const float hi = __uint_as_float(p01[t]);
+                                    const float lo = __uint_as_float(p01[8 + t]);
+                                    if constexpr (FMT)
+                                        v[t] = fmaf(fmaf(__uint_as_float(p23[t]), 0.0625f, lo), 0.0625f, hi);
+                                    else v[t] = hi + lo;
+                                }
+                            } else if constexpr (NT == 16) {
+                                uint32_t p0[16], p1[16], p2[16];
+                                ptx::tmem_ld16(ai, p0);
+                                ptx::tmem_ld16(ai + 16, p1);
+                                if constexpr (FMT) ptx::tmem_ld16(ai + 32, p2);
+                                ptx::tmem_ld_wait();
+#pragma unroll
+                                for (int t = 0; t < 16; ++t) {
+                                    const float hi = __uint_as_float(p0[t]), lo = __uint_as_float(p1[t]);
+                                    if constexpr (FMT)
+                                        v[t] = fmaf(fmaf(__uint_as_float(p2[t]), 0.0625f, lo), 0.0625f, hi);
+                                    else v[t] = hi + lo;
+                                }
+                            }
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                if constexpr (FMT) {
+                                    if (t < tokens)
+                                        s[t] = fmaf(v[t], ctl->hscale[turn][16 * i + t] * bsn[i], s[t]);
+                                } else {
+                                    s[t] = v[t];
+                                }
+                            }
+                        }
+                        ptx::tc_fence_before();
+                        release(&ctl->tempty[buf]);
+                        if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
+                    }
+                    if (!ok) break;
+                    if (mine_row) {
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            if (t < tokens) __stcg(a.yp + (int64_t)(row0 + t) * a.d + col, s[t] * rs);
                     }
                 }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) sg[t] = silu_mul(sg[t], su[t]);
-                store_h<FMT, NT>(a, sc, ctl, un, sg, r, shared);
-            } else {
-                const int tokens = __popc(mask);
-                const int w = NT == 8 || tokens <= 8 ? 8 : 16;
-                const int I = sh ? a.Is : a.I;
-                const int hrow0 = row0 - (sh || !shared ? 0 : a.T);
-                float s[NT];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) s[t] = 0.0f;
-                const int drains = FMT ? un.ns : 1;
-                for (int k = 0; k < drains; ++k) {
-                    if (!pass(&ctl->tfull[buf], bphase, 42)) { ok = false; break; }
-                    ptx::tc_fence_after();
+                release(&ctl->summed[mine]);
+                release(&ctl->qempty[mine]);
+            }
+        } else {
+            // ---------------------------------------------- finishing
+            // Its own warps, so that the fence and the count of a part (microseconds while
+            // the memory is busy) hold up neither the sums nor the stream.
+            while (pass(&ctl->summed[slot], qphase, 50)) {
+                const int uid = ctl->queue[slot];
+                release(&ctl->qempty[slot]);
+                if (++slot == kQueue) { slot = 0; qphase ^= 1u; }
+                if (uid < 0) break;
+                const Unit un = unit_at(sc, uid, shared);
+                if (!un.down) {
                     if constexpr (FMT) {
-                        if (k == 0) {
-                            // h's scales of the unit, [K tile][token]; visible once a product of
-                            // the unit is: its rows were loaded after the group's h was done
-                            const int k0 = 2 * un.s0, nk = min(2 * un.ns, I / 128 - k0);
-                            const float* hs = sh ? a.hs_s : a.hs;
-                            for (int i = r; i < nk * tokens; i += 128) {
-                                const int c = i % tokens, q = i / tokens;
-                                ctl->hscale[q * NT + c] =
-                                    __ldcg(hs + (int64_t)(hrow0 + c) * (I / 128) + k0 + q);
-                            }
-                            if constexpr (FMT == 2) {
-                                const float* ws = (sh ? a.ss_down : a.s_down) +
-                                                  ((int64_t)e * (a.d / 128) + un.tile) * (I / 128) + k0;
-                                for (int i = r; i < nk; i += 128) ctl->wscale[0][i] = __ldg(ws + i);
-                            }
-                            drain_sync();
-                        }
+                        // the 128 rows that share h's scales
+                        const int blocks = max(a.I, a.Is) / 128, parts = 128 / a.rg;
+                        int* counter = a.gticket + un.group * blocks + un.tile / parts;
+                        if (!last_part(ctl, counter, parts, r)) continue;
                     }
-                    const uint32_t at = tmem + lanes + buf * 128;
-                    const int nq = FMT ? tiles_of_stage<FMT>(a, un, shared, k) : 1;
-                    for (int q = 0; q < nq; ++q) {
-                        float v[NT];
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) v[t] = 0.0f;
-                        if (w == 8) {
-                            uint32_t p01[16], p23[16];
-                            ptx::tmem_ld16(at + q * kAcc1, p01);
-                            if constexpr (FMT) ptx::tmem_ld16(at + q * kAcc1 + 16, p23);
-                            ptx::tmem_ld_wait();
-#pragma unroll
-                            for (int t = 0; t < 8; ++t) {
-                                const float hi = __uint_as_float(p01[t]), lo = __uint_as_float(p01[8 + t]);
-                                if constexpr (FMT)
-                                    v[t] = fmaf(fmaf(__uint_as_float(p23[t]), 0.0625f, lo), 0.0625f, hi);
-                                else v[t] = hi + lo;
-                            }
-                        } else if constexpr (NT == 16) {
-                            uint32_t p0[16], p1[16], p2[16];
-                            ptx::tmem_ld16(at + q * kAcc1, p0);
-                            ptx::tmem_ld16(at + q * kAcc1 + 16, p1);
-                            if constexpr (FMT) ptx::tmem_ld16(at + q * kAcc1 + 32, p2);
-                            ptx::tmem_ld_wait();
-#pragma unroll
-                            for (int t = 0; t < 16; ++t) {
-                                const float hi = __uint_as_float(p0[t]), lo = __uint_as_float(p1[t]);
-                                if constexpr (FMT)
-                                    v[t] = fmaf(fmaf(__uint_as_float(p2[t]), 0.0625f, lo), 0.0625f, hi);
-                                else v[t] = hi + lo;
-                            }
-                        }
-                        const float wsc = FMT == 2 ? ctl->wscale[0][2 * k + q] : 1.0f;
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            if constexpr (FMT) {
-                                if (t < tokens)
-                                    s[t] = fmaf(v[t], ctl->hscale[(2 * k + q) * NT + t] * wsc, s[t]);
-                            } else {
-                                s[t] += v[t];
-                            }
-                        }
-                    }
-                    ptx::tc_fence_before();
-                    release(&ctl->tempty[buf]);
-                    if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
+                    finish_h<FMT, NT>(a, ctl, un, r, shared);
+                } else if (last_part(ctl, a.dticket + un.tile, ctl->groups, r)) {
+                    join_tile(a, ctl, un.tile, r);
                 }
-                if (!ok) break;
-                const int col = un.tile * 128 + r;
-                float rs = 1.0f;
-                if constexpr (FMT == 1)
-                    rs = __ldg((sh ? a.ss_down : a.s_down) + (int64_t)e * a.d + col);  // d a multiple of 128
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    if (t < tokens && col < a.d)
-                        __stcg(a.yp + ((int64_t)(row0 + t) * a.max_parts + un.part) * a.d + col, s[t] * rs);
-                const int parts = (shared ? sc.dps : 0) + (ctl->groups - shared) * sc.dpr;
-                if (last_part(ctl, a.dticket + un.tile, parts, r))
-                    join_tile(a, sc, ctl, un.tile, warp - 4, lane);
             }
         }
     }
@@ -1001,7 +1011,7 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == 3) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
     }
@@ -1013,34 +1023,68 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// [n][rows][cols] matrices of `size`-byte elements, box = 128 bytes x box_rows rows of one;
-// rank 2 for n = 0 ([rows][cols]).
-bool make_map(CUtensorMap* m, const void* base, int64_t n, int64_t rows, int64_t cols, int size,
-              int box_rows) {
+// a map of `rank` dimensions, the first 128 bytes or more of `size`-byte elements; strides in
+// bytes, of all but the first
+bool make_map(CUtensorMap* m, const void* base, int size, int rank, const int64_t (&dim)[4],
+              const int64_t (&stride)[3], const int (&box)[4]) {
     const EncodeTiledFn fn = (EncodeTiledFn)tensor_map_encoder();
     if (!fn) return false;
-    const cuuint32_t rank = n ? 3 : 2;
-    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
-    const cuuint64_t strides[2] = {(cuuint64_t)(cols * size), (cuuint64_t)(rows * cols * size)};
-    const cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
+    cuuint64_t dims[4], strides[3];
+    cuuint32_t boxes[4], ones[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) {
+        dims[i] = (cuuint64_t)dim[i];
+        boxes[i] = (cuuint32_t)box[i];
+        if (i < 3) strides[i] = (cuuint64_t)stride[i];
+    }
     return fn(m, size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank,
-              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// gate or up weights [n][rows][cols]: `box` rows of one K tile
+bool gate_map(CUtensorMap* m, const void* base, int size, int64_t n, int64_t rows, int64_t cols,
+              int box) {
+    return make_map(m, base, size, 3, {cols, rows, n, 1}, {cols * size, rows * cols * size, 0},
+                    {128 / size, box, 1, 1});
+}
+
+// down weights [n][rows][cols]: `box` rows of q K tiles, tile after tile
+bool down_map(CUtensorMap* m, const void* base, int size, int64_t n, int64_t rows, int64_t cols,
+              int box, int q) {
+    return make_map(m, base, size, 4, {128 / size, rows, cols * size / 128, n},
+                    {cols * size, 128, rows * cols * size}, {128 / size, box, q, 1});
+}
+
+// planes [p][rows][cols] of x or h: `box` rows of every plane, of q K tiles
+bool rows_map(CUtensorMap* m, const void* base, int size, int64_t planes, int64_t rows, int64_t cols,
+              int box, int q) {
+    return make_map(m, base, size, 4, {128 / size, rows, planes, cols * size / 128},
+                    {cols * size, rows * cols * size, 128}, {128 / size, box, (int)planes, q});
+}
+
 template <int FMT, int NT>
 cudaError_t go(const FewArgs& a, cudaStream_t st) {
-    using C = Cfg<FMT, NT>;
-    constexpr size_t smem = 1024 + (size_t)C::kStages * C::kStage + sizeof(Ctl);
+    constexpr size_t smem = 1024 + (size_t)kStages * kStage + sizeof(Ctl);
     static_assert(smem <= 232448, "shared memory exceeds the per-block limit");
-    static_assert(sizeof(float) * kMaxT * 1024 <= (size_t)C::kStages * C::kStage, "keys fit the ring");
+    static_assert(8u * kMaxT * 1024 <= (size_t)kStages * kStage, "keys and scores fit the ring");
+    static_assert(sizeof(FewArgs) <= 4000, "the arguments fit the launch");
     cudaError_t e = cudaFuncSetAttribute(few_experts_kernel<FMT, NT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(few_experts_kernel<FMT, NT>, dim3(device_sm_count()), dim3(kThreads), smem, st, a);
+    // no more blocks than units, were every pick another expert's
+    const int64_t groups = a.T * a.K < a.E ? a.T * a.K : a.E;
+    const int64_t units = a.Is / a.rg + groups * (a.I / a.rg) +
+                          (groups + (a.Is > 0)) * ceil_div(a.d, a.rd);
+    const int sms = device_sm_count();
+    return launch_pdl(few_experts_kernel<FMT, NT>, dim3((unsigned)(units < sms ? units : sms)),
+                      dim3(kThreads), smem, st, a);
 }
+
+constexpr int kClaimInts = 64;
+constexpr double kGateUnits = 0.01, kDownUnits = 0.01;
+
+int least(int a, int b, int c) { return a < b ? (a < c ? a : c) : (b < c ? b : c); }
 
 int score_splits(int d) {
     const int n = d / 8 / 96;  // about three 16-byte vectors a lane
@@ -1054,26 +1098,26 @@ FewWs few_ws(const moe_shape& s, int fmt) {
     FewWs w{};
     const int64_t T = s.T, K = s.K, d = s.d, I = s.inter, Is = s.inter_shared, n = T * K;
     const int64_t groups = (n < s.E ? n : s.E) + 1;
-    const int64_t ti = ceil_div(I, 128), ts = ceil_div(Is, 128), td = ceil_div(d, 128);
+    const int64_t ti = ceil_div(I, 128), ts = ceil_div(Is, 128), td = ceil_div(d, 32);
     w.splits = score_splits(s.d);
-    w.max_parts = T <= 4 ? 16 : 8;
     size_t o = 256;  // the error record, then the counters
     auto take = [&](int64_t bytes) {
         const size_t at = o;
         o = (o + (size_t)bytes + 255) / 256 * 256;
         return at;
     };
-    w.counters = (int)(1 + groups + td + groups * (ti > ts ? ti : ts));
+    // the claims' counter in a cache line of its own
+    w.counters = (int)(kClaimInts + groups + td + (fmt ? groups * (ti > ts ? ti : ts) : 0));
     w.claim = take(4 * (int64_t)w.counters);
     w.part = take(4 * (int64_t)w.splits * T * s.E);
     w.xq = take(fmt ? 2 * T * d : 0);
     w.xs = take(fmt ? 4 * T : 0);
-    w.gpart = take(4 * (n * ti + T * ts) * w.max_parts * 256);
+    w.gpart = take(8 * (n * I + T * Is));
     w.h = take(fmt ? 3 * n * I : 4 * n * I);
     w.h_s = take(fmt ? 3 * T * Is : 4 * T * Is);
     w.hs = take(fmt ? 4 * n * ti : 0);
     w.hs_s = take(fmt ? 4 * T * ts : 0);
-    w.yp = take(4 * (n + (Is ? T : 0)) * w.max_parts * d);
+    w.yp = take(4 * (n + (Is ? T : 0)) * d);
     w.total = o;
     return w;
 }
@@ -1088,18 +1132,17 @@ cudaError_t launch_few(const moe_shape& s, int fmt, const FewCall& c, void* work
     a.T = s.T; a.d = s.d; a.E = s.E; a.K = s.K; a.I = s.inter; a.Is = s.inter_shared;
     a.sigmoid = s.router == MOE_ROUTER_SIGMOID;
     a.splits = w.splits;
-    a.max_parts = w.max_parts;
     a.bias = c.bias;
     a.residual = (const bf16*)c.residual;
     a.y = (bf16*)c.y;
     a.err = reinterpret_cast<DevError*>(base);
     a.claim = reinterpret_cast<int*>(base + w.claim);
     const int64_t groups = (n < E ? n : E) + 1;
-    a.ready = a.claim + 1;
+    a.ready = a.claim + kClaimInts;
     a.dticket = a.ready + groups;
-    a.gticket = a.dticket + ceil_div(d, 128);
+    a.gticket = a.dticket + ceil_div(d, 32);
     a.part = reinterpret_cast<float*>(base + w.part);
-    a.xs = reinterpret_cast<float*>(base + w.xs);
+    a.xs = fmt ? reinterpret_cast<float*>(base + w.xs) : nullptr;
     a.gpart = reinterpret_cast<float*>(base + w.gpart);
     a.h = base + w.h;
     a.h_s = base + w.h_s;
@@ -1110,22 +1153,39 @@ cudaError_t launch_few(const moe_shape& s, int fmt, const FewCall& c, void* work
     a.ss_gate = c.ss_gate; a.ss_up = c.ss_up; a.ss_down = c.ss_down;
     a.timeout_ns = tc_timeout_ns();
     a.test_stall = tc_test_stall();
-    bool ok = make_map(&a.maps[kMapGate], c.w_gate, E, I, d, size, 128) &&
-              make_map(&a.maps[kMapUp], c.w_up, E, I, d, size, 128) &&
-              make_map(&a.maps[kMapDown], c.w_down, E, d, I, size, 128) &&
-              make_map(&a.maps[kMapH], a.h, 0, (fmt ? 3 : 2) * n, I, size, 8) &&
-              (fmt ? make_map(&a.maps[kMapX], base + w.xq, 0, 2 * T, d, 1, nt)
-                   : make_map(&a.maps[kMapX], c.x, 0, T, d, 2, 16));
+    // Rows of a unit.  More rows spare copies of x and h beside the weights, fewer even out what
+    // the blocks get: the most that give every block about `kGateUnits` and `kDownUnits` of
+    // them, were all experts equally likely.
+    const double routed = E * (1.0 - pow(1.0 - (double)s.K / E, (double)T));
+    const double sms = device_sm_count();
+    a.rg = 64;
+    while (a.rg > 16 && (routed * I + Is) / a.rg < kGateUnits * sms) a.rg /= 2;
+    a.rd = 128;
+    while (a.rd > 32 && (routed + (Is > 0)) * d / a.rd < kDownUnits * sms) a.rd /= 2;
+    // K tiles of a stage: as many as the weights' and the rows' shares of it hold, and the
+    // accumulators where each tile has its own
+    const int elems = 128 / size, xcols = fmt ? 2 * nt : 16, hcols = (fmt ? 4 : 2) * nt;
+    a.qg = least(kABytes / (2 * a.rg * 128), kBBytes / (xcols * 128), fmt == 2 ? 128 / xcols : 8);
+    a.qd = least(kABytes / (a.rd * 128), kBBytes / ((fmt ? 3 : 2) * nt * 128), fmt ? 128 / hcols : 8);
+    bool ok = gate_map(&a.maps[kMapGate], c.w_gate, size, E, I, d, a.rg) &&
+              gate_map(&a.maps[kMapUp], c.w_up, size, E, I, d, a.rg) &&
+              down_map(&a.maps[kMapDown], c.w_down, size, E, d, I, a.rd, a.qd) &&
+              rows_map(&a.maps[kMapH8], a.h, size, fmt ? 3 : 2, n, I, 8, a.qd) &&
+              rows_map(&a.maps[kMapH16], a.h, size, fmt ? 3 : 2, n, I, nt, a.qd) &&
+              (fmt ? rows_map(&a.maps[kMapX], base + w.xq, 1, 2, T, d, nt, a.qg)
+                   : make_map(&a.maps[kMapX], c.x, 2, 3, {elems, T, d / elems, 1}, {d * 2, 128, 0},
+                              {elems, 16, a.qg, 1}));
     if (Is > 0) {
-        ok = ok && make_map(&a.maps[kMapSGate], c.ws_gate, 1, Is, d, size, 128) &&
-             make_map(&a.maps[kMapSUp], c.ws_up, 1, Is, d, size, 128) &&
-             make_map(&a.maps[kMapSDown], c.ws_down, 1, d, Is, size, 128) &&
-             make_map(&a.maps[kMapHS], a.h_s, 0, (fmt ? 3 : 2) * T, Is, size, 8);
+        ok = ok && gate_map(&a.maps[kMapSGate], c.ws_gate, size, 1, Is, d, a.rg) &&
+             gate_map(&a.maps[kMapSUp], c.ws_up, size, 1, Is, d, a.rg) &&
+             down_map(&a.maps[kMapSDown], c.ws_down, size, 1, d, Is, a.rd, a.qd) &&
+             rows_map(&a.maps[kMapHS8], a.h_s, size, fmt ? 3 : 2, T, Is, 8, a.qd) &&
+             rows_map(&a.maps[kMapHS16], a.h_s, size, fmt ? 3 : 2, T, Is, nt, a.qd);
     } else {
         // never loaded from: any valid map
         a.maps[kMapSGate] = a.maps[kMapSUp] = a.maps[kMapGate];
         a.maps[kMapSDown] = a.maps[kMapDown];
-        a.maps[kMapHS] = a.maps[kMapH];
+        a.maps[kMapHS8] = a.maps[kMapHS16] = a.maps[kMapH8];
     }
     if (!ok) return cudaErrorInvalidValue;
 
