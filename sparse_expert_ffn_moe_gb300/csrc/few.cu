@@ -60,7 +60,11 @@ constexpr int kScoreSplits = 8;
 constexpr int kThreads = 384;
 constexpr int kBufs = 4;       // accumulator buffers of 128 tensor-memory columns
 constexpr int kQueue = 8;      // units between the roles
-constexpr int kABytes = 32768; // weights of a stage
+constexpr int kGateRows = 64;  // gate and up rows of a unit: 128 rows of a product in all
+constexpr int kDownRows = 128;
+constexpr int kTiles = 2;      // K tiles of a stage
+constexpr int kWTile = 16384;  // bytes of a weight tile: 128 rows x 128 bytes
+constexpr int kABytes = kTiles * kWTile;
 constexpr int kBBytes = 16384; // the rows beside them
 constexpr int kStage = kABytes + kBBytes;
 constexpr int kStages = 4;
@@ -75,6 +79,10 @@ struct Cfg {
     // in shared memory and are not read.
     static constexpr int kXCols = FMT ? 2 * NT : 16, kHCols = FMT ? 4 : 2;
     static constexpr int kXTile = kXCols * 128;    // bytes beside one weight tile
+    // products with h read whole 16s of columns
+    static_assert(kTiles * kXTile <= kBBytes &&
+                      ((kTiles - 1) * kHPlanes + kHCols) * NT * 128 <= kBBytes, "rows fit the stage");
+    static_assert(kTiles * kHCols * NT <= 128, "a stage's accumulators fit a buffer");
 };
 
 enum { kMapGate, kMapUp, kMapDown, kMapSGate, kMapSUp, kMapSDown, kMapX, kMapH8, kMapHS8, kMapH16,
@@ -83,8 +91,7 @@ enum { kMapGate, kMapUp, kMapDown, kMapSGate, kMapSUp, kMapSDown, kMapX, kMapH8,
 struct FewArgs {
     CUtensorMap maps[kMaps];
     int T, d, E, K, I, Is, sigmoid, splits, test_stall;
-    int rg, rd;  // rows of a gate/up unit (of each of the two) and of a down unit
-    int qg, qd;  // K tiles of a stage
+    int gp, dp;  // parts that a gate/up and a down tile's K is cut into
     unsigned long long timeout_ns;
     const float* bias;
     const bf16* residual;
@@ -113,17 +120,17 @@ struct Ctl {
     float xs[kMaxT];              // scales of x
     float top[4][kMaxT];
     float hscale[2][4 * kMaxT];   // of a stage of h: [K tile][token], two in turn
-    alignas(16) float strand[512];  // read and written as float4
+    alignas(16) float strand[4][128];  // read and written as float4
 };
 
 struct Unit {
-    int down, group, tile, n;  // n: K tiles
+    int down, group, tile, part, k0, n;  // K tiles k0 .. k0 + n - 1
 };
 
 // The work as units, the same in every block.
 struct Sched {
     int nk, nks, nkr;   // K tiles: gate/up, shared and routed down
-    int gs, gr, td;     // units of a group: shared and routed gate/up, down
+    int gs, gr, td;     // tiles of a group: shared and routed gate/up, down
     int u1, u2, u3, u4; // ends of: shared gate/up, routed, shared down, routed down
 };
 
@@ -133,25 +140,45 @@ __device__ __forceinline__ Sched make_sched(const FewArgs& a, int groups, int el
     s.nk = a.d / elems;
     s.nks = a.Is / elems;
     s.nkr = a.I / elems;
-    s.gs = a.Is / a.rg;
-    s.gr = a.I / a.rg;
-    s.td = (a.d + a.rd - 1) / a.rd;
-    s.u1 = s.gs;
-    s.u2 = s.u1 + routed * s.gr;
-    s.u3 = s.u2 + shared * s.td;
-    s.u4 = s.u3 + routed * s.td;
+    s.gs = a.Is / kGateRows;
+    s.gr = a.I / kGateRows;
+    s.td = (a.d + kDownRows - 1) / kDownRows;
+    s.u1 = s.gs * a.gp;
+    s.u2 = s.u1 + routed * s.gr * a.gp;
+    s.u3 = s.u2 + shared * s.td * a.dp;
+    s.u4 = s.u3 + routed * s.td * a.dp;
     return s;
 }
 
-__device__ __forceinline__ Unit unit_at(const Sched& s, int u, int shared) {
-    if (u < s.u1) return {0, 0, u, s.nk};
+// part p of n K tiles in `parts` parts: whole stages but for the last (a part may be empty)
+__device__ __forceinline__ void cut(int n, int parts, int p, int& k0, int& k) {
+    const int each = ((n + kTiles - 1) / kTiles + parts - 1) / parts * kTiles;
+    k0 = min(n, p * each);
+    k = min(each, n - k0);
+}
+
+__device__ __forceinline__ Unit unit_at(const FewArgs& a, const Sched& s, int u, int shared) {
+    Unit t;
+    int n;
     if (u < s.u2) {
-        u -= s.u1;
-        return {0, shared + u / s.gr, u % s.gr, s.nk};
+        t.down = 0;
+        t.part = u % a.gp;
+        u /= a.gp;
+        t.group = u < s.gs ? 0 : shared + (u - s.gs) / s.gr;
+        t.tile = u < s.gs ? u : (u - s.gs) % s.gr;
+        n = s.nk;
+        cut(n, a.gp, t.part, t.k0, t.n);
+    } else {
+        u -= s.u2;
+        t.down = 1;
+        t.part = u % a.dp;
+        u /= a.dp;
+        t.group = u / s.td;
+        t.tile = u % s.td;
+        n = t.group < shared ? s.nks : s.nkr;
+        cut(n, a.dp, t.part, t.k0, t.n);
     }
-    if (u < s.u3) return {1, 0, u - s.u2, s.nks};
-    u -= s.u3;
-    return {1, shared + u / s.td, u % s.td, s.nkr};
+    return t;
 }
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, Ctl* ctl,
@@ -276,16 +303,25 @@ few_scores_kernel(const bf16* __restrict__ x, const bf16* __restrict__ w_g,
 #pragma unroll
         for (int m = 0; m < TT; ++m) acc[m] = 0.0f;
         const bf16* wrow = w_g + (int64_t)e * d;
-#pragma unroll 4
-        for (int v = v0 + lane; v < v1; v += 32) {
-            float wf[8];
-            unpack(ld_stream(wrow + v * 8), wf, (const bf16*)nullptr);
+        // four vectors a lane at a time, all asked for before the first is used
+        for (int vb = v0 + lane; vb < v1; vb += 128) {
+            uint4 wv[4];
 #pragma unroll
-            for (int m = 0; m < TT; ++m) {
-                float xf[8];
-                unpack(ld_ro(x + (int64_t)min(t0 + m, T - 1) * d + v * 8), xf, (const bf16*)nullptr);
+            for (int i = 0; i < 4; ++i)
+                wv[i] = vb + 32 * i < v1 ? ld_stream(wrow + (vb + 32 * i) * 8) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) acc[m] = fmaf(wf[q], xf[q], acc[m]);
+            for (int i = 0; i < 4; ++i) {
+                float wf[8];
+                unpack(wv[i], wf, (const bf16*)nullptr);
+                const int v = min(vb + 32 * i, nvec - 1);  // past the share the weights are 0 ...
+#pragma unroll
+                for (int m = 0; m < TT; ++m) {
+                    float xf[8];
+                    unpack(ld_ro(x + (int64_t)min(t0 + m, T - 1) * d + v * 8), xf, (const bf16*)nullptr);
+                    if (vb + 32 * i < v1)  // ... and x may not be finite
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) acc[m] = fmaf(wf[q], xf[q], acc[m]);
+                }
             }
         }
 #pragma unroll
@@ -331,21 +367,30 @@ __device__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* keys, float* scores
     }
     __syncthreads();
     for (int t = warp; t < a.T; t += kThreads / 32) {
+        // A lane has the experts lane, lane + 32, ...; its best one that is not taken (0: none;
+        // no key is 0, which would be a NaN of all ones: it is read as 1).  The first eight
+        // stay in registers, more are read again after each pick.
         uint32_t* key = keys + t * a.E;
-        // a lane's best among its experts lane, lane + 32, ... that are not taken (0: none;
-        // no key is 0, which would be a NaN of all ones: it is read as 1)
-        uint32_t best = 0u, taken = 0u;
+        uint32_t k8[8], best = 0u;
         int at = 0;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) k8[m] = lane + 32 * m < a.E ? max(key[lane + 32 * m], 1u) : 0u;
         const auto rescan = [&]() {
             best = 0u;
-            for (int e = lane, m = 0; e < a.E; e += 32, ++m) {
-                const uint32_t k = max(key[e], 1u);
-                if (!(taken >> m & 1u) && k > best) {
-                    best = k;
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+                if (k8[m] > best) {
+                    best = k8[m];
+                    at = lane + 32 * m;
+                }
+#pragma unroll 4
+            for (int e = lane + 256; e < a.E; e += 32)
+                if (key[e] > best) {
+                    best = key[e];
                     at = e;
                 }
-            }
         };
+        for (int e = lane + 256; e < a.E; e += 32) key[e] = max(key[e], 1u);
         rescan();
         int mine = 0;  // lane j: the j-th pick
         for (int j = 0; j < a.K; ++j) {
@@ -353,7 +398,10 @@ __device__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* keys, float* scores
             const int e = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7fffffff);
             if (lane == j) mine = e;
             if ((e & 31) == lane) {
-                taken |= 1u << (e >> 5);
+#pragma unroll
+                for (int m = 0; m < 8; ++m)
+                    if (e == lane + 32 * m) k8[m] = 0u;
+                if (e >= 256) key[e] = 0u;
                 rescan();
             }
         }
@@ -427,48 +475,45 @@ __device__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* keys, float* scores
     if (a.xs && threadIdx.x < a.T) ctl->xs[threadIdx.x] = __ldcg(a.xs + threadIdx.x);
 }
 
-// y of a tile of rd columns from every group's part of every row: the shared expert first,
-// then a token's picks in their order.  A set of rd / 4 threads takes a token, or a strand of
-// its rows where there are fewer tokens than sets.
-__device__ void join_tile(const FewArgs& a, Ctl* ctl, int m, int r) {
+// y of a tile of 128 columns from every part of every row: the shared expert first, then a
+// token's picks in their order.  A warp takes a token, or a strand of its parts where there
+// are fewer tokens than warps.
+__device__ void join_tile(const FewArgs& a, Ctl* ctl, int m, int warp, int lane) {
     const int shared = a.Is > 0;
-    const int lanes = a.rd / 4, sets = 128 / lanes, set = r / lanes;
-    const int cl = (r % lanes) * 4, c = m * a.rd + cl;
+    const int c = m * kDownRows + lane * 4;
     const bool in = c < a.d;
-    int strands = 1;
-    while (2 * strands * a.T <= sets) strands *= 2;
-    const int n = shared + a.K;
-    for (int item0 = 0; item0 < a.T * strands; item0 += sets) {
-        const int item = item0 + set, t = item / strands, q = item % strands;
-        const bool on = in && item < a.T * strands;
+    const int strands = a.T == 1 ? 4 : a.T == 2 ? 2 : 1;
+    const int n = (shared + a.K) * a.dp;
+    for (int item = warp; item < a.T * strands; item += 4) {
+        const int t = item / strands, q = item % strands;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (on) {
+        if (in) {
 #pragma unroll 8
             for (int i = q; i < n; i += strands) {
-                const int j = i - shared;
+                const int j = i / a.dp - shared;
                 const int row = j < 0 ? t : ctl->pick[t * a.K + j];
                 const float w = j < 0 ? 1.0f : ctl->weight[t * a.K + j];
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.yp + (int64_t)row * a.d + c));
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                    a.yp + ((int64_t)row * a.dp + i % a.dp) * a.d + c));
                 s.x = fmaf(w, v.x, s.x);
                 s.y = fmaf(w, v.y, s.y);
                 s.z = fmaf(w, v.z, s.z);
                 s.w = fmaf(w, v.w, s.w);
             }
         }
-        if (strands > 1) {  // then all items are in one turn
-            *reinterpret_cast<float4*>(&ctl->strand[set * a.rd + cl]) = s;
+        if (strands > 1) {  // then every warp has one item
+            *reinterpret_cast<float4*>(&ctl->strand[warp][lane * 4]) = s;
             finish_sync();
-            if (on && q == 0)
+            if (q == 0)
                 for (int k = 1; k < strands; ++k) {
-                    const float4 v =
-                        *reinterpret_cast<const float4*>(&ctl->strand[(set + k) * a.rd + cl]);
+                    const float4 v = *reinterpret_cast<const float4*>(&ctl->strand[warp + k][lane * 4]);
                     s.x += v.x;
                     s.y += v.y;
                     s.z += v.z;
                     s.w += v.w;
                 }
         }
-        if (!on || q != 0) continue;
+        if (!in || q != 0) continue;
         const int64_t at = (int64_t)t * a.d + c;
         if (a.residual) {
             // not through the read-only path: y may be the residual itself
@@ -502,15 +547,27 @@ __device__ __forceinline__ bool last_part(Ctl* ctl, int* counter, int parts, int
     return ctl->last != 0;
 }
 
-// Gate and up sums of a row: [unit of the group][gate rg, up rg]
-__device__ __forceinline__ float* gate_row(const FewArgs& a, int row, bool sh, int shared) {
-    const int64_t at = sh ? (int64_t)row * a.Is
-                          : (int64_t)(shared ? a.T : 0) * a.Is + (int64_t)(row - (shared ? a.T : 0)) * a.I;
-    return a.gpart + 2 * at;
+// Gate and up sums of a row: [tile of the group][part][gate 64, up 64]
+__device__ __forceinline__ float* gate_sums(const FewArgs& a, int row, bool sh, int shared, int tile) {
+    const int first = shared ? a.T : 0;
+    const int64_t at = sh ? (int64_t)row * (a.Is / kGateRows)
+                          : (int64_t)first * (a.Is / kGateRows) + (int64_t)(row - first) * (a.I / kGateRows);
+    return a.gpart + (at + tile) * a.gp * 2 * kGateRows;
 }
 
-// h of a finished gate/up unit (bf16) or of 128 rows of finished units (8-bit: a scale per
-// token and 128 values), stored as planes; then the group's count of finished ones.
+// h of row i of a tile from its parts' sums, in their order
+__device__ __forceinline__ float h_of(const FewArgs& a, const float* p) {
+    float g = 0.0f, u = 0.0f;
+#pragma unroll 4
+    for (int q = 0; q < a.gp; ++q, p += 2 * kGateRows) {
+        g += __ldcg(p);
+        u += __ldcg(p + kGateRows);
+    }
+    return silu_mul(g, u);
+}
+
+// h of a finished gate/up tile (bf16) or of two (8-bit: a scale per token and 128 values),
+// stored as planes; then the group's count of finished ones.
 template <int FMT, int NT>
 __device__ __forceinline__ void finish_h(const FewArgs& a, Ctl* ctl, const Unit& u, int r, int shared) {
     using C = Cfg<FMT, NT>;
@@ -519,20 +576,17 @@ __device__ __forceinline__ void finish_h(const FewArgs& a, Ctl* ctl, const Unit&
     const int grow0 = ctl->row0[u.group], row0 = grow0 - (sh || !shared ? 0 : a.T);
     const int tokens = __popc((uint32_t)ctl->mask[u.group]);
     if constexpr (FMT == 0) {
-        // rg threads a token
-        const int i = r % a.rg;
+        const int i = r % kGateRows;
         bf16* base = reinterpret_cast<bf16*>(sh ? a.h_s : a.h);
-        for (int c = r / a.rg; c < tokens; c += 128 / a.rg) {
-            const float* p = gate_row(a, grow0 + c, sh, shared) + u.tile * 2 * a.rg + i;
-            const float h = silu_mul(__ldcg(p), __ldcg(p + a.rg));
-            bf16* hp = base + (int64_t)(row0 + c) * I + u.tile * a.rg + i;
+        for (int c = r / kGateRows; c < tokens; c += 128 / kGateRows) {
+            const float h = h_of(a, gate_sums(a, grow0 + c, sh, shared, u.tile) + i);
+            bf16* hp = base + (int64_t)(row0 + c) * I + u.tile * kGateRows + i;
             const bf16 hi = __float2bfloat16_rn(h);
             hp[0] = hi;
             hp[(int64_t)rows * I] = __float2bfloat16_rn(h - __bfloat162float(hi));
         }
     } else {
-        const int block = u.tile * a.rg / 128, i = block * 128 + r;
-        const int at = i / a.rg * 2 * a.rg + i % a.rg;
+        const int block = u.tile / 2, i = block * 128 + r;
         uint8_t* base = reinterpret_cast<uint8_t*>(sh ? a.h_s : a.h);
         float* hs = sh ? a.hs_s : a.hs;
         float h[NT];
@@ -540,12 +594,7 @@ __device__ __forceinline__ void finish_h(const FewArgs& a, Ctl* ctl, const Unit&
         for (int c = 0; c < NT; ++c) {
             h[c] = 0.0f;
             if (c >= tokens) continue;
-            const float* p = gate_row(a, grow0 + c, sh, shared) + at;
-            h[c] = silu_mul(__ldcg(p), __ldcg(p + a.rg));
-        }
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-            if (c >= tokens) continue;
+            h[c] = h_of(a, gate_sums(a, grow0 + c, sh, shared, i / kGateRows) + i % kGateRows);
             float m = fabsf(h[c]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -574,6 +623,38 @@ __device__ __forceinline__ void finish_h(const FewArgs& a, Ctl* ctl, const Unit&
     finish_sync();
     if (r == 0)
         asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(a.ready + u.group) : "memory");
+}
+
+// 16 or 32 columns of tensor memory
+template <int N>
+__device__ __forceinline__ void load_cols(uint32_t at, uint32_t (&v)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) {
+        uint32_t (&part)[16] = *reinterpret_cast<uint32_t (*)[16]>(&v[c]);
+        ptx::tmem_ld16(at + c, part);
+    }
+}
+
+// The planes of down sums joined, W columns a plane: of one accumulator (bf16) or of each K
+// tile's (8-bit: two finer planes, the next columns are not read).
+template <int FMT, int W, int NT>
+__device__ __forceinline__ void down_cols(uint32_t at, float (&v)[FMT ? kTiles : 1][NT]) {
+    constexpr int N = FMT ? 4 * W : 2 * W, L = FMT && W == 16 ? 48 : N;
+    uint32_t c[FMT ? kTiles : 1][L];
+#pragma unroll
+    for (int i = 0; i < (FMT ? kTiles : 1); ++i) load_cols(at + i * N, c[i]);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < (FMT ? kTiles : 1); ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            v[i][t] = 0.0f;
+            if (t >= W) continue;
+            const float hi = __uint_as_float(c[i][t % W]), lo = __uint_as_float(c[i][W + t % W]);
+            if constexpr (FMT)
+                v[i][t] = fmaf(fmaf(__uint_as_float(c[i][2 * W + t % W]), 0.0625f, lo), 0.0625f, hi);
+            else v[i][t] = hi + lo;
+        }
 }
 
 template <int FMT, int NT>
@@ -638,28 +719,27 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                 const int u = claim;
                 claim = atomicAdd(a.claim, 1);  // answered while this unit's copies go out
                 if (!post(u)) { ok = false; break; }
-                const Unit un = unit_at(sc, u, shared);
+                const Unit un = unit_at(a, sc, u, shared);
                 const bool sh = un.group < shared;
                 const int e = sh ? 0 : ctl->expert[un.group];
-                const int row = un.tile * (un.down ? a.rd : a.rg), q = un.down ? a.qd : a.qg;
-                for (int k = 0; k < un.n; k += q) {
+                for (int k = un.k0; k < un.k0 + un.n; k += kTiles) {
                     if (!wait_bounded(&ctl->empty[stage], phase ^ 1u, ctl, a, 11)) { ok = false; break; }
                     uint8_t* dst = ring + stage * kStage;
                     uint64_t* bar = &ctl->full[stage];
                     if (!un.down) {
                         // a K tile's gate rows, then its up rows
-                        const int nk = min(q, un.n - k), tile = a.rg * 128;
-                        ptx::mbar_arrive_expect_tx(bar, nk * 2 * tile);
-                        for (int i = 0; i < nk; ++i) {
+                        const int nk = min(kTiles, un.k0 + un.n - k), row = un.tile * kGateRows;
+                        ptx::mbar_arrive_expect_tx(bar, nk * kWTile);
+                        for (int i = 0; i < nk; ++i, dst += kWTile) {
                             const int c = (k + i) * C::kElems;
                             tma_load_3d(dst, &a.maps[sh ? kMapSGate : kMapGate], bar, c, row, e);
-                            tma_load_3d(dst + tile, &a.maps[sh ? kMapSUp : kMapUp], bar, c, row, e);
-                            dst += 2 * tile;
+                            tma_load_3d(dst + kWTile / 2, &a.maps[sh ? kMapSUp : kMapUp], bar, c, row, e);
                         }
                     } else {
                         // K tiles past the end are zero-filled and counted all the same
-                        ptx::mbar_arrive_expect_tx(bar, q * a.rd * 128);
-                        tma_load_4d(dst, &a.maps[sh ? kMapSDown : kMapDown], bar, 0, row, k, e);
+                        ptx::mbar_arrive_expect_tx(bar, kABytes);
+                        tma_load_4d(dst, &a.maps[sh ? kMapSDown : kMapDown], bar, 0,
+                                    un.tile * kDownRows, k, e);
                     }
                     if (++stage == kStages) { stage = 0; phase ^= 1u; }
                 }
@@ -678,7 +758,7 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
             ptx::mbar_arrive(&ctl->qempty[slot]);
             if (++slot == kQueue) { slot = 0; qphase ^= 1u; }
             if (u < 0) break;
-            const Unit un = unit_at(sc, u, shared);
+            const Unit un = unit_at(a, sc, u, shared);
             const bool sh = un.group < shared;
             const int tokens = __popc((uint32_t)ctl->mask[un.group]);
             const int w = NT == 8 || tokens <= 8 ? 8 : 16;
@@ -702,19 +782,18 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                 }
                 fence_proxy_async_all();
             }
-            const int q = un.down ? a.qd : a.qg;
             const CUtensorMap* map =
                 &a.maps[w == 8 ? (sh ? kMapHS8 : kMapH8) : (sh ? kMapHS16 : kMapH16)];
-            for (int k = 0; k < un.n; k += q) {
+            for (int k = un.k0; k < un.k0 + un.n; k += kTiles) {
                 if (!wait_bounded(&ctl->empty[stage], phase ^ 1u, ctl, a, 22)) { ok = false; break; }
                 uint8_t* dst = ring + stage * kStage + kABytes;
                 uint64_t* bar = &ctl->full[stage];
                 if (!un.down) {
-                    ptx::mbar_arrive_expect_tx(bar, q * C::kXTile);
+                    ptx::mbar_arrive_expect_tx(bar, kTiles * C::kXTile);
                     if (FMT) tma_load_4d(dst, &a.maps[kMapX], bar, 0, 0, 0, k);
                     else tma_load_3d(dst, &a.maps[kMapX], bar, 0, 0, k);
                 } else {
-                    ptx::mbar_arrive_expect_tx(bar, q * C::kHPlanes * w * 128);
+                    ptx::mbar_arrive_expect_tx(bar, kTiles * C::kHPlanes * w * 128);
                     tma_load_4d(dst, map, bar, 0, row0, 0, k);
                 }
                 if (++stage == kStages) { stage = 0; phase ^= 1u; }
@@ -733,18 +812,14 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                 ptx::mbar_arrive(&ctl->qempty[slot]);
                 if (++slot == kQueue) { slot = 0; qphase ^= 1u; }
                 if (u < 0) break;
-                const Unit un = unit_at(sc, u, shared);
+                const Unit un = unit_at(a, sc, u, shared);
                 const int w = NT == 8 || __popc((uint32_t)ctl->mask[un.group]) <= 8 ? 8 : 16;
                 const int n = un.down ? C::kHCols * w : C::kXCols;
                 const uint32_t idesc = FMT ? ptx::idesc_e4m3_f32(128, n) : ptx::idesc_bf16_f32(128, n);
-                const int q = un.down ? a.qd : a.qg;
-                // weight tiles of fewer than 128 rows: the products' other rows are whatever
-                // follows in shared memory, and are not read
-                const uint32_t wtile = (un.down ? a.rd : 2 * a.rg) * 128;
                 const uint32_t btile = un.down ? C::kHPlanes * w * 128 : C::kXTile;
                 // an accumulator a K tile, emptied every stage, where the scales change along K
                 const bool each = un.down ? FMT != 0 : FMT == 2;
-                for (int k = 0; k < un.n; k += q) {
+                for (int k = 0; k < un.n; k += kTiles) {
                     if (each || k == 0) {
                         if (!wait_bounded(&ctl->tempty[buf], bphase ^ 1u, ctl, a, 31)) { ok = false; break; }
                     }
@@ -752,12 +827,12 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                     ptx::tc_fence_after();
                     const uint32_t w0 = ptx::smem_u32(ring + stage * kStage), b0 = w0 + kABytes;
                     const uint32_t d0 = tmem + buf * 128;
-                    const int nk = min(q, un.n - k);
+                    const int nk = min(kTiles, un.n - k);
                     for (int i = 0; i < nk; ++i) {
                         const uint32_t acc = each ? d0 + i * n : d0;
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            const uint64_t wd = ptx::sw128_kmajor_desc(w0 + i * wtile + kk * 32);
+                            const uint64_t wd = ptx::sw128_kmajor_desc(w0 + i * kWTile + kk * 32);
                             const uint64_t bd = ptx::sw128_kmajor_desc(b0 + i * btile + kk * 32);
                             const bool fresh = kk == 0 && (each || (k == 0 && i == 0));
                             if constexpr (FMT) ptx::tc_mma_f8(acc, wd, bd, idesc, fresh ? 0u : 1u);
@@ -767,7 +842,7 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                     any = true;
                     ptx::tc_commit(&ctl->empty[stage]);
                     if (++stage == kStages) { stage = 0; phase ^= 1u; }
-                    if (each || k + q >= un.n) {
+                    if (each || k + kTiles >= un.n) {
                         ptx::tc_commit(&ctl->tfull[buf]);
                         if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
                     }
@@ -809,7 +884,7 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                     release(&ctl->summed[mine]);
                     break;
                 }
-                const Unit un = unit_at(sc, uid, shared);
+                const Unit un = unit_at(a, sc, uid, shared);
                 const bool sh = un.group < shared;
                 const int e = sh ? 0 : ctl->expert[un.group];
                 const uint32_t mask = ctl->mask[un.group];
@@ -819,159 +894,121 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                     float s[NT];
 #pragma unroll
                     for (int t = 0; t < NT; ++t) s[t] = 0.0f;
-                    const bool up = r >= a.rg;
-                    const int q = FMT == 2 ? a.qg : un.n;
+                    const bool up = r >= kGateRows;
+                    const int step = FMT == 2 ? kTiles : un.n;
                     // the thread's row scale, or its blocks' scales along K (asked for a stage ahead)
                     const float* sp = FMT ? (up ? (sh ? a.ss_up : a.s_up) : (sh ? a.ss_gate : a.s_gate))
                                           : nullptr;
-                    float rs = 1.0f, bs[8];
+                    float rs = 1.0f, bs[kTiles];
                     if constexpr (FMT == 1)
-                        if (r < 2 * a.rg)
-                            rs = __ldg(sp + (int64_t)e * I + un.tile * a.rg + (up ? r - a.rg : r));
+                        rs = __ldg(sp + (int64_t)e * I + un.tile * kGateRows + r % kGateRows);
                     if constexpr (FMT == 2)
-                        sp += ((int64_t)e * (I / 128) + un.tile * a.rg / 128) * (a.d / 128);
+                        sp += ((int64_t)e * (I / 128) + un.tile / 2) * (a.d / 128) + un.k0;
                     const auto ask = [&](int k) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) bs[i] = i < q && k + i < un.n ? __ldg(sp + k + i) : 0.0f;
+                        for (int i = 0; i < kTiles; ++i) bs[i] = k + i < un.n ? __ldg(sp + k + i) : 0.0f;
                     };
                     if constexpr (FMT == 2) ask(0);
-                    for (int k = 0; k < un.n; k += q) {
+                    for (int k = 0; k < un.n; k += step) {
                         if (!pass(&ctl->tfull[buf], bphase, 41)) { ok = false; break; }
                         ptx::tc_fence_after();
                         const uint32_t at = tmem + lanes + buf * 128;
+                        uint32_t v[FMT == 2 ? kTiles : 1][C::kXCols];
 #pragma unroll
-                        for (int i = 0; i < (FMT == 2 ? 8 : 1); ++i) {
-                            if (FMT == 2 && (i >= q || k + i >= un.n)) continue;
-                            uint32_t v[16], lo[16];
-                            ptx::tmem_ld16(at + i * C::kXCols, v);
-                            if constexpr (FMT && NT == 16) ptx::tmem_ld16(at + i * C::kXCols + 16, lo);
-                            ptx::tmem_ld_wait();
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                float x = __uint_as_float(v[t]);
-                                if constexpr (FMT)
-                                    x = fmaf(__uint_as_float(NT == 16 ? lo[t] : v[8 + (t & 7)]),
-                                             0.0625f, x);
-                                s[t] = FMT == 2 ? fmaf(x, bs[i], s[t]) : x;
-                            }
-                        }
+                        for (int i = 0; i < (FMT == 2 ? kTiles : 1); ++i) load_cols(at + i * C::kXCols, v[i]);
+                        ptx::tmem_ld_wait();
                         ptx::tc_fence_before();
                         release(&ctl->tempty[buf]);
                         if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
-                        if constexpr (FMT == 2) ask(k + q);
+#pragma unroll
+                        for (int i = 0; i < (FMT == 2 ? kTiles : 1); ++i) {
+                            if (FMT == 2 && k + i >= un.n) continue;  // not written
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                float x = __uint_as_float(v[i][t]);
+                                if constexpr (FMT) x = fmaf(__uint_as_float(v[i][NT + t]), 0.0625f, x);
+                                s[t] = FMT == 2 ? fmaf(x, bs[i], s[t]) : x;
+                            }
+                        }
+                        if constexpr (FMT == 2) ask(k + step);
                     }
                     if (!ok) break;
-                    if (r < 2 * a.rg) {
-                        int c = 0;
+                    int c = 0;
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            if (!(mask >> t & 1u)) continue;
-                            const float x = FMT ? ctl->xs[t] * rs : 1.0f;
-                            __stcg(gate_row(a, row0 + c, sh, shared) + un.tile * 2 * a.rg + r, s[t] * x);
-                            ++c;
-                        }
+                    for (int t = 0; t < NT; ++t) {
+                        if (!(mask >> t & 1u)) continue;
+                        const float x = FMT ? ctl->xs[t] * rs : 1.0f;
+                        __stcg(gate_sums(a, row0 + c, sh, shared, un.tile) + un.part * 2 * kGateRows + r,
+                               s[t] * x);
+                        ++c;
                     }
                 } else {
                     const int tokens = __popc(mask);
                     const int w = NT == 8 || tokens <= 8 ? 8 : 16;
-                    const int col = un.tile * a.rd + r;
-                    const bool mine_row = r < a.rd && col < a.d;
+                    const int col = un.tile * kDownRows + r;
                     float s[NT];
 #pragma unroll
                     for (int t = 0; t < NT; ++t) s[t] = 0.0f;
-                    const int q = FMT ? a.qd : un.n;
-                    float rs = 1.0f, bs[4], hv = 0.0f;
+                    const int step = FMT ? kTiles : un.n;
+                    float rs = 1.0f, bs[kTiles], hv = 0.0f;
                     const float* sp = FMT ? (sh ? a.ss_down : a.s_down) : nullptr;
-                    if constexpr (FMT == 1)
-                        if (mine_row) rs = __ldg(sp + (int64_t)e * a.d + col);
+                    if constexpr (FMT == 1) rs = __ldg(sp + (int64_t)e * a.d + col);  // d a multiple of 128
                     if constexpr (FMT == 2)
-                        sp += ((int64_t)e * (a.d / 128) + un.tile * a.rd / 128) * (I / 128);
+                        sp += ((int64_t)e * (a.d / 128) + un.tile) * (I / 128) + un.k0;
                     // scales of the stage from K tile k: h's go through shared memory (thread
                     // 16 i + c: tile k + i, token c), asked for a stage ahead
-                    const float* hs = FMT ? (sh ? a.hs_s : a.hs) +
+                    const float* hs = FMT ? (sh ? a.hs_s : a.hs) + un.k0 +
                                                 (int64_t)(row0 - (sh || !shared ? 0 : a.T)) * (I / 128)
                                           : nullptr;
                     const auto ask = [&](int k) {
                         const int i = r >> 4, c = r & 15;
-                        hv = i < q && k + i < un.n && c < tokens
+                        hv = i < kTiles && k + i < un.n && c < tokens
                                  ? __ldcg(hs + (int64_t)c * (I / 128) + k + i) : 0.0f;
                         if constexpr (FMT == 2)
 #pragma unroll
-                            for (int i2 = 0; i2 < 4; ++i2)
-                                bs[i2] = i2 < q && k + i2 < un.n ? __ldg(sp + k + i2) : 0.0f;
+                            for (int j = 0; j < kTiles; ++j) bs[j] = k + j < un.n ? __ldg(sp + k + j) : 0.0f;
                     };
                     int turn = 0;
-                    for (int k = 0; k < un.n; k += q, turn ^= 1) {
-                        if (FMT && k > 0 && r < 64) ctl->hscale[turn][r] = hv;
+                    for (int k = 0; k < un.n; k += step, turn ^= 1) {
+                        if (FMT && k > 0 && r < 16 * kTiles) ctl->hscale[turn][r] = hv;
                         if (!pass(&ctl->tfull[buf], bphase, 42)) { ok = false; break; }
                         ptx::tc_fence_after();
-                        float bsn[4] = {1.0f, 1.0f, 1.0f, 1.0f};
                         if constexpr (FMT) {
-                            if (k == 0) {
-                                // h is done: a product with it is
+                            if (k == 0) {  // h is done: a product with it is
                                 ask(0);
-                                if (r < 64) ctl->hscale[turn][r] = hv;
+                                if (r < 16 * kTiles) ctl->hscale[turn][r] = hv;
                                 asm volatile("bar.sync 1, 128;" ::: "memory");
                             }
-                            if constexpr (FMT == 2)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) bsn[i] = bs[i];
-                            ask(k + q);
                         }
                         const uint32_t at = tmem + lanes + buf * 128;
+                        float v[FMT ? kTiles : 1][NT];
+                        if (w == 8) down_cols<FMT, 8, NT>(at, v);
+                        else if constexpr (NT == 16) down_cols<FMT, 16, NT>(at, v);
+                        ptx::tc_fence_before();
+                        release(&ctl->tempty[buf]);
+                        if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
 #pragma unroll
-                        for (int i = 0; i < (FMT ? 4 : 1); ++i) {
-                            if (FMT && (i >= q || k + i >= un.n)) continue;
-                            const uint32_t ai = at + i * C::kHCols * w;
-                            float v[NT];
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) v[t] = 0.0f;
-                            if (w == 8) {
-                                uint32_t p01[16], p23[16];
-                                ptx::tmem_ld16(ai, p01);
-                                if constexpr (FMT) ptx::tmem_ld16(ai + 16, p23);
-                                ptx::tmem_ld_wait();
-#pragma unroll
-                                for (int t = 0; t < 8; ++t) {
-                                    const float hi = __uint_as_float(p01[t]);
-                                    const float lo = __uint_as_float(p01[8 + t]);
-                                    if constexpr (FMT)
-                                        v[t] = fmaf(fmaf(__uint_as_float(p23[t]), 0.0625f, lo), 0.0625f, hi);
-                                    else v[t] = hi + lo;
-                                }
-                            } else if constexpr (NT == 16) {
-                                uint32_t p0[16], p1[16], p2[16];
-                                ptx::tmem_ld16(ai, p0);
-                                ptx::tmem_ld16(ai + 16, p1);
-                                if constexpr (FMT) ptx::tmem_ld16(ai + 32, p2);
-                                ptx::tmem_ld_wait();
-#pragma unroll
-                                for (int t = 0; t < 16; ++t) {
-                                    const float hi = __uint_as_float(p0[t]), lo = __uint_as_float(p1[t]);
-                                    if constexpr (FMT)
-                                        v[t] = fmaf(fmaf(__uint_as_float(p2[t]), 0.0625f, lo), 0.0625f, hi);
-                                    else v[t] = hi + lo;
-                                }
-                            }
+                        for (int i = 0; i < (FMT ? kTiles : 1); ++i) {
+                            if (FMT && k + i >= un.n) continue;  // not written
+                            const float b = FMT == 2 ? bs[i] : 1.0f;
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
                                 if constexpr (FMT) {
                                     if (t < tokens)
-                                        s[t] = fmaf(v[t], ctl->hscale[turn][16 * i + t] * bsn[i], s[t]);
+                                        s[t] = fmaf(v[i][t], ctl->hscale[turn][16 * i + t] * b, s[t]);
                                 } else {
-                                    s[t] = v[t];
+                                    s[t] = v[i][t];
                                 }
                             }
                         }
-                        ptx::tc_fence_before();
-                        release(&ctl->tempty[buf]);
-                        if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
+                        if constexpr (FMT) ask(k + step);
                     }
                     if (!ok) break;
-                    if (mine_row) {
+                    if (col < a.d) {
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
-                            if (t < tokens) __stcg(a.yp + (int64_t)(row0 + t) * a.d + col, s[t] * rs);
+                            if (t < tokens)
+                                __stcg(a.yp + ((int64_t)(row0 + t) * a.dp + un.part) * a.d + col, s[t] * rs);
                     }
                 }
                 release(&ctl->summed[mine]);
@@ -986,17 +1023,15 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                 release(&ctl->qempty[slot]);
                 if (++slot == kQueue) { slot = 0; qphase ^= 1u; }
                 if (uid < 0) break;
-                const Unit un = unit_at(sc, uid, shared);
+                const Unit un = unit_at(a, sc, uid, shared);
                 if (!un.down) {
-                    if constexpr (FMT) {
-                        // the 128 rows that share h's scales
-                        const int blocks = max(a.I, a.Is) / 128, parts = 128 / a.rg;
-                        int* counter = a.gticket + un.group * blocks + un.tile / parts;
-                        if (!last_part(ctl, counter, parts, r)) continue;
-                    }
+                    // all parts of the tile; 8-bit: of the two tiles that share h's scales
+                    const int tiles = FMT ? max(a.I, a.Is) / 128 : max(sc.gr, sc.gs);
+                    int* counter = a.gticket + un.group * tiles + (FMT ? un.tile / 2 : un.tile);
+                    if (!last_part(ctl, counter, FMT ? 2 * a.gp : a.gp, r)) continue;
                     finish_h<FMT, NT>(a, ctl, un, r, shared);
-                } else if (last_part(ctl, a.dticket + un.tile, ctl->groups, r)) {
-                    join_tile(a, ctl, un.tile, r);
+                } else if (last_part(ctl, a.dticket + un.tile, ctl->groups * a.dp, r)) {
+                    join_tile(a, ctl, un.tile, warp & 3, lane);
                 }
             }
         }
@@ -1074,21 +1109,29 @@ cudaError_t go(const FewArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     // no more blocks than units, were every pick another expert's
     const int64_t groups = a.T * a.K < a.E ? a.T * a.K : a.E;
-    const int64_t units = a.Is / a.rg + groups * (a.I / a.rg) +
-                          (groups + (a.Is > 0)) * ceil_div(a.d, a.rd);
+    const int64_t units = a.gp * (a.Is + groups * a.I) / kGateRows +
+                          a.dp * (groups + (a.Is > 0)) * ceil_div(a.d, kDownRows);
     const int sms = device_sm_count();
     return launch_pdl(few_experts_kernel<FMT, NT>, dim3((unsigned)(units < sms ? units : sms)),
                       dim3(kThreads), smem, st, a);
 }
 
 constexpr int kClaimInts = 64;
-constexpr double kGateUnits = 0.01, kDownUnits = 0.01;
-
-int least(int a, int b, int c) { return a < b ? (a < c ? a : c) : (b < c ? b : c); }
+// Parts that K is cut into: enough that every block gets about this many units, were all
+// experts equally likely, with at least this many stages left in each.
+constexpr double kGateUnits = 2, kDownUnits = 3;
+constexpr int kLeastStages = 4;
 
 int score_splits(int d) {
     const int n = d / 8 / 96;  // about three 16-byte vectors a lane
     return n < 1 ? 1 : n > kScoreSplits ? kScoreSplits : n;
+}
+
+int parts_for(double tiles, double units, int64_t k_tiles) {
+    const double sms = 152;  // not asked of the device: the workspace query needs none
+    int p = 1;
+    while (p < 8 && tiles * p < units * sms && k_tiles / kTiles / (p + 1) >= kLeastStages) ++p;
+    return p;
 }
 
 }  // namespace
@@ -1098,7 +1141,11 @@ FewWs few_ws(const moe_shape& s, int fmt) {
     FewWs w{};
     const int64_t T = s.T, K = s.K, d = s.d, I = s.inter, Is = s.inter_shared, n = T * K;
     const int64_t groups = (n < s.E ? n : s.E) + 1;
-    const int64_t ti = ceil_div(I, 128), ts = ceil_div(Is, 128), td = ceil_div(d, 32);
+    const int64_t ti = ceil_div(I, 128), ts = ceil_div(Is, 128), td = ceil_div(d, kDownRows);
+    const double routed = s.E * (1.0 - pow(1.0 - (double)K / s.E, (double)T));
+    const int elems = fmt ? 128 : 64;
+    w.gp = parts_for((routed * I + Is) / kGateRows, kGateUnits, d / elems);
+    w.dp = parts_for((routed + (Is > 0)) * td, kDownUnits, (I > Is ? I : Is) / elems);
     w.splits = score_splits(s.d);
     size_t o = 256;  // the error record, then the counters
     auto take = [&](int64_t bytes) {
@@ -1107,17 +1154,17 @@ FewWs few_ws(const moe_shape& s, int fmt) {
         return at;
     };
     // the claims' counter in a cache line of its own
-    w.counters = (int)(kClaimInts + groups + td + (fmt ? groups * (ti > ts ? ti : ts) : 0));
+    w.counters = (int)(kClaimInts + groups + td + groups * 2 * (ti > ts ? ti : ts));
     w.claim = take(4 * (int64_t)w.counters);
     w.part = take(4 * (int64_t)w.splits * T * s.E);
     w.xq = take(fmt ? 2 * T * d : 0);
     w.xs = take(fmt ? 4 * T : 0);
-    w.gpart = take(8 * (n * I + T * Is));
+    w.gpart = take(8 * (n * I + T * Is) * w.gp);
     w.h = take(fmt ? 3 * n * I : 4 * n * I);
     w.h_s = take(fmt ? 3 * T * Is : 4 * T * Is);
     w.hs = take(fmt ? 4 * n * ti : 0);
     w.hs_s = take(fmt ? 4 * T * ts : 0);
-    w.yp = take(4 * (n + (Is ? T : 0)) * d);
+    w.yp = take(4 * (n + (Is ? T : 0)) * d * w.dp);
     w.total = o;
     return w;
 }
@@ -1140,7 +1187,7 @@ cudaError_t launch_few(const moe_shape& s, int fmt, const FewCall& c, void* work
     const int64_t groups = (n < E ? n : E) + 1;
     a.ready = a.claim + kClaimInts;
     a.dticket = a.ready + groups;
-    a.gticket = a.dticket + ceil_div(d, 32);
+    a.gticket = a.dticket + ceil_div(d, kDownRows);
     a.part = reinterpret_cast<float*>(base + w.part);
     a.xs = fmt ? reinterpret_cast<float*>(base + w.xs) : nullptr;
     a.gpart = reinterpret_cast<float*>(base + w.gpart);
@@ -1153,34 +1200,23 @@ cudaError_t launch_few(const moe_shape& s, int fmt, const FewCall& c, void* work
     a.ss_gate = c.ss_gate; a.ss_up = c.ss_up; a.ss_down = c.ss_down;
     a.timeout_ns = tc_timeout_ns();
     a.test_stall = tc_test_stall();
-    // Rows of a unit.  More rows spare copies of x and h beside the weights, fewer even out what
-    // the blocks get: the most that give every block about `kGateUnits` and `kDownUnits` of
-    // them, were all experts equally likely.
-    const double routed = E * (1.0 - pow(1.0 - (double)s.K / E, (double)T));
-    const double sms = device_sm_count();
-    a.rg = 64;
-    while (a.rg > 16 && (routed * I + Is) / a.rg < kGateUnits * sms) a.rg /= 2;
-    a.rd = 128;
-    while (a.rd > 32 && (routed + (Is > 0)) * d / a.rd < kDownUnits * sms) a.rd /= 2;
-    // K tiles of a stage: as many as the weights' and the rows' shares of it hold, and the
-    // accumulators where each tile has its own
-    const int elems = 128 / size, xcols = fmt ? 2 * nt : 16, hcols = (fmt ? 4 : 2) * nt;
-    a.qg = least(kABytes / (2 * a.rg * 128), kBBytes / (xcols * 128), fmt == 2 ? 128 / xcols : 8);
-    a.qd = least(kABytes / (a.rd * 128), kBBytes / ((fmt ? 3 : 2) * nt * 128), fmt ? 128 / hcols : 8);
-    bool ok = gate_map(&a.maps[kMapGate], c.w_gate, size, E, I, d, a.rg) &&
-              gate_map(&a.maps[kMapUp], c.w_up, size, E, I, d, a.rg) &&
-              down_map(&a.maps[kMapDown], c.w_down, size, E, d, I, a.rd, a.qd) &&
-              rows_map(&a.maps[kMapH8], a.h, size, fmt ? 3 : 2, n, I, 8, a.qd) &&
-              rows_map(&a.maps[kMapH16], a.h, size, fmt ? 3 : 2, n, I, nt, a.qd) &&
-              (fmt ? rows_map(&a.maps[kMapX], base + w.xq, 1, 2, T, d, nt, a.qg)
+    a.gp = w.gp;
+    a.dp = w.dp;
+    const int elems = 128 / size;
+    bool ok = gate_map(&a.maps[kMapGate], c.w_gate, size, E, I, d, kGateRows) &&
+              gate_map(&a.maps[kMapUp], c.w_up, size, E, I, d, kGateRows) &&
+              down_map(&a.maps[kMapDown], c.w_down, size, E, d, I, kDownRows, kTiles) &&
+              rows_map(&a.maps[kMapH8], a.h, size, fmt ? 3 : 2, n, I, 8, kTiles) &&
+              rows_map(&a.maps[kMapH16], a.h, size, fmt ? 3 : 2, n, I, nt, kTiles) &&
+              (fmt ? rows_map(&a.maps[kMapX], base + w.xq, 1, 2, T, d, nt, kTiles)
                    : make_map(&a.maps[kMapX], c.x, 2, 3, {elems, T, d / elems, 1}, {d * 2, 128, 0},
-                              {elems, 16, a.qg, 1}));
+                              {elems, 16, kTiles, 1}));
     if (Is > 0) {
-        ok = ok && gate_map(&a.maps[kMapSGate], c.ws_gate, size, 1, Is, d, a.rg) &&
-             gate_map(&a.maps[kMapSUp], c.ws_up, size, 1, Is, d, a.rg) &&
-             down_map(&a.maps[kMapSDown], c.ws_down, size, 1, d, Is, a.rd, a.qd) &&
-             rows_map(&a.maps[kMapHS8], a.h_s, size, fmt ? 3 : 2, T, Is, 8, a.qd) &&
-             rows_map(&a.maps[kMapHS16], a.h_s, size, fmt ? 3 : 2, T, Is, nt, a.qd);
+        ok = ok && gate_map(&a.maps[kMapSGate], c.ws_gate, size, 1, Is, d, kGateRows) &&
+             gate_map(&a.maps[kMapSUp], c.ws_up, size, 1, Is, d, kGateRows) &&
+             down_map(&a.maps[kMapSDown], c.ws_down, size, 1, d, Is, kDownRows, kTiles) &&
+             rows_map(&a.maps[kMapHS8], a.h_s, size, fmt ? 3 : 2, T, Is, 8, kTiles) &&
+             rows_map(&a.maps[kMapHS16], a.h_s, size, fmt ? 3 : 2, T, Is, nt, kTiles);
     } else {
         // never loaded from: any valid map
         a.maps[kMapSGate] = a.maps[kMapSUp] = a.maps[kMapGate];

@@ -305,7 +305,7 @@ cudaError_t launch_rmsnorm_backward(const NormArgs& a, cudaStream_t st);
 // few.cu: the whole layer for at most kFewMaxTokens tokens
 constexpr int kFewMaxTokens = 16;
 struct FewWs {
-    int splits, counters;
+    int splits, gp, dp, counters;
     size_t claim, part, xq, xs, gpart, h, h_s, hs, hs_s, yp, total;
 };
 FewWs few_ws(const moe_shape& s, int fmt);
