@@ -65,9 +65,9 @@ constexpr int kDownRows = 128;
 constexpr int kTiles = 2;      // K tiles of a stage
 constexpr int kWTile = 16384;  // bytes of a weight tile: 128 rows x 128 bytes
 constexpr int kABytes = kTiles * kWTile;
-constexpr int kBBytes = 16384; // the rows beside them
-constexpr int kStage = kABytes + kBBytes;
-constexpr int kStages = 4;
+constexpr int kMaxStages = 5;
+constexpr int kHint = 4096;    // bytes of an L2 prefetch
+constexpr int64_t kHintMost = 8 << 20;  // of each of two matrices
 
 // FMT: 0 bf16 weights, 1 E4M3 with a scale a row, 2 E4M3 with a scale per 128 x 128 block.
 // NT: columns that tokens take (8 or 16).
@@ -79,9 +79,13 @@ struct Cfg {
     // in shared memory and are not read.
     static constexpr int kXCols = FMT ? 2 * NT : 16, kHCols = FMT ? 4 : 2;
     static constexpr int kXTile = kXCols * 128;    // bytes beside one weight tile
-    // products with h read whole 16s of columns
-    static_assert(kTiles * kXTile <= kBBytes &&
-                      ((kTiles - 1) * kHPlanes + kHCols) * NT * 128 <= kBBytes, "rows fit the stage");
+    // a stage: the weights and the rows beside them (products with h read whole 16s of columns)
+    static constexpr int kXStage = kTiles * kXTile;
+    static constexpr int kHStage = ((kTiles - 1) * kHPlanes + kHCols) * NT * 128;
+    static constexpr int kStage = kABytes + (kXStage > kHStage ? kXStage : kHStage);
+    // Fewer in flight cost bandwidth (E4M3, T = 8: 5 stages 323 us, 4 326, 3 333, 2 370), more
+    // hold up what the joints wait for (bf16, T = 1, six experts of 1408: 5 stages 42 us, 6 44).
+    static constexpr int kStages = kStage <= 40960 ? 5 : 4;
     static_assert(kTiles * kHCols * NT <= 128, "a stage's accumulators fit a buffer");
 };
 
@@ -92,6 +96,8 @@ struct FewArgs {
     CUtensorMap maps[kMaps];
     int T, d, E, K, I, Is, sigmoid, splits, test_stall;
     int gp, dp;  // parts that a gate/up and a down tile's K is cut into
+    const uint8_t *ws_gate, *ws_up;  // the shared expert's, and their bytes to prefetch
+    int64_t hint;
     unsigned long long timeout_ns;
     const float* bias;
     const bf16* residual;
@@ -104,7 +110,7 @@ struct FewArgs {
 };
 
 struct Ctl {
-    uint64_t full[kStages], empty[kStages], tfull[kBufs], tempty[kBufs];
+    uint64_t full[kMaxStages], empty[kMaxStages], tfull[kBufs], tempty[kBufs];
     uint64_t qfull[kQueue], qempty[kQueue], summed[kQueue];
     uint32_t tmem;
     int abort_flag;
@@ -198,8 +204,12 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, Ctl
     }
 }
 
-__device__ __forceinline__ void fence_proxy_async_all() {
-    asm volatile("fence.proxy.async;" ::: "memory");
+// between h's stores, seen by way of an acquired count, and the asynchronous copies of it
+__device__ __forceinline__ void fence_proxy_async_global() {
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ int ld_acquire(const int* p) {
     int v;
@@ -618,8 +628,6 @@ __device__ __forceinline__ void finish_h(const FewArgs& a, Ctl* ctl, const Unit&
             }
         }
     }
-    // the copies that read h are of the asynchronous proxy
-    fence_proxy_async_all();
     finish_sync();
     if (r == 0)
         asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(a.ready + u.group) : "memory");
@@ -663,11 +671,11 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
     using C = Cfg<FMT, NT>;
     extern __shared__ uint8_t raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    Ctl* ctl = reinterpret_cast<Ctl*>(ring + kStages * kStage);
+    Ctl* ctl = reinterpret_cast<Ctl*>(ring + C::kStages * C::kStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int shared = a.Is > 0;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < C::kStages; ++i) {
             ptx::mbar_init(&ctl->full[i], 2);
             ptx::mbar_init(&ctl->empty[i], 1);
         }
@@ -688,6 +696,16 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
         ptx::tmem_relinquish();
     }
     if (warp == 2 && lane < kMaps) ptx::prefetch_tmap(&a.maps[lane]);
+    // The shared expert's weights are wanted whatever is chosen: the first of them go to L2
+    // while the scores are computed (a hint: nothing is read before the wait below).
+    if (warp == 1) {
+        for (int64_t at = ((int64_t)blockIdx.x * 32 + lane) * kHint; at < a.hint;
+             at += (int64_t)gridDim.x * 32 * kHint) {
+            const uint32_t n = (uint32_t)min((int64_t)kHint, a.hint - at);
+            prefetch_l2(a.ws_gate + at, n);
+            prefetch_l2(a.ws_up + at, n);
+        }
+    }
     pdl_wait();
     pdl_trigger();
     // thread 0's first claim: asked for here, answered while the experts are chosen
@@ -724,7 +742,7 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                 const int e = sh ? 0 : ctl->expert[un.group];
                 for (int k = un.k0; k < un.k0 + un.n; k += kTiles) {
                     if (!wait_bounded(&ctl->empty[stage], phase ^ 1u, ctl, a, 11)) { ok = false; break; }
-                    uint8_t* dst = ring + stage * kStage;
+                    uint8_t* dst = ring + stage * C::kStage;
                     uint64_t* bar = &ctl->full[stage];
                     if (!un.down) {
                         // a K tile's gate rows, then its up rows
@@ -741,7 +759,7 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                         tma_load_4d(dst, &a.maps[sh ? kMapSDown : kMapDown], bar, 0,
                                     un.tile * kDownRows, k, e);
                     }
-                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
                 }
             }
             if (ok) post(-1);
@@ -780,13 +798,13 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                     }
                     if (!ok) break;
                 }
-                fence_proxy_async_all();
+                fence_proxy_async_global();
             }
             const CUtensorMap* map =
                 &a.maps[w == 8 ? (sh ? kMapHS8 : kMapH8) : (sh ? kMapHS16 : kMapH16)];
             for (int k = un.k0; k < un.k0 + un.n; k += kTiles) {
                 if (!wait_bounded(&ctl->empty[stage], phase ^ 1u, ctl, a, 22)) { ok = false; break; }
-                uint8_t* dst = ring + stage * kStage + kABytes;
+                uint8_t* dst = ring + stage * C::kStage + kABytes;
                 uint64_t* bar = &ctl->full[stage];
                 if (!un.down) {
                     ptx::mbar_arrive_expect_tx(bar, kTiles * C::kXTile);
@@ -796,7 +814,7 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                     ptx::mbar_arrive_expect_tx(bar, kTiles * C::kHPlanes * w * 128);
                     tma_load_4d(dst, map, bar, 0, row0, 0, k);
                 }
-                if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
             }
         }
         }
@@ -825,7 +843,7 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                     }
                     if (!wait_bounded(&ctl->full[stage], phase, ctl, a, 32)) { ok = false; break; }
                     ptx::tc_fence_after();
-                    const uint32_t w0 = ptx::smem_u32(ring + stage * kStage), b0 = w0 + kABytes;
+                    const uint32_t w0 = ptx::smem_u32(ring + stage * C::kStage), b0 = w0 + kABytes;
                     const uint32_t d0 = tmem + buf * 128;
                     const int nk = min(kTiles, un.n - k);
                     for (int i = 0; i < nk; ++i) {
@@ -841,7 +859,7 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                     }
                     any = true;
                     ptx::tc_commit(&ctl->empty[stage]);
-                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
                     if (each || k + kTiles >= un.n) {
                         ptx::tc_commit(&ctl->tfull[buf]);
                         if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
@@ -1100,9 +1118,10 @@ bool rows_map(CUtensorMap* m, const void* base, int size, int64_t planes, int64_
 
 template <int FMT, int NT>
 cudaError_t go(const FewArgs& a, cudaStream_t st) {
-    constexpr size_t smem = 1024 + (size_t)kStages * kStage + sizeof(Ctl);
+    using C = Cfg<FMT, NT>;
+    constexpr size_t smem = 1024 + (size_t)C::kStages * C::kStage + sizeof(Ctl);
     static_assert(smem <= 232448, "shared memory exceeds the per-block limit");
-    static_assert(8u * kMaxT * 1024 <= (size_t)kStages * kStage, "keys and scores fit the ring");
+    static_assert(8u * kMaxT * 1024 <= (size_t)C::kStages * C::kStage, "keys and scores fit the ring");
     static_assert(sizeof(FewArgs) <= 4000, "the arguments fit the launch");
     cudaError_t e = cudaFuncSetAttribute(few_experts_kernel<FMT, NT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -1200,6 +1219,9 @@ cudaError_t launch_few(const moe_shape& s, int fmt, const FewCall& c, void* work
     a.ss_gate = c.ss_gate; a.ss_up = c.ss_up; a.ss_down = c.ss_down;
     a.timeout_ns = tc_timeout_ns();
     a.test_stall = tc_test_stall();
+    a.ws_gate = (const uint8_t*)c.ws_gate;
+    a.ws_up = (const uint8_t*)c.ws_up;
+    a.hint = Is * d * size < kHintMost ? Is * d * size : kHintMost;
     a.gp = w.gp;
     a.dp = w.dp;
     const int elems = 128 / size;

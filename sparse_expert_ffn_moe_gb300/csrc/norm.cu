@@ -21,8 +21,8 @@ namespace moe {
 
 namespace {
 
+constexpr int kTeamVecs = 64;      // widest row of a team, in vectors
 constexpr int kTeamThreads = 256;   // block of the variants whose team is part of a warp
-constexpr int kBlockThreads = 512;  // most threads of the variants whose team is the block
 
 __device__ __forceinline__ uint4 pack(const float (&f)[4], const float*) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
@@ -124,22 +124,33 @@ __device__ __forceinline__ void load_weight(const T* w, const Span<T, AL>& sp, i
     }
 }
 
-template <typename T, int TEAM, int VPT, bool AL>
-__global__ void __launch_bounds__(TEAM ? kTeamThreads : kBlockThreads, VPT <= 4 ? 2 : 1)
+// E4M3 codes of the values over the scale, four to a word
+template <int N>
+__device__ __forceinline__ void to_codes(const float (&f)[N], float inv_scale, uint32_t (&c)[N / 4]) {
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+            make_float2(f[4 * k] * inv_scale, f[4 * k + 1] * inv_scale), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+            make_float2(f[4 * k + 2] * inv_scale, f[4 * k + 3] * inv_scale), __NV_SATFINITE, __NV_E4M3);
+        c[k] = lo | hi << 16;
+    }
+}
+
+template <typename T, int TEAM, int VPT, bool AL, bool RES, bool CODES>
+__global__ void __launch_bounds__(kTeamThreads)
 rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, float eps, T* s_out,
                T* y, uint8_t* codes, float* __restrict__ scales, int64_t rows, int d) {
     constexpr int V = Elem<T>::kPerVec;
-    __shared__ float2 red[2][32];
     pdl_wait();
     pdl_trigger();
-    const int team = TEAM ? TEAM : blockDim.x;
-    const int lane = TEAM ? threadIdx.x % (TEAM ? TEAM : 1) : threadIdx.x;
-    const int per_block = TEAM ? kTeamThreads / (TEAM ? TEAM : 1) : 1;
+    constexpr int team = TEAM, per_block = kTeamThreads / TEAM;
+    const int lane = threadIdx.x % TEAM;
     const int64_t stride = (int64_t)gridDim.x * per_block;
     // every team of a block runs as many turns as its first, for the warp-wide shuffles
     const int64_t first = (int64_t)blockIdx.x * per_block;
     const int64_t turns = first < rows ? (rows - first + stride - 1) / stride : 0;
-    int64_t row = first + (TEAM ? threadIdx.x / (TEAM ? TEAM : 1) : 0);
+    int64_t row = first + threadIdx.x / TEAM;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     const float inv_d = 1.0f / (float)d;
     for (int64_t it = 0; it < turns; ++it, row += stride) {
@@ -151,7 +162,7 @@ rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, floa
             const int64_t e = sp.at(lane + j * team);
             sv[j] = live && sp.any(e) ? load_vec<T, AL>(x, sp, e) : zero;
         }
-        if (residual) {
+        if constexpr (RES) {
             uint4 rv[VPT];
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
@@ -175,19 +186,19 @@ rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, floa
             unpack(sv[j], f, (const T*)nullptr);
 #pragma unroll
             for (int k = 0; k < V; ++k) sum = fmaf(f[k], f[k], sum);
-            if (codes) {
+            if constexpr (CODES) {
                 load_weight<T, AL>(weight, sp, sp.at(lane + j * team), g);
 #pragma unroll
                 for (int k = 0; k < V; ++k) top = fmaxf(top, fabsf(f[k] * g[k]));
             }
         }
-        team_reduce<TEAM, true>(sum, top, red[it & 1]);
+        team_reduce<TEAM, true>(sum, top, nullptr);
         if (!live) continue;  // the last turn of a block of teams
         const float r = 1.0f / sqrtf(fmaf(sum, inv_d, eps));
         const float most = top * r;
         const float scale = most > 0.0f ? most / 448.0f : 1.0f;
         const float inv_scale = 1.0f / scale;
-        if (codes && lane == 0) scales[row] = scale;
+        if (CODES && lane == 0) scales[row] = scale;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int64_t e = sp.at(lane + j * team);
@@ -199,18 +210,9 @@ rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, floa
 #pragma unroll
             for (int k = 0; k < V; ++k) f[k] = f[k] * r * g[k];
             if (y) store_vec<T, AL>(y, sp, e, pack(f, (const T*)nullptr));
-            if (codes) {
+            if constexpr (CODES) {
                 uint32_t c[V / 4];
-#pragma unroll
-                for (int k = 0; k < V / 4; ++k) {
-                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-                        make_float2(f[4 * k] * inv_scale, f[4 * k + 1] * inv_scale), __NV_SATFINITE,
-                        __NV_E4M3);
-                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-                        make_float2(f[4 * k + 2] * inv_scale, f[4 * k + 3] * inv_scale),
-                        __NV_SATFINITE, __NV_E4M3);
-                    c[k] = lo | hi << 16;
-                }
+                to_codes(f, inv_scale, c);
                 if (sp.whole(e)) {
                     if constexpr (V == 8)
                         *reinterpret_cast<uint2*>(codes + e) = make_uint2(c[0], c[V / 4 - 1]);
@@ -223,6 +225,98 @@ rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, floa
                             codes[e + k] = (uint8_t)(c[k / 4] >> (8 * (k & 3)));
                 }
             }
+        }
+    }
+}
+
+// A wide row of whole vectors: a block of its own, which ends with it.  Many small blocks in
+// different parts of their rows keep the memory busy; blocks that stayed for many rows, with
+// or without a ring of copies ahead, did not (16384 x 7168 bf16 with residual and codes: 178
+// and 186 us, this 161).
+template <int VPT> constexpr int kBlockThreads = VPT <= 4 ? 256 : 512;
+
+template <typename T, int VPT, bool RES, bool CODES>
+__global__ void __launch_bounds__(kBlockThreads<VPT>, VPT <= 4 ? 4 : 1)
+rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight, float eps, T* s_out,
+                     T* y, uint8_t* codes, float* __restrict__ scales, int d) {
+    constexpr int V = Elem<T>::kPerVec;
+    __shared__ float2 red[32];
+    pdl_wait();
+    pdl_trigger();
+    const int nt = blockDim.x, vecs = d / V;
+    const int64_t at = (int64_t)blockIdx.x * d;
+    const uint4* px = reinterpret_cast<const uint4*>(x + at);
+    const uint4* pr = reinterpret_cast<const uint4*>(residual + at);
+    const T* const no = nullptr;
+    uint4 sv[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int c = threadIdx.x + j * nt;
+        sv[j] = c < vecs ? px[c] : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if constexpr (RES) {
+        uint4 rv[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = threadIdx.x + j * nt;
+            rv[j] = c < vecs ? pr[c] : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            float f[V], g[V];
+            unpack(sv[j], f, no);
+            unpack(rv[j], g, no);
+#pragma unroll
+            for (int k = 0; k < V; ++k) f[k] += g[k];
+            sv[j] = pack(f, no);
+        }
+        if (s_out) {  // may be x or the residual: this thread's values, read above
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int c = threadIdx.x + j * nt;
+                if (c < vecs) reinterpret_cast<uint4*>(s_out + at)[c] = sv[j];
+            }
+        }
+    }
+    float sum = 0.0f, top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int c = threadIdx.x + j * nt;
+        float f[V], g[V];
+        unpack(sv[j], f, no);
+#pragma unroll
+        for (int k = 0; k < V; ++k) sum = fmaf(f[k], f[k], sum);
+        if constexpr (CODES) {
+            if (c >= vecs) continue;
+            unpack(ld_ro(weight + c * V), g, no);
+#pragma unroll
+            for (int k = 0; k < V; ++k) top = fmaxf(top, fabsf(f[k] * g[k]));
+        }
+    }
+    team_reduce<0, true>(sum, top, red);
+    const float r = 1.0f / sqrtf(fmaf(sum, 1.0f / (float)d, eps));
+    const float most = top * r;
+    const float scale = most > 0.0f ? most / 448.0f : 1.0f;
+    const float inv_scale = 1.0f / scale;
+    if (CODES && threadIdx.x == 0) scales[blockIdx.x] = scale;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int c = threadIdx.x + j * nt;
+        if (c >= vecs) continue;
+        float f[V], g[V];
+        unpack(sv[j], f, no);
+        unpack(ld_ro(weight + c * V), g, no);
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] = f[k] * r * g[k];
+        if (!RES && s_out) reinterpret_cast<uint4*>(s_out + at)[c] = sv[j];
+        if (y) reinterpret_cast<uint4*>(y + at)[c] = pack(f, no);
+        if constexpr (CODES) {
+            uint32_t q[V / 4];
+            to_codes(f, inv_scale, q);
+            if constexpr (V == 8)
+                reinterpret_cast<uint2*>(codes + at)[c] = make_uint2(q[0], q[V / 4 - 1]);
+            else
+                reinterpret_cast<uint32_t*>(codes + at)[c] = q[0];
         }
     }
 }
@@ -243,25 +337,20 @@ __device__ __forceinline__ void open(const typename Raw<T, W>::type& v, float (&
     else unpack(v, f, (const T*)nullptr);
 }
 
-// block-sized teams: most threads, by the registers that a thread's columns take
-template <int W> constexpr int kBackThreads = W == 1 ? 1024 : 512;
-
 template <typename T, int TEAM, int VPT, int W>
-__global__ void __launch_bounds__(TEAM ? kTeamThreads : kBackThreads<W>, W > 1 && VPT <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(kTeamThreads)
 rmsnorm_backward_kernel(const T* d_y, const T* s, const T* __restrict__ weight, float eps,
                         const T* d_s, T* d_x, float* __restrict__ part, int64_t rows, int d) {
     using R = typename Raw<T, W>::type;
     extern __shared__ float acc_sm[];
-    __shared__ float2 red[2][32];
     pdl_wait();
     pdl_trigger();
-    const int team = TEAM ? TEAM : blockDim.x;
-    const int lane = TEAM ? threadIdx.x % (TEAM ? TEAM : 1) : threadIdx.x;
-    const int per_block = TEAM ? kTeamThreads / (TEAM ? TEAM : 1) : 1;
+    constexpr int team = TEAM, per_block = kTeamThreads / TEAM;
+    const int lane = threadIdx.x % TEAM;
     const int64_t stride = (int64_t)gridDim.x * per_block;
     const int64_t first = (int64_t)blockIdx.x * per_block;
     const int64_t turns = first < rows ? (rows - first + stride - 1) / stride : 0;
-    int64_t row = first + (TEAM ? threadIdx.x / (TEAM ? TEAM : 1) : 0);
+    int64_t row = first + threadIdx.x / TEAM;
     float acc[VPT][W];
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
@@ -293,7 +382,7 @@ rmsnorm_backward_kernel(const T* d_y, const T* s, const T* __restrict__ weight, 
                 gs = fmaf(fy[k] * fw[k], fs[k], gs);
             }
         }
-        team_reduce<TEAM, false>(sq, gs, red[it & 1]);
+        team_reduce<TEAM, false>(sq, gs, nullptr);
         const float r = 1.0f / sqrtf(fmaf(sq, inv_d, eps));
         const float back = gs * inv_d * r * r;  // times s: what the bracket takes off
 #pragma unroll
@@ -316,14 +405,7 @@ rmsnorm_backward_kernel(const T* d_y, const T* s, const T* __restrict__ weight, 
         }
     }
     if (!part) return;
-    if constexpr (TEAM == 0) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int k = 0; k < W; ++k)
-                if ((lane + j * team) * W < d)
-                    part[(int64_t)blockIdx.x * d + (lane + j * team) * W + k] = acc[j][k];
-    } else {
+    {
         // acc_sm[team of the block][columns of a team]
         constexpr int kCols = TEAM * VPT * W;
         const int mine = threadIdx.x / TEAM;
@@ -337,6 +419,297 @@ rmsnorm_backward_kernel(const T* d_y, const T* s, const T* __restrict__ weight, 
             for (int q = 0; q < kTeamThreads / TEAM; ++q) t += acc_sm[q * kCols + c];
             part[(int64_t)blockIdx.x * d + c] = t;
         }
+    }
+}
+
+// ---------------------------------------------------------------- rings
+// Blocks that stay for many rows copy the next ones to shared memory while they work on one
+// (cp.async: neither registers nor barriers hold the copies up).  Used where blocks have to
+// stay, for the sums of d_w over rows, and for rows that 16-byte vectors do not tile.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+constexpr int kDepth = 3;  // rows in a ring, or 1 where three do not fit
+
+constexpr int kRingThreads = 512;
+constexpr size_t kRingSmem = 220 * 1024;  // of an SM, for the rings of its blocks
+
+// Rows of whole vectors: each thread copies and reads its own.  s and d_y by way of the ring,
+// d_s straight to registers, asked for before the row's sums.
+template <typename T, int VPT>
+__global__ void __launch_bounds__(kRingThreads, VPT <= 2 ? 2 : 1)
+rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ weight, float eps,
+                             const T* d_s, T* d_x, float* __restrict__ part, int64_t rows, int d) {
+    constexpr int V = Elem<T>::kPerVec;
+    constexpr int D = VPT <= 4 ? kDepth : 1;  // 8 vectors: fp32 rows of more than 8192
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float2 red[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const int nt = blockDim.x, vecs = d / V, row_bytes = vecs * 16;
+    const bool add = d_s && d_x;
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+    const int64_t stride = gridDim.x;
+    const T* const no = nullptr;
+    auto fetch = [&](int64_t row, int slot) {
+        if (row < rows) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int c = threadIdx.x + j * nt;
+                if (c < vecs) {
+                    const uint32_t dst = base + slot * 2 * row_bytes + c * 16;
+                    copy_async(dst, s + row * d + c * V);
+                    copy_async(dst + row_bytes, d_y + row * d + c * V);
+                }
+            }
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) fetch(blockIdx.x + i * stride, i);
+    float acc[VPT][V];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[j][k] = 0.0f;
+    const float inv_d = 1.0f / (float)d;
+    int slot = 0, turn = 0;
+    for (int64_t row = blockIdx.x; row < rows; row += stride, turn ^= 1) {
+        uint4 av[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = threadIdx.x + j * nt;
+            av[j] = add && c < vecs ? *reinterpret_cast<const uint4*>(d_s + row * d + c * V)
+                                    : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if constexpr (D == 1) fetch(row, 0);
+        copy_wait<D == 1 ? 0 : D - 2>();
+        const uint8_t* mine = ring + slot * 2 * row_bytes;
+        float sq = 0.0f, gs = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = threadIdx.x + j * nt;
+            if (c >= vecs) continue;
+            float fs[V], fy[V], fw[V];
+            unpack(*reinterpret_cast<const uint4*>(mine + c * 16), fs, no);
+            unpack(*reinterpret_cast<const uint4*>(mine + row_bytes + c * 16), fy, no);
+            unpack(ld_ro(weight + c * V), fw, no);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                sq = fmaf(fs[k], fs[k], sq);
+                gs = fmaf(fy[k] * fw[k], fs[k], gs);
+            }
+        }
+        team_reduce<0, false>(sq, gs, red[turn]);
+        // into the place of the row before this one, used up before the barrier
+        if constexpr (D > 1) fetch(row + (D - 1) * stride, slot == 0 ? D - 1 : slot - 1);
+        const float r = 1.0f / sqrtf(fmaf(sq, inv_d, eps));
+        const float back = gs * inv_d * r * r;  // times s: what the bracket takes off
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = threadIdx.x + j * nt;
+            if (c >= vecs) continue;
+            float fs[V], fy[V], fw[V], fa[V];
+            unpack(*reinterpret_cast<const uint4*>(mine + c * 16), fs, no);
+            unpack(*reinterpret_cast<const uint4*>(mine + row_bytes + c * 16), fy, no);
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[j][k] = fmaf(fy[k], fs[k] * r, acc[j][k]);
+            if (!d_x) continue;
+            unpack(ld_ro(weight + c * V), fw, no);
+            unpack(av[j], fa, no);
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                fa[k] = fmaf(r, fmaf(-back, fs[k], fy[k] * fw[k]), fa[k]);
+            *reinterpret_cast<uint4*>(d_x + row * d + c * V) = pack(fa, no);
+        }
+        if (++slot == D) slot = 0;
+    }
+    copy_wait<0>();
+    if (!part) return;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int c = threadIdx.x + j * nt;
+        if (c >= vecs) continue;
+#pragma unroll
+        for (int k = 0; k < V; ++k) part[(int64_t)blockIdx.x * d + c * V + k] = acc[j][k];
+    }
+}
+
+// Rows that start within a vector: the ring holds the whole vectors that cover a row, and a
+// thread reads the elements of its columns, the same in every row.
+template <typename T>
+struct Window {
+    int bytes;  // of a slot's array
+    __device__ __forceinline__ explicit Window(int d) : bytes((d * (int)sizeof(T) + 15 + 15) / 16 * 16) {}
+    // bytes of the row before its first element
+    __device__ __forceinline__ static int skip(int64_t row, int d) {
+        return (int)((row * d * (int64_t)sizeof(T)) & 15);
+    }
+    // copies the vectors; those that reach past the array's end go by element
+    __device__ __forceinline__ void fetch(uint32_t dst, uint8_t* to, const T* p, int64_t row, int d,
+                                          int64_t rows) const {
+        const int64_t b0 = row * d * (int64_t)sizeof(T), from = b0 & ~(int64_t)15;
+        const int64_t end = b0 + d * (int64_t)sizeof(T), total = rows * d * (int64_t)sizeof(T);
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(p);
+        for (int64_t at = from + threadIdx.x * 16; at < end; at += blockDim.x * 16) {
+            if (at + 16 <= total) {
+                copy_async(dst + (uint32_t)(at - from), src + at);
+            } else {
+                for (int64_t e = at; e < end; e += sizeof(T))
+                    *reinterpret_cast<T*>(to + (e - from)) = *reinterpret_cast<const T*>(src + e);
+            }
+        }
+    }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kRingThreads, 2)
+rmsnorm_window_kernel(const T* x, const T* residual, const T* __restrict__ weight, float eps, T* s_out,
+                      T* y, uint8_t* codes, float* __restrict__ scales, int64_t rows, int d) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float2 red[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const Window<T> win(d);
+    const int arrays = residual ? 2 : 1;
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+    const int64_t stride = gridDim.x;
+    auto fetch = [&](int64_t row, int slot) {
+        if (row < rows) {
+            const int at = slot * arrays * win.bytes;
+            win.fetch(base + at, ring + at, x, row, d, rows);
+            if (residual) win.fetch(base + at + win.bytes, ring + at + win.bytes, residual, row, d, rows);
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) fetch(blockIdx.x + i * stride, i);
+    const float inv_d = 1.0f / (float)d;
+    int slot = 0, turn = 0;
+    for (int64_t row = blockIdx.x; row < rows; row += stride, turn ^= 1) {
+        if constexpr (D == 1) {
+            __syncthreads();  // everyone is done with the last row
+            fetch(row, 0);
+            copy_wait<0>();
+        } else {
+            copy_wait<D - 2>();
+        }
+        __syncthreads();  // everyone's copies of this row are there (and the last row is done with)
+        if constexpr (D > 1) fetch(row + (D - 1) * stride, slot == 0 ? D - 1 : slot - 1);
+        const uint8_t* at = ring + slot * arrays * win.bytes + Window<T>::skip(row, d);
+        const T* px = reinterpret_cast<const T*>(at);
+        const T* pr = reinterpret_cast<const T*>(at + win.bytes);
+        const auto value = [&](int c) {  // as the residual stream holds it
+            float v = Elem<T>::to_f32(px[c]);
+            if (residual) v = Elem<T>::to_f32(Elem<T>::from_f32(v + Elem<T>::to_f32(pr[c])));
+            return v;
+        };
+        float sum = 0.0f, top = 0.0f;
+#pragma unroll 4
+        for (int c = threadIdx.x; c < d; c += blockDim.x) {
+            const float v = value(c);
+            sum = fmaf(v, v, sum);
+            if (codes) top = fmaxf(top, fabsf(v * Elem<T>::to_f32(__ldg(weight + c))));
+        }
+        team_reduce<0, true>(sum, top, red[turn]);
+        const float r = 1.0f / sqrtf(fmaf(sum, inv_d, eps));
+        const float most = top * r;
+        const float scale = most > 0.0f ? most / 448.0f : 1.0f;
+        const float inv_scale = 1.0f / scale;
+        if (codes && threadIdx.x == 0) scales[row] = scale;
+        const int64_t e = row * d;
+#pragma unroll 4
+        for (int c = threadIdx.x; c < d; c += blockDim.x) {
+            const float v = value(c);
+            if (s_out) s_out[e + c] = Elem<T>::from_f32(v);
+            const float o = v * r * Elem<T>::to_f32(__ldg(weight + c));
+            if (y) y[e + c] = Elem<T>::from_f32(o);
+            if (codes) codes[e + c] = __nv_cvt_float_to_fp8(o * inv_scale, __NV_SATFINITE, __NV_E4M3);
+        }
+        if (++slot == D) slot = 0;
+    }
+    copy_wait<0>();
+}
+
+template <typename T, int EPT, int D>
+__global__ void __launch_bounds__(kRingThreads, EPT <= 16 ? 2 : 1)
+rmsnorm_backward_window_kernel(const T* d_y, const T* s, const T* __restrict__ weight, float eps,
+                               const T* d_s, T* d_x, float* __restrict__ part, int64_t rows, int d) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float2 red[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const Window<T> win(d);
+    const bool add = d_s && d_x;
+    const int nt = blockDim.x;
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+    const int64_t stride = gridDim.x;
+    auto fetch = [&](int64_t row, int slot) {
+        if (row < rows) {
+            const int at = slot * 3 * win.bytes;
+            win.fetch(base + at, ring + at, s, row, d, rows);
+            win.fetch(base + at + win.bytes, ring + at + win.bytes, d_y, row, d, rows);
+            if (add)
+                win.fetch(base + at + 2 * win.bytes, ring + at + 2 * win.bytes, d_s, row, d, rows);
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) fetch(blockIdx.x + i * stride, i);
+    float acc[EPT];
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) acc[j] = 0.0f;
+    const float inv_d = 1.0f / (float)d;
+    int slot = 0, turn = 0;
+    for (int64_t row = blockIdx.x; row < rows; row += stride, turn ^= 1) {
+        if constexpr (D == 1) {
+            __syncthreads();  // everyone is done with the last row
+            fetch(row, 0);
+            copy_wait<0>();
+        } else {
+            copy_wait<D - 2>();
+        }
+        __syncthreads();  // everyone's copies of this row are there (and the last row is done with)
+        if constexpr (D > 1) fetch(row + (D - 1) * stride, slot == 0 ? D - 1 : slot - 1);
+        const uint8_t* at = ring + slot * 3 * win.bytes + Window<T>::skip(row, d);
+        const T* ps = reinterpret_cast<const T*>(at);
+        const T* py = reinterpret_cast<const T*>(at + win.bytes);
+        const T* pa = reinterpret_cast<const T*>(at + 2 * win.bytes);
+        float sq = 0.0f, gs = 0.0f;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const int c = threadIdx.x + j * nt;
+            if (c >= d) continue;
+            const float fs = Elem<T>::to_f32(ps[c]);
+            sq = fmaf(fs, fs, sq);
+            gs = fmaf(Elem<T>::to_f32(py[c]) * Elem<T>::to_f32(__ldg(weight + c)), fs, gs);
+        }
+        team_reduce<0, false>(sq, gs, red[turn]);
+        const float r = 1.0f / sqrtf(fmaf(sq, inv_d, eps));
+        const float back = gs * inv_d * r * r;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const int c = threadIdx.x + j * nt;
+            if (c >= d) continue;
+            const float fs = Elem<T>::to_f32(ps[c]), fy = Elem<T>::to_f32(py[c]);
+            acc[j] = fmaf(fy, fs * r, acc[j]);
+            if (!d_x) continue;
+            const float g = fy * Elem<T>::to_f32(__ldg(weight + c));
+            d_x[row * d + c] = Elem<T>::from_f32(
+                fmaf(r, fmaf(-back, fs, g), add ? Elem<T>::to_f32(pa[c]) : 0.0f));
+        }
+        if (++slot == D) slot = 0;
+    }
+    copy_wait<0>();
+    if (!part) return;
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+        const int c = threadIdx.x + j * nt;
+        if (c < d) part[(int64_t)blockIdx.x * d + c] = acc[j];
     }
 }
 
@@ -367,38 +740,91 @@ int blocks_that_fit(K kernel, int threads, size_t smem) {
     return (n > 0 ? n : 1) * device_sm_count();
 }
 
+// launches kernel<..., RES, CODES> by what the call wants
+#define MOE_NORM_FLAGS(GO)                        \
+    do {                                          \
+        if (a.residual) {                         \
+            if (a.codes) return GO(true, true);   \
+            return GO(true, false);               \
+        }                                         \
+        if (a.codes) return GO(false, true);      \
+        return GO(false, false);                  \
+    } while (0)
+
 template <typename T, int TEAM, int VPT, bool AL>
-cudaError_t go_forward(const NormArgs& a, int threads, cudaStream_t st) {
-    auto kernel = rmsnorm_kernel<T, TEAM, VPT, AL>;
-    const int per_block = TEAM ? kTeamThreads / (TEAM ? TEAM : 1) : 1;
-    const int64_t want = ceil_div(a.rows, per_block);
-    const int64_t wave = blocks_that_fit(kernel, threads, 0);
-    return launch_pdl(kernel, dim3((unsigned)(want < wave ? want : wave)), dim3(threads), 0, st,
-                      (const T*)a.x, (const T*)a.residual, (const T*)a.weight, a.eps, (T*)a.s,
-                      (T*)a.y, a.codes, a.scales, a.rows, a.d);
+cudaError_t go_teams(const NormArgs& a, cudaStream_t st) {
+    const auto go = [&](auto kernel) {
+        const int64_t want = ceil_div(a.rows, kTeamThreads / TEAM);
+        const int64_t wave = blocks_that_fit(kernel, kTeamThreads, 0);
+        return launch_pdl(kernel, dim3((unsigned)(want < wave ? want : wave)), dim3(kTeamThreads), 0, st,
+                          (const T*)a.x, (const T*)a.residual, (const T*)a.weight, a.eps, (T*)a.s,
+                          (T*)a.y, a.codes, a.scales, a.rows, a.d);
+    };
+#define MOE_GO(RES, CODES) go(rmsnorm_kernel<T, TEAM, VPT, AL, RES, CODES>)
+    MOE_NORM_FLAGS(MOE_GO);
+#undef MOE_GO
+}
+
+template <typename T, int VPT>
+cudaError_t go_blocks(const NormArgs& a, cudaStream_t st) {
+    const auto go = [&](auto kernel) {
+        const int64_t lanes = ceil_div(a.d, Elem<T>::kPerVec * VPT);
+        return launch_pdl(kernel, dim3((unsigned)a.rows), dim3((unsigned)ceil_div(lanes, 32) * 32), 0, st,
+                          (const T*)a.x, (const T*)a.residual, (const T*)a.weight, a.eps, (T*)a.s,
+                          (T*)a.y, a.codes, a.scales, a.d);
+    };
+#define MOE_GO(RES, CODES) go(rmsnorm_block_kernel<T, VPT, RES, CODES>)
+    MOE_NORM_FLAGS(MOE_GO);
+#undef MOE_GO
 }
 
 template <typename T, bool AL>
-cudaError_t pick_forward(const NormArgs& a, cudaStream_t st) {
-    // vectors that cover a row, wherever it starts
-    const int nv = (int)ceil_div(a.d, Elem<T>::kPerVec) + (AL ? 0 : 1);
-    if (nv <= 4) return go_forward<T, 4, 1, AL>(a, kTeamThreads, st);
-    if (nv <= 8) return go_forward<T, 8, 1, AL>(a, kTeamThreads, st);
-    if (nv <= 16) return go_forward<T, 16, 1, AL>(a, kTeamThreads, st);
-    if (nv <= 32) return go_forward<T, 32, 1, AL>(a, kTeamThreads, st);
-    if (nv <= 64) return go_forward<T, 32, 2, AL>(a, kTeamThreads, st);
-    if (nv <= 128) return go_forward<T, 32, 4, AL>(a, kTeamThreads, st);
-    const auto warps = [](int64_t lanes) { return (int)ceil_div(lanes, 32) * 32; };
-    if (nv <= 2 * kBlockThreads) return go_forward<T, 0, 2, AL>(a, warps(ceil_div(nv, 2)), st);
-    // the widest row (16384 values) has 4096 vectors of fp32 or 2048 of bf16, and one
-    // more where it starts within a vector
-    if constexpr (Elem<T>::kPerVec == 4) {
-        if (nv > 4 * kBlockThreads)
-            return go_forward<T, 0, AL ? 8 : 9, AL>(a, warps(ceil_div(nv, AL ? 8 : 9)), st);
-        return go_forward<T, 0, 4, AL>(a, warps(ceil_div(nv, 4)), st);
-    } else {
-        return go_forward<T, 0, AL ? 4 : 5, AL>(a, warps(ceil_div(nv, AL ? 4 : 5)), st);
-    }
+cudaError_t teams_for(const NormArgs& a, int nv, cudaStream_t st) {
+    if (nv <= 4) return go_teams<T, 4, 1, AL>(a, st);
+    if (nv <= 8) return go_teams<T, 8, 1, AL>(a, st);
+    if (nv <= 16) return go_teams<T, 16, 1, AL>(a, st);
+    if (nv <= 32) return go_teams<T, 32, 1, AL>(a, st);
+    return go_teams<T, 32, 2, AL>(a, st);
+}
+
+int threads_for(int64_t lanes) { return (int)ceil_div(lanes, 32) * 32; }
+
+// Blocks an SM for a ring of `smem` bytes and blocks of `threads`, by what a GB300's SM has.
+int ring_blocks(size_t smem, int threads) {
+    const int by_smem = (int)(kRingSmem / smem), by_threads = 1024 / threads;
+    const int n = by_smem < by_threads ? by_smem : by_threads;
+    return n < 1 ? 1 : n > 16 ? 16 : n;
+}
+
+struct RingPlan {
+    int per_thread, threads, per_sm, depth;  // per_thread: columns
+    size_t smem;
+};
+
+// rows that start within vectors, more than 64 of them
+RingPlan window_plan(int dtype, int d, int arrays) {
+    RingPlan p{};
+    const int size = dtype == MOE_BF16 ? 2 : 4;
+    p.smem = (size_t)arrays * ((d * size + 30) / 16 * 16);
+    p.depth = kDepth * p.smem <= kRingSmem ? kDepth : 1;
+    p.smem *= p.depth;
+    p.per_thread = 4;
+    while (p.per_thread < 32 && d > p.per_thread * 256) p.per_thread *= 2;
+    p.threads = threads_for(ceil_div(d, p.per_thread));
+    p.per_sm = ring_blocks(p.smem, p.threads);
+    return p;
+}
+
+template <typename T>
+cudaError_t go_window(const NormArgs& a, cudaStream_t st) {
+    const RingPlan p = window_plan(a.dtype, a.d, a.residual ? 2 : 1);
+    auto kernel = p.depth == 1 ? rmsnorm_window_kernel<T, 1> : rmsnorm_window_kernel<T, kDepth>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+    if (e != cudaSuccess) return e;
+    const int64_t wave = blocks_that_fit(kernel, p.threads, p.smem);
+    return launch_pdl(kernel, dim3((unsigned)(a.rows < wave ? a.rows : wave)), dim3(p.threads), p.smem,
+                      st, (const T*)a.x, (const T*)a.residual, (const T*)a.weight, a.eps, (T*)a.s,
+                      (T*)a.y, a.codes, a.scales, a.rows, a.d);
 }
 
 template <typename T, int TEAM, int VPT, int W>
@@ -410,88 +836,114 @@ cudaError_t go_backward(const NormArgs& a, int threads, int blocks, cudaStream_t
                       a.rows, a.d);
 }
 
-// lanes of a team (0: a block of threads) and vectors a lane for rows of nv vectors
-struct Team {
-    int lanes, vpt, threads;
-};
-
-Team team_for(int nv, bool vec) {
-    if (nv <= 4) return {4, 1, kTeamThreads};
-    if (nv <= 8) return {8, 1, kTeamThreads};
-    if (nv <= 16) return {16, 1, kTeamThreads};
-    if (nv <= 32) return {32, 1, kTeamThreads};
-    if (nv <= 64) return {32, 2, kTeamThreads};
-    if (nv <= 128) return {32, 4, kTeamThreads};
-    const auto warps = [](int64_t lanes) { return (int)ceil_div(lanes, 32) * 32; };
-    const int most = vec ? kBackThreads<8> : kBackThreads<1>;
-    if (nv <= 2 * most) return {0, 2, warps(ceil_div(nv, 2))};
-    if (nv <= 4 * most) return {0, 4, warps(ceil_div(nv, 4))};
-    return vec ? Team{0, 8, warps(ceil_div(nv, 8))} : Team{0, 16, warps(ceil_div(nv, 16))};
-}
-
-template <typename T, int W>
-cudaError_t pick_backward(const NormArgs& a, const Team& t, int blocks, cudaStream_t st) {
-    if (t.lanes == 4) return go_backward<T, 4, 1, W>(a, t.threads, blocks, st);
-    if (t.lanes == 8) return go_backward<T, 8, 1, W>(a, t.threads, blocks, st);
-    if (t.lanes == 16) return go_backward<T, 16, 1, W>(a, t.threads, blocks, st);
-    if (t.lanes == 32 && t.vpt == 1) return go_backward<T, 32, 1, W>(a, t.threads, blocks, st);
-    if (t.lanes == 32 && t.vpt == 2) return go_backward<T, 32, 2, W>(a, t.threads, blocks, st);
-    if (t.lanes == 32) return go_backward<T, 32, 4, W>(a, t.threads, blocks, st);
-    if (t.vpt == 2) return go_backward<T, 0, 2, W>(a, t.threads, blocks, st);
-    if (t.vpt == 4) return go_backward<T, 0, 4, W>(a, t.threads, blocks, st);
-    if constexpr (W == 8) return cudaErrorInvalidValue;  // 16384 bf16 values: 4 vectors a thread
-    else return go_backward<T, 0, W == 1 ? 16 : 8, W>(a, t.threads, blocks, st);
+template <typename T>
+cudaError_t forward(const NormArgs& a, cudaStream_t st) {
+    constexpr int V = Elem<T>::kPerVec;
+    if (a.d % V) {
+        const int nv = (int)ceil_div(a.d, V) + 1;  // vectors that cover a row, wherever it starts
+        return nv <= kTeamVecs ? teams_for<T, false>(a, nv, st) : go_window<T>(a, st);
+    }
+    const int nv = a.d / V;
+    if (nv <= kTeamVecs) return teams_for<T, true>(a, nv, st);
+    if (nv <= 2 * kBlockThreads<2>) return go_blocks<T, 2>(a, st);
+    if (nv <= 4 * kBlockThreads<4>) return go_blocks<T, 4>(a, st);
+    return go_blocks<T, 8>(a, st);
 }
 
 // 16-byte vectors tile the rows
 bool whole_vectors(int dtype, int d) { return d % (dtype == MOE_BF16 ? 8 : 4) == 0; }
 
-Team backward_team(int dtype, int d) {
+// How the backward pass runs: teams within a warp (lanes > 0) of `per_thread` vectors (or
+// elements, where vectors do not tile the rows) a lane, or a ring a block.
+struct BackPlan {
+    int lanes, per_thread, threads, blocks, depth;
+    size_t smem;
+};
+
+// The blocks, and with them the partial rows of d_w, are counted for 152 SMs and not asked of
+// the device, whatever gradients are wanted: the workspace query needs no device, and the
+// order of the sums depends on the sizes alone.
+BackPlan back_plan(int dtype, int64_t rows, int d) {
+    BackPlan p{};
     const bool vec = whole_vectors(dtype, d);
-    return team_for(vec ? d / (dtype == MOE_BF16 ? 8 : 4) : d, vec);
+    const int nv = vec ? d / (dtype == MOE_BF16 ? 8 : 4) : d;
+    int64_t want = rows, wave;
+    if (nv <= kTeamVecs) {
+        p.lanes = nv <= 4 ? 4 : nv <= 8 ? 8 : nv <= 16 ? 16 : 32;
+        p.per_thread = nv <= 32 ? 1 : 2;
+        p.threads = kTeamThreads;
+        want = ceil_div(rows, kTeamThreads / p.lanes);
+        wave = 152 * 4;
+    } else if (vec) {
+        p.per_thread = nv <= 2 * kRingThreads ? 2 : nv <= 4 * kRingThreads ? 4 : 8;
+        p.threads = threads_for(ceil_div(nv, p.per_thread));
+        p.smem = (size_t)(p.per_thread <= 4 ? kDepth : 1) * 2 * nv * 16;
+        wave = 152 * ring_blocks(p.smem, p.threads);
+    } else {
+        const RingPlan w = window_plan(dtype, d, 3);
+        p.per_thread = w.per_thread;
+        p.threads = w.threads;
+        p.smem = w.smem;
+        p.depth = w.depth;
+        wave = 152 * w.per_sm;
+    }
+    p.blocks = (int)(want < wave ? want : wave);
+    return p;
+}
+
+template <typename T, int W>
+cudaError_t back_teams(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
+    if (p.lanes == 4) return go_backward<T, 4, 1, W>(a, p.threads, p.blocks, st);
+    if (p.lanes == 8) return go_backward<T, 8, 1, W>(a, p.threads, p.blocks, st);
+    if (p.lanes == 16) return go_backward<T, 16, 1, W>(a, p.threads, p.blocks, st);
+    if (p.per_thread == 1) return go_backward<T, 32, 1, W>(a, p.threads, p.blocks, st);
+    return go_backward<T, 32, 2, W>(a, p.threads, p.blocks, st);
+}
+
+template <typename T>
+cudaError_t backward(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
+    constexpr int V = Elem<T>::kPerVec;
+    const bool vec = whole_vectors(a.dtype, a.d);
+    if (p.lanes) return vec ? back_teams<T, V>(a, p, st) : back_teams<T, 1>(a, p, st);
+    const auto go = [&](auto kernel) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kernel, dim3(p.blocks), dim3(p.threads), p.smem, st, (const T*)a.d_y,
+                          (const T*)a.x, (const T*)a.weight, a.eps, (const T*)a.d_s, (T*)a.d_x, a.part,
+                          a.rows, a.d);
+    };
+    if (!vec) {
+        // up to 4096 columns three rows of three arrays fit
+        if (p.per_thread == 4) return go(rmsnorm_backward_window_kernel<T, 4, kDepth>);
+        if (p.per_thread == 8) return go(rmsnorm_backward_window_kernel<T, 8, kDepth>);
+        if (p.per_thread == 16) return go(rmsnorm_backward_window_kernel<T, 16, kDepth>);
+        if (p.depth == 1) return go(rmsnorm_backward_window_kernel<T, 32, 1>);
+        return go(rmsnorm_backward_window_kernel<T, 32, kDepth>);
+    }
+    if (p.per_thread == 2) return go(rmsnorm_backward_ring_kernel<T, 2>);
+    if constexpr (V == 4)
+        if (p.per_thread == 8) return go(rmsnorm_backward_ring_kernel<T, 8>);
+    return go(rmsnorm_backward_ring_kernel<T, 4>);
 }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t st) {
-    const bool al = whole_vectors(a.dtype, a.d);
-    if (a.dtype == MOE_BF16)
-        return al ? pick_forward<bf16, true>(a, st) : pick_forward<bf16, false>(a, st);
-    return al ? pick_forward<float, true>(a, st) : pick_forward<float, false>(a, st);
+    return a.dtype == MOE_BF16 ? forward<bf16>(a, st) : forward<float>(a, st);
 }
 
-// Partial rows of d_w: counted for 152 SMs, not asked of the device, so that the
-// workspace query needs no device and the order of the sums depends on the sizes alone.
 int rmsnorm_backward_blocks(int64_t rows, int d) {
-    // the larger of the two types' counts (their teams may differ)
-    int most = 1;
-    for (int dtype : {(int)MOE_F32, (int)MOE_BF16}) {
-        const Team t = backward_team(dtype, d);
-        const int per_block = t.lanes ? kTeamThreads / t.lanes : 1;
-        const int wave = 152 * (t.lanes ? 4 : t.threads > 512 ? 1 : 1024 / t.threads);
-        const int64_t want = ceil_div(rows, per_block);
-        const int n = (int)(want < wave ? want : wave);
-        most = n > most ? n : most;
-    }
-    return most;
+    const int a = back_plan(MOE_F32, rows, d).blocks, b = back_plan(MOE_BF16, rows, d).blocks;
+    return a > b ? a : b;
 }
 
 cudaError_t launch_rmsnorm_backward(const NormArgs& a, cudaStream_t st) {
-    const Team t = backward_team(a.dtype, a.d);
-    const int per_block = t.lanes ? kTeamThreads / t.lanes : 1;
-    const int wave = 152 * (t.lanes ? 4 : t.threads > 512 ? 1 : 1024 / t.threads);
-    const int64_t want = ceil_div(a.rows, per_block);
-    const int blocks = (int)(want < wave ? want : wave);
-    cudaError_t e;
-    const bool vec = whole_vectors(a.dtype, a.d);
-    if (a.dtype == MOE_BF16)
-        e = vec ? pick_backward<bf16, 8>(a, t, blocks, st) : pick_backward<bf16, 1>(a, t, blocks, st);
-    else
-        e = vec ? pick_backward<float, 4>(a, t, blocks, st)
-                : pick_backward<float, 1>(a, t, blocks, st);
+    const BackPlan p = back_plan(a.dtype, a.rows, a.d);
+    const cudaError_t e = a.dtype == MOE_BF16 ? backward<bf16>(a, p, st) : backward<float>(a, p, st);
     if (e != cudaSuccess || !a.part) return e;
     return launch_pdl(rmsnorm_dw_kernel, dim3((unsigned)ceil_div(a.d, 32)), dim3(1024), 0, st,
-                      (const float*)a.part, blocks, a.d, a.d_weight);
+                      (const float*)a.part, p.blocks, a.d, a.d_weight);
 }
 
 }  // namespace moe
