@@ -382,6 +382,21 @@ moe_status moe_forward_w8a8_blocks(const moe_shape *shape, const void *x, const 
                                    const float *bias, const moe_fp8_experts *w, void *y,
                                    void *workspace, size_t ws_bytes, void *stream);
 
+/* The W8A8 layer on rows that are in 8 bits already (moe_rmsnorm's codes and
+ * scales): x_codes [T][d] E4M3 and x_scales [T] (fp32), 16-byte aligned, take
+ * the place of the rows that moe_forward_w8a8 / moe_forward_w8a8_blocks would
+ * quantise; x (bf16) is read by the router alone.  With the codes and scales
+ * that those calls make of x, the same bits as those calls. */
+moe_status moe_forward_w8a8_codes(const moe_shape *shape, const void *x, const uint8_t *x_codes,
+                                  const float *x_scales, const void *w_g, const float *bias,
+                                  const moe_fp8_experts *w, void *y, void *workspace,
+                                  size_t ws_bytes, void *stream);
+moe_status moe_forward_w8a8_blocks_codes(const moe_shape *shape, const void *x,
+                                         const uint8_t *x_codes, const float *x_scales,
+                                         const void *w_g, const float *bias,
+                                         const moe_fp8_experts *w, void *y, void *workspace,
+                                         size_t ws_bytes, void *stream);
+
 /*
  * ---- training the router -----------------------------------------------------
  * What a router is trained with beside the forward pass above: the balance

@@ -27,7 +27,8 @@ EXPORTED = ("moe_status_string", "moe_workspace_bytes", "moe_route", "moe_permut
             "moe_quantize_fp8_rows", "moe_expert_ffn_fp8", "moe_forward_fp8",
             "moe_quantize_fp8_blocks", "moe_expert_ffn_fp8_blocks", "moe_forward_fp8_blocks",
             "moe_expert_ffn_w8a8", "moe_forward_w8a8", "moe_expert_ffn_w8a8_blocks",
-            "moe_forward_w8a8_blocks", "moe_balance_workspace_bytes", "moe_balance_loss",
+            "moe_forward_w8a8_blocks", "moe_forward_w8a8_codes", "moe_forward_w8a8_blocks_codes",
+            "moe_balance_workspace_bytes", "moe_balance_loss",
             "moe_route_backward", "moe_dropout", "moe_combine_dropout", "moe_combine_backward",
             "moe_few_workspace_bytes", "moe_forward_few", "moe_forward_few_fp8",
             "moe_forward_few_fp8_blocks",
@@ -86,6 +87,8 @@ def _load_lib() -> ctypes.CDLL:
     lib.moe_forward_w8a8.argtypes = [sp, vp, vp, vp, fp, vp, vp, sz, vp]
     lib.moe_expert_ffn_w8a8_blocks.argtypes = lib.moe_expert_ffn_w8a8.argtypes
     lib.moe_forward_w8a8_blocks.argtypes = lib.moe_forward_w8a8.argtypes
+    lib.moe_forward_w8a8_codes.argtypes = [sp, vp, vp, vp, vp, vp, fp, vp, vp, sz, vp]
+    lib.moe_forward_w8a8_blocks_codes.argtypes = lib.moe_forward_w8a8_codes.argtypes
     f64, f32 = ctypes.c_double, ctypes.c_float
     lib.moe_balance_workspace_bytes.argtypes = [sp, i32]
     lib.moe_balance_workspace_bytes.restype = sz
@@ -109,7 +112,8 @@ def _load_lib() -> ctypes.CDLL:
               "moe_forward", "moe_quantize_fp8_rows", "moe_expert_ffn_fp8", "moe_forward_fp8",
               "moe_quantize_fp8_blocks", "moe_expert_ffn_fp8_blocks", "moe_forward_fp8_blocks",
               "moe_expert_ffn_w8a8", "moe_forward_w8a8", "moe_expert_ffn_w8a8_blocks",
-              "moe_forward_w8a8_blocks", "moe_balance_loss", "moe_route_backward", "moe_dropout",
+              "moe_forward_w8a8_blocks", "moe_forward_w8a8_codes", "moe_forward_w8a8_blocks_codes",
+              "moe_balance_loss", "moe_route_backward", "moe_dropout",
               "moe_combine_dropout", "moe_combine_backward", "moe_forward_few",
               "moe_forward_few_fp8", "moe_forward_few_fp8_blocks", "moe_rmsnorm", "moe_rmsnorm_backward",
               "moe_get_device_error"):
@@ -354,6 +358,31 @@ def _rng(rng):
     if rng is None:
         return None
     return _arg(rng, "rng", torch.uint64 if rng.dtype == torch.uint64 else torch.int64, 2)
+
+
+def _w8a8_codes(call, name, s, x, x_codes, x_scales, w_g, bias, w, y, workspace, stream):
+    bf = torch.bfloat16
+    ws, nws = _ws(workspace)
+    _check(call(ctypes.byref(s), _arg(x, "x", bf, s.T * s.d),
+                _arg(x_codes, "x_codes", torch.uint8, s.T * s.d),
+                _arg(x_scales, "x_scales", torch.float32, s.T), _arg(w_g, "w_g", bf, s.E * s.d),
+                _arg(bias, "bias", torch.float32, s.E, True), ctypes.byref(w),
+                _arg(y, "y", bf, s.T * s.d), ws, nws, _stream(stream)), name)
+
+
+def moe_forward_w8a8_codes(shape, x, x_codes, x_scales, w_g, bias, w: moe_fp8_experts, y, workspace,
+                           stream=None):
+    """moe_forward_w8a8 on rows that are in 8 bits already (codes uint8 [T][d], scales [T]);
+    x (bf16) is the router's."""
+    _w8a8_codes(_lib.moe_forward_w8a8_codes, "moe_forward_w8a8_codes", shape, x, x_codes, x_scales,
+                w_g, bias, w, y, workspace, stream)
+
+
+def moe_forward_w8a8_blocks_codes(shape, x, x_codes, x_scales, w_g, bias, w: moe_fp8_experts, y,
+                                  workspace, stream=None):
+    """moe_forward_w8a8_blocks on rows that are in 8 bits already."""
+    _w8a8_codes(_lib.moe_forward_w8a8_blocks_codes, "moe_forward_w8a8_blocks_codes", shape, x,
+                x_codes, x_scales, w_g, bias, w, y, workspace, stream)
 
 
 def moe_balance_workspace_bytes(shape: moe_shape, n_seq: int = 1) -> int:

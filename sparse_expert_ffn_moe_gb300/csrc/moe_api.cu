@@ -855,10 +855,12 @@ moe_status moe_expert_ffn_w8a8_blocks(const moe_shape* shape, const void* x_perm
                                 kWBlock);
 }
 
-// moe_forward_w8a8 (wblock = 0) and moe_forward_w8a8_blocks (wblock = kWBlock).
-static moe_status forward_w8a8_call(const moe_shape* shape, const void* x, const void* w_g,
-                                    const float* bias, const moe_fp8_experts* w, void* y,
-                                    void* workspace, size_t ws_bytes, void* stream, int wblock) {
+// moe_forward_w8a8 (wblock = 0) and moe_forward_w8a8_blocks (wblock = kWBlock); with x_codes,
+// their *_codes forms.
+static moe_status forward_w8a8_call(const moe_shape* shape, const void* x, const uint8_t* x_codes,
+                                    const float* x_scales, const void* w_g, const float* bias,
+                                    const moe_fp8_experts* w, void* y, void* workspace,
+                                    size_t ws_bytes, void* stream, int wblock) {
     moe_status st = check_shape(shape);
     if (st != MOE_OK) return st;
     const moe_shape& s = *shape;
@@ -892,7 +894,9 @@ static moe_status forward_w8a8_call(const moe_shape* shape, const void* x, const
     const int64_t R = (int64_t)s.T * s.K;
     float* sc = at<float>(workspace, L.ascale);
     uint8_t* xq_perm = at<uint8_t>(workspace, L.x_perm);
-    uint8_t* xq = xq_perm + R * s.d;
+    // the rows' codes and scales: the caller's, or made here
+    const uint8_t* xq = x_codes ? x_codes : xq_perm + R * s.d;
+    const float* xs = x_codes ? x_scales : sc;
     FfnGroups g{};
     g.E = s.E;
     g.has_shared = shared ? 1 : 0;
@@ -921,7 +925,7 @@ static moe_status forward_w8a8_call(const moe_shape* shape, const void* x, const
     g.ss_down = w->ss_down;
     g.wblock = wblock;
     g.sa_routed = sc + s.T;
-    g.sa_shared = sc;
+    g.sa_shared = xs;
     g.sa_h = sc + s.T + R;
     g.sa_hs = sc + s.T + 2 * R;
     g.h = at<void>(workspace, L.h);
@@ -941,8 +945,9 @@ static moe_status forward_w8a8_call(const moe_shape* shape, const void* x, const
     else
         e = launch_dispatch(s, topk_idx, counts, offsets, perm, inv, tok,
                             at<int32_t>(workspace, L.blk_hist), err, cs);
-    if (e == cudaSuccess) e = launch_quantize_act_rows(s.T, s.d, x, s.d, xq, s.d, sc, cs);
-    if (e == cudaSuccess) e = launch_gather_codes(s, xq, sc, inv, xq_perm, sc + s.T, cs);
+    if (e == cudaSuccess && !x_codes)
+        e = launch_quantize_act_rows(s.T, s.d, x, s.d, xq_perm + R * s.d, s.d, sc, cs);
+    if (e == cudaSuccess) e = launch_gather_codes(s, xq, xs, inv, xq_perm, sc + s.T, cs);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
 
     // 3. routed and shared experts, W8A8 on the tensor cores
@@ -957,13 +962,44 @@ static moe_status forward_w8a8_call(const moe_shape* shape, const void* x, const
 moe_status moe_forward_w8a8(const moe_shape* shape, const void* x, const void* w_g,
                             const float* bias, const moe_fp8_experts* w, void* y, void* workspace,
                             size_t ws_bytes, void* stream) {
-    return forward_w8a8_call(shape, x, w_g, bias, w, y, workspace, ws_bytes, stream, 0);
+    return forward_w8a8_call(shape, x, nullptr, nullptr, w_g, bias, w, y, workspace, ws_bytes, stream,
+                             0);
 }
 
 moe_status moe_forward_w8a8_blocks(const moe_shape* shape, const void* x, const void* w_g,
                                    const float* bias, const moe_fp8_experts* w, void* y,
                                    void* workspace, size_t ws_bytes, void* stream) {
-    return forward_w8a8_call(shape, x, w_g, bias, w, y, workspace, ws_bytes, stream, kWBlock);
+    return forward_w8a8_call(shape, x, nullptr, nullptr, w_g, bias, w, y, workspace, ws_bytes, stream,
+                             kWBlock);
+}
+
+// the *_codes forms check what the others make
+static moe_status forward_codes_call(const moe_shape* shape, const void* x, const uint8_t* x_codes,
+                                     const float* x_scales, const void* w_g, const float* bias,
+                                     const moe_fp8_experts* w, void* y, void* workspace,
+                                     size_t ws_bytes, void* stream, int wblock) {
+    if (shape && shape->T > 0 &&
+        (!x_codes || !x_scales || !aligned16(x_codes) || !aligned16(x_scales)))
+        return MOE_ERR_INVALID_ARG;
+    return forward_w8a8_call(shape, x, x_codes, x_scales, w_g, bias, w, y, workspace, ws_bytes, stream,
+                             wblock);
+}
+
+moe_status moe_forward_w8a8_codes(const moe_shape* shape, const void* x, const uint8_t* x_codes,
+                                  const float* x_scales, const void* w_g, const float* bias,
+                                  const moe_fp8_experts* w, void* y, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+    return forward_codes_call(shape, x, x_codes, x_scales, w_g, bias, w, y, workspace, ws_bytes, stream,
+                              0);
+}
+
+moe_status moe_forward_w8a8_blocks_codes(const moe_shape* shape, const void* x,
+                                         const uint8_t* x_codes, const float* x_scales,
+                                         const void* w_g, const float* bias,
+                                         const moe_fp8_experts* w, void* y, void* workspace,
+                                         size_t ws_bytes, void* stream) {
+    return forward_codes_call(shape, x, x_codes, x_scales, w_g, bias, w, y, workspace, ws_bytes, stream,
+                              kWBlock);
 }
 
 moe_status moe_get_device_error(const void* workspace, int32_t* code_out) {

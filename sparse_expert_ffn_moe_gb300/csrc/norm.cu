@@ -21,7 +21,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kTeamVecs = 64;      // widest row of a team, in vectors
+constexpr int kTeamVecs = 32;      // widest row of a team, in vectors
 constexpr int kTeamThreads = 256;   // block of the variants whose team is part of a warp
 
 __device__ __forceinline__ uint4 pack(const float (&f)[4], const float*) {
@@ -38,47 +38,84 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8], const bf16*) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// Where a lane's vectors of a row lie: vector j is elements at(j) .. at(j) + V - 1 of
-// the whole array, of which [a0, a1) belong to the row.
+// A row that starts `skip` elements into a vector: vector c of the row is elements
+// c V - skip .. of it, those outside [0, d) not the row's.
 template <typename T, bool AL>
-struct Span {
+struct Row {
     static constexpr int V = Elem<T>::kPerVec;
-    int64_t a0, a1, v0;
-    __device__ __forceinline__ Span(int64_t row, int d) {
-        a0 = row * d;
-        a1 = a0 + d;
-        v0 = a0 / V * V;
+    int64_t at;  // the first vector, in elements of the array; a multiple of V
+    int skip, d, vecs;
+    __device__ __forceinline__ Row(int64_t row, int d_) : d(d_) {
+        const int64_t a = row * d_;
+        skip = AL ? 0 : (int)(a % V);
+        at = a - skip;
+        vecs = AL ? d_ / V : (skip + d_ + V - 1) / V;
     }
-    __device__ __forceinline__ int64_t at(int i) const { return v0 + (int64_t)i * V; }
-    __device__ __forceinline__ bool any(int64_t e) const { return e < a1; }
-    __device__ __forceinline__ bool whole(int64_t e) const {
-        return AL || (e >= a0 && e + V <= a1);
+    __device__ __forceinline__ bool whole(int c) const {
+        return AL || (c * V >= skip && c * V + V <= skip + d);
+    }
+    __device__ __forceinline__ bool has(int c, int k) const {
+        return AL || (c * V + k >= skip && c * V + k < skip + d);
+    }
+    // vector c of p, elements that are not the row's 0; `total`: elements of the array
+    __device__ __forceinline__ uint4 load(const T* p, int c, int64_t total) const {
+        if (AL) return *reinterpret_cast<const uint4*>(p + at + c * V);
+        const int64_t e = at + c * V;
+        if (e + V > total) {  // the array's last vector
+            float f[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) f[k] = has(c, k) ? Elem<T>::to_f32(p[e + k]) : 0.0f;
+            return pack(f, (const T*)nullptr);
+        }
+        return mask(*reinterpret_cast<const uint4*>(p + e), c);
+    }
+    __device__ __forceinline__ uint4 mask(const uint4& v, int c) const {
+        if (whole(c)) return v;
+        float f[V];
+        unpack(v, f, (const T*)nullptr);
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] = has(c, k) ? f[k] : 0.0f;
+        return pack(f, (const T*)nullptr);
+    }
+    __device__ __forceinline__ void store(T* p, int c, const uint4& v) const {
+        if (whole(c)) {
+            *reinterpret_cast<uint4*>(p + at + c * V) = v;
+            return;
+        }
+        float f[V];
+        unpack(v, f, (const T*)nullptr);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (has(c, k)) p[at + c * V + k] = Elem<T>::from_f32(f[k]);
+    }
+    // vector i of the weight itself, 0 past its end
+    __device__ __forceinline__ uint4 weight_vec(const T* w, int i) const {
+        if (i < 0 || i * V >= d) return make_uint4(0u, 0u, 0u, 0u);
+        if (i * V + V <= d) return ld_ro(w + i * V);
+        float f[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] = i * V + k < d ? Elem<T>::to_f32(__ldg(w + i * V + k)) : 0.0f;
+        return pack(f, (const T*)nullptr);
+    }
+    // the weights of vector c: `skip` elements of the vector before, then the next
+    __device__ __forceinline__ uint4 weight(const T* w, int c) const {
+        if (AL) return ld_ro(w + c * V);
+        const uint4 a = weight_vec(w, c - 1), b = weight_vec(w, c);
+        uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        // x from element V - skip on: by 4, 2 and 1 words, and half a word of bf16
+        const int by = (V - skip) * (int)sizeof(T);  // bytes, 2 .. 16
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] = by & 16 ? x[q + 4] : x[q];
+#pragma unroll
+        for (int q = 0; q < 6; ++q) x[q] = by & 8 ? x[q + 2] : x[q];
+#pragma unroll
+        for (int q = 0; q < 5; ++q) x[q] = by & 4 ? x[q + 1] : x[q];
+        if constexpr (sizeof(T) == 2)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[q] = by & 2 ? __funnelshift_r(x[q], x[q + 1], 16) : x[q];
+        return make_uint4(x[0], x[1], x[2], x[3]);
     }
 };
-
-// the vector at element e of p, elements outside the row 0
-template <typename T, bool AL>
-__device__ __forceinline__ uint4 load_vec(const T* p, const Span<T, AL>& sp, int64_t e) {
-    if (sp.whole(e)) return *reinterpret_cast<const uint4*>(p + e);
-    float f[Span<T, AL>::V];
-#pragma unroll
-    for (int k = 0; k < Span<T, AL>::V; ++k)
-        f[k] = (e + k >= sp.a0 && e + k < sp.a1) ? Elem<T>::to_f32(p[e + k]) : 0.0f;
-    return pack(f, (const T*)nullptr);
-}
-
-template <typename T, bool AL>
-__device__ __forceinline__ void store_vec(T* p, const Span<T, AL>& sp, int64_t e, const uint4& v) {
-    if (sp.whole(e)) {
-        *reinterpret_cast<uint4*>(p + e) = v;
-        return;
-    }
-    float f[Span<T, AL>::V];
-    unpack(v, f, (const T*)nullptr);
-#pragma unroll
-    for (int k = 0; k < Span<T, AL>::V; ++k)
-        if (e + k >= sp.a0 && e + k < sp.a1) p[e + k] = Elem<T>::from_f32(f[k]);
-}
 
 // (sum, max) or (sum, sum) over the team, in every thread.  TEAM 0: the block, through
 // `red` (one of two buffers in turn, so that one barrier a row is enough).
@@ -107,23 +144,6 @@ __device__ __forceinline__ void team_reduce(float& a, float& b, float2* red) {
     }
 }
 
-// the weights of the vector at element e
-template <typename T, bool AL>
-__device__ __forceinline__ void load_weight(const T* w, const Span<T, AL>& sp, int64_t e,
-                                            float (&f)[Span<T, AL>::V]) {
-    if constexpr (AL) {
-        if (e < sp.a1) unpack(ld_ro(w + (e - sp.a0)), f, (const T*)nullptr);
-        else
-#pragma unroll
-            for (int k = 0; k < Span<T, AL>::V; ++k) f[k] = 0.0f;
-    } else {
-#pragma unroll
-        for (int k = 0; k < Span<T, AL>::V; ++k)
-            f[k] = (e + k >= sp.a0 && e + k < sp.a1) ? Elem<T>::to_f32(__ldg(w + (e + k - sp.a0)))
-                                                     : 0.0f;
-    }
-}
-
 // E4M3 codes of the values over the scale, four to a word
 template <int N>
 __device__ __forceinline__ void to_codes(const float (&f)[N], float inv_scale, uint32_t (&c)[N / 4]) {
@@ -137,60 +157,61 @@ __device__ __forceinline__ void to_codes(const float (&f)[N], float inv_scale, u
     }
 }
 
-template <typename T, int TEAM, int VPT, bool AL, bool RES, bool CODES>
+template <typename T, bool AL>
+__device__ __forceinline__ void store_codes(uint8_t* codes, const Row<T, AL>& row, int c,
+                                            const float (&f)[Row<T, AL>::V], float inv_scale) {
+    constexpr int V = Row<T, AL>::V;
+    uint32_t q[V / 4];
+    to_codes(f, inv_scale, q);
+    uint8_t* p = codes + row.at + c * V;
+    if (row.whole(c)) {
+        if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[V / 4 - 1]);
+        else *reinterpret_cast<uint32_t*>(p) = q[0];
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (row.has(c, k)) p[k] = (uint8_t)(q[k / 4] >> (8 * (k & 3)));
+    }
+}
+
+// Narrow rows: a lane a vector, a team of a warp's lanes a row, blocks stay for many.
+template <typename T, int TEAM, bool AL, bool RES, bool CODES>
 __global__ void __launch_bounds__(kTeamThreads)
 rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, float eps, T* s_out,
                T* y, uint8_t* codes, float* __restrict__ scales, int64_t rows, int d) {
-    constexpr int V = Elem<T>::kPerVec;
+    constexpr int V = Elem<T>::kPerVec, per_block = kTeamThreads / TEAM;
     pdl_wait();
     pdl_trigger();
-    constexpr int team = TEAM, per_block = kTeamThreads / TEAM;
     const int lane = threadIdx.x % TEAM;
-    const int64_t stride = (int64_t)gridDim.x * per_block;
+    const int64_t stride = (int64_t)gridDim.x * per_block, total = rows * d;
     // every team of a block runs as many turns as its first, for the warp-wide shuffles
     const int64_t first = (int64_t)blockIdx.x * per_block;
     const int64_t turns = first < rows ? (rows - first + stride - 1) / stride : 0;
-    int64_t row = first + threadIdx.x / TEAM;
+    int64_t at = first + threadIdx.x / TEAM;
+    const T* const no = nullptr;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     const float inv_d = 1.0f / (float)d;
-    for (int64_t it = 0; it < turns; ++it, row += stride) {
-        const Span<T, AL> sp(row, d);
-        const bool live = row < rows;
-        uint4 sv[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int64_t e = sp.at(lane + j * team);
-            sv[j] = live && sp.any(e) ? load_vec<T, AL>(x, sp, e) : zero;
-        }
+    for (int64_t it = 0; it < turns; ++it, at += stride) {
+        const Row<T, AL> row(at, d);
+        const bool live = at < rows;
+        const bool mine = live && lane < row.vecs;
+        uint4 sv = mine ? row.load(x, lane, total) : zero;
+        float f[V], g[V];
         if constexpr (RES) {
-            uint4 rv[VPT];
+            const uint4 rv = mine ? row.load(residual, lane, total) : zero;
+            unpack(sv, f, no);
+            unpack(rv, g, no);
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int64_t e = sp.at(lane + j * team);
-                rv[j] = live && sp.any(e) ? load_vec<T, AL>(residual, sp, e) : zero;
-            }
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                float f[V], g[V];
-                unpack(sv[j], f, (const T*)nullptr);
-                unpack(rv[j], g, (const T*)nullptr);
-#pragma unroll
-                for (int k = 0; k < V; ++k) f[k] += g[k];
-                sv[j] = pack(f, (const T*)nullptr);
-            }
+            for (int k = 0; k < V; ++k) f[k] += g[k];
+            sv = pack(f, no);
         }
+        unpack(sv, f, no);
+        unpack(lane < row.vecs ? row.weight(weight, lane) : zero, g, no);
         float sum = 0.0f, top = 0.0f;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            float f[V], g[V];
-            unpack(sv[j], f, (const T*)nullptr);
-#pragma unroll
-            for (int k = 0; k < V; ++k) sum = fmaf(f[k], f[k], sum);
-            if constexpr (CODES) {
-                load_weight<T, AL>(weight, sp, sp.at(lane + j * team), g);
-#pragma unroll
-                for (int k = 0; k < V; ++k) top = fmaxf(top, fabsf(f[k] * g[k]));
-            }
+        for (int k = 0; k < V; ++k) {
+            sum = fmaf(f[k], f[k], sum);
+            if (CODES) top = fmaxf(top, fabsf(f[k] * g[k]));
         }
         team_reduce<TEAM, true>(sum, top, nullptr);
         if (!live) continue;  // the last turn of a block of teams
@@ -198,68 +219,46 @@ rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, floa
         const float most = top * r;
         const float scale = most > 0.0f ? most / 448.0f : 1.0f;
         const float inv_scale = 1.0f / scale;
-        if (CODES && lane == 0) scales[row] = scale;
+        if (CODES && lane == 0) scales[at] = scale;
+        if (lane >= row.vecs) continue;
+        if (s_out) row.store(s_out, lane, sv);
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int64_t e = sp.at(lane + j * team);
-            if (!sp.any(e)) continue;
-            float f[V], g[V];
-            if (s_out) store_vec<T, AL>(s_out, sp, e, sv[j]);
-            unpack(sv[j], f, (const T*)nullptr);
-            load_weight<T, AL>(weight, sp, e, g);
-#pragma unroll
-            for (int k = 0; k < V; ++k) f[k] = f[k] * r * g[k];
-            if (y) store_vec<T, AL>(y, sp, e, pack(f, (const T*)nullptr));
-            if constexpr (CODES) {
-                uint32_t c[V / 4];
-                to_codes(f, inv_scale, c);
-                if (sp.whole(e)) {
-                    if constexpr (V == 8)
-                        *reinterpret_cast<uint2*>(codes + e) = make_uint2(c[0], c[V / 4 - 1]);
-                    else
-                        *reinterpret_cast<uint32_t*>(codes + e) = c[0];
-                } else {
-#pragma unroll
-                    for (int k = 0; k < V; ++k)
-                        if (e + k >= sp.a0 && e + k < sp.a1)
-                            codes[e + k] = (uint8_t)(c[k / 4] >> (8 * (k & 3)));
-                }
-            }
-        }
+        for (int k = 0; k < V; ++k) f[k] = f[k] * r * g[k];
+        if (y) row.store(y, lane, pack(f, no));
+        if constexpr (CODES) store_codes(codes, row, lane, f, inv_scale);
     }
 }
 
-// A wide row of whole vectors: a block of its own, which ends with it.  Many small blocks in
-// different parts of their rows keep the memory busy; blocks that stayed for many rows, with
-// or without a ring of copies ahead, did not (16384 x 7168 bf16 with residual and codes: 178
-// and 186 us, this 161).
+// A wide row: a block of its own, which ends with it.  Many small blocks in different parts
+// of their rows keep the memory busy; blocks that stayed for many rows, with or without a ring
+// of copies ahead, did not (16384 x 7168 bf16 with residual and codes: 178 and 186 us, this
+// 153).  AL: whole vectors tile the rows.
 template <int VPT> constexpr int kBlockThreads = VPT <= 4 ? 256 : 512;
 
-template <typename T, int VPT, bool RES, bool CODES>
+template <typename T, int VPT, bool AL, bool RES, bool CODES>
 __global__ void __launch_bounds__(kBlockThreads<VPT>, VPT <= 4 ? 4 : 1)
 rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight, float eps, T* s_out,
-                     T* y, uint8_t* codes, float* __restrict__ scales, int d) {
+                     T* y, uint8_t* codes, float* __restrict__ scales, int64_t rows, int d) {
     constexpr int V = Elem<T>::kPerVec;
     __shared__ float2 red[32];
     pdl_wait();
     pdl_trigger();
-    const int nt = blockDim.x, vecs = d / V;
-    const int64_t at = (int64_t)blockIdx.x * d;
-    const uint4* px = reinterpret_cast<const uint4*>(x + at);
-    const uint4* pr = reinterpret_cast<const uint4*>(residual + at);
+    const int nt = blockDim.x;
+    const int64_t total = rows * d;
+    const Row<T, AL> row(blockIdx.x, d);
     const T* const no = nullptr;
     uint4 sv[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int c = threadIdx.x + j * nt;
-        sv[j] = c < vecs ? px[c] : make_uint4(0u, 0u, 0u, 0u);
+        sv[j] = c < row.vecs ? row.load(x, c, total) : make_uint4(0u, 0u, 0u, 0u);
     }
     if constexpr (RES) {
         uint4 rv[VPT];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = threadIdx.x + j * nt;
-            rv[j] = c < vecs ? pr[c] : make_uint4(0u, 0u, 0u, 0u);
+            rv[j] = c < row.vecs ? row.load(residual, c, total) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -274,7 +273,7 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int c = threadIdx.x + j * nt;
-                if (c < vecs) reinterpret_cast<uint4*>(s_out + at)[c] = sv[j];
+                if (c < row.vecs) row.store(s_out, c, sv[j]);
             }
         }
     }
@@ -287,8 +286,8 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
 #pragma unroll
         for (int k = 0; k < V; ++k) sum = fmaf(f[k], f[k], sum);
         if constexpr (CODES) {
-            if (c >= vecs) continue;
-            unpack(ld_ro(weight + c * V), g, no);
+            if (c >= row.vecs) continue;
+            unpack(row.weight(weight, c), g, no);
 #pragma unroll
             for (int k = 0; k < V; ++k) top = fmaxf(top, fabsf(f[k] * g[k]));
         }
@@ -302,21 +301,16 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int c = threadIdx.x + j * nt;
-        if (c >= vecs) continue;
+        if (c >= row.vecs) continue;
         float f[V], g[V];
         unpack(sv[j], f, no);
-        unpack(ld_ro(weight + c * V), g, no);
+        unpack(row.weight(weight, c), g, no);
 #pragma unroll
         for (int k = 0; k < V; ++k) f[k] = f[k] * r * g[k];
-        if (!RES && s_out) reinterpret_cast<uint4*>(s_out + at)[c] = sv[j];
-        if (y) reinterpret_cast<uint4*>(y + at)[c] = pack(f, no);
+        if (!RES && s_out) row.store(s_out, c, sv[j]);
+        if (y) row.store(y, c, pack(f, no));
         if constexpr (CODES) {
-            uint32_t q[V / 4];
-            to_codes(f, inv_scale, q);
-            if constexpr (V == 8)
-                reinterpret_cast<uint2*>(codes + at)[c] = make_uint2(q[0], q[V / 4 - 1]);
-            else
-                reinterpret_cast<uint32_t*>(codes + at)[c] = q[0];
+            store_codes(codes, row, c, f, inv_scale);
         }
     }
 }
@@ -337,88 +331,67 @@ __device__ __forceinline__ void open(const typename Raw<T, W>::type& v, float (&
     else unpack(v, f, (const T*)nullptr);
 }
 
-template <typename T, int TEAM, int VPT, int W>
+template <typename T, int TEAM, int W>
 __global__ void __launch_bounds__(kTeamThreads)
 rmsnorm_backward_kernel(const T* d_y, const T* s, const T* __restrict__ weight, float eps,
                         const T* d_s, T* d_x, float* __restrict__ part, int64_t rows, int d) {
     using R = typename Raw<T, W>::type;
-    extern __shared__ float acc_sm[];
+    constexpr int per_block = kTeamThreads / TEAM, kCols = TEAM * W;
+    extern __shared__ float acc_sm[];  // [team of the block][columns of a team]
     pdl_wait();
     pdl_trigger();
-    constexpr int team = TEAM, per_block = kTeamThreads / TEAM;
-    const int lane = threadIdx.x % TEAM;
+    const int team = threadIdx.x / TEAM, c = threadIdx.x % TEAM * W;
     const int64_t stride = (int64_t)gridDim.x * per_block;
     const int64_t first = (int64_t)blockIdx.x * per_block;
     const int64_t turns = first < rows ? (rows - first + stride - 1) / stride : 0;
-    int64_t row = first + threadIdx.x / TEAM;
-    float acc[VPT][W];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int k = 0; k < W; ++k) acc[j][k] = 0.0f;
+    int64_t row = first + team;
     const R zero = R{};
+    float fw[W], acc[W];
+    open<T, W>(c < d ? __ldg(reinterpret_cast<const R*>(weight + c)) : zero, fw);
+#pragma unroll
+    for (int k = 0; k < W; ++k) acc[k] = 0.0f;
+    R sv, yv, av;
+    const auto fetch = [&](int64_t at) {
+        const bool go = at < rows && c < d;
+        sv = go ? *reinterpret_cast<const R*>(s + at * d + c) : zero;
+        yv = go ? *reinterpret_cast<const R*>(d_y + at * d + c) : zero;
+        av = go && d_s && d_x ? *reinterpret_cast<const R*>(d_s + at * d + c) : zero;
+    };
+    fetch(row);
     const float inv_d = 1.0f / (float)d;
     for (int64_t it = 0; it < turns; ++it, row += stride) {
-        const bool live = row < rows;
-        R sv[VPT], yv[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = (lane + j * team) * W;
-            const bool go = live && c < d;
-            sv[j] = go ? *reinterpret_cast<const R*>(s + row * d + c) : zero;
-            yv[j] = go ? *reinterpret_cast<const R*>(d_y + row * d + c) : zero;
-        }
+        float fs[W], fy[W], fa[W];
+        open<T, W>(sv, fs);
+        open<T, W>(yv, fy);
+        open<T, W>(av, fa);
+        if (it + 1 < turns) fetch(row + stride);  // in flight over this row
         float sq = 0.0f, gs = 0.0f;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = (lane + j * team) * W;
-            float fs[W], fy[W], fw[W];
-            open<T, W>(sv[j], fs);
-            open<T, W>(yv[j], fy);
-            open<T, W>(c < d ? __ldg(reinterpret_cast<const R*>(weight + c)) : zero, fw);
-#pragma unroll
-            for (int k = 0; k < W; ++k) {
-                sq = fmaf(fs[k], fs[k], sq);
-                gs = fmaf(fy[k] * fw[k], fs[k], gs);
-            }
+        for (int k = 0; k < W; ++k) {
+            sq = fmaf(fs[k], fs[k], sq);
+            gs = fmaf(fy[k] * fw[k], fs[k], gs);
         }
         team_reduce<TEAM, false>(sq, gs, nullptr);
+        if (row >= rows || c >= d) continue;
         const float r = 1.0f / sqrtf(fmaf(sq, inv_d, eps));
         const float back = gs * inv_d * r * r;  // times s: what the bracket takes off
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = (lane + j * team) * W;
-            if (!live || c >= d) continue;
-            float fs[W], fy[W], fw[W], fa[W];
-            open<T, W>(sv[j], fs);
-            open<T, W>(yv[j], fy);
-#pragma unroll
-            for (int k = 0; k < W; ++k) acc[j][k] = fmaf(fy[k], fs[k] * r, acc[j][k]);
-            if (!d_x) continue;
-            open<T, W>(__ldg(reinterpret_cast<const R*>(weight + c)), fw);
-            open<T, W>(d_s ? *reinterpret_cast<const R*>(d_s + row * d + c) : zero, fa);
-#pragma unroll
-            for (int k = 0; k < W; ++k)
-                fa[k] = fmaf(r, fmaf(-back, fs[k], fy[k] * fw[k]), fa[k]);
-            if constexpr (W == 1) d_x[row * d + c] = Elem<T>::from_f32(fa[0]);
-            else *reinterpret_cast<uint4*>(d_x + row * d + c) = pack(fa, (const T*)nullptr);
+        for (int k = 0; k < W; ++k) {
+            acc[k] = fmaf(fy[k], fs[k] * r, acc[k]);
+            fa[k] = fmaf(r, fmaf(-back, fs[k], fy[k] * fw[k]), fa[k]);
         }
+        if (!d_x) continue;
+        if constexpr (W == 1) d_x[row * d + c] = Elem<T>::from_f32(fa[0]);
+        else *reinterpret_cast<uint4*>(d_x + row * d + c) = pack(fa, (const T*)nullptr);
     }
     if (!part) return;
-    {
-        // acc_sm[team of the block][columns of a team]
-        constexpr int kCols = TEAM * VPT * W;
-        const int mine = threadIdx.x / TEAM;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int k = 0; k < W; ++k) acc_sm[mine * kCols + (lane + j * TEAM) * W + k] = acc[j][k];
-        __syncthreads();
-        for (int c = threadIdx.x; c < d; c += kTeamThreads) {
-            float t = 0.0f;
-            for (int q = 0; q < kTeamThreads / TEAM; ++q) t += acc_sm[q * kCols + c];
-            part[(int64_t)blockIdx.x * d + c] = t;
-        }
+    for (int k = 0; k < W; ++k) acc_sm[team * kCols + c + k] = acc[k];
+    __syncthreads();
+    for (int col = threadIdx.x; col < d; col += kTeamThreads) {
+        float t = 0.0f;
+        for (int q = 0; q < per_block; ++q) t += acc_sm[q * kCols + col];
+        part[(int64_t)blockIdx.x * d + col] = t;
     }
 }
 
@@ -433,71 +406,97 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-constexpr int kDepth = 3;  // rows in a ring, or 1 where three do not fit
+constexpr int kDepth = 3;  // rows in a ring
 
-constexpr int kRingThreads = 512;
 constexpr size_t kRingSmem = 220 * 1024;  // of an SM, for the rings of its blocks
 
-// Rows of whole vectors: each thread copies and reads its own.  s and d_y by way of the ring,
-// d_s straight to registers, asked for before the row's sums.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(kRingThreads, VPT <= 2 ? 2 : 1)
+// s and d_y come by way of the ring, where each thread copies and reads its own; d_s straight
+// to registers, asked for before the row's sums.  A thread's columns are the same in every
+// row: rows that start within vectors (AL false) go to blocks by where they start (the grid
+// is then a multiple of V, or has a row a block).
+template <int VPT> constexpr int kBackThreads = VPT <= 4 ? 256 : 512;
+
+template <typename T, int VPT, bool AL>
+__global__ void __launch_bounds__(kBackThreads<VPT>, VPT <= 4 ? 2 : 1)
 rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ weight, float eps,
                              const T* d_s, T* d_x, float* __restrict__ part, int64_t rows, int d) {
     constexpr int V = Elem<T>::kPerVec;
-    constexpr int D = VPT <= 4 ? kDepth : 1;  // 8 vectors: fp32 rows of more than 8192
+    constexpr bool kKeep = VPT <= 4;  // a row's values stay in registers between sums and stores
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 red[2][32];
     pdl_wait();
     pdl_trigger();
-    const int nt = blockDim.x, vecs = d / V, row_bytes = vecs * 16;
+    const int nt = blockDim.x;
+    const int64_t stride = gridDim.x, total = rows * d;
+    const Row<T, AL> first(blockIdx.x, d);
+    const int vecs = first.vecs, row_bytes = vecs * 16;
     const bool add = d_s && d_x;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
-    const int64_t stride = gridDim.x;
     const T* const no = nullptr;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     auto fetch = [&](int64_t row, int slot) {
         if (row < rows) {
+            const int64_t at = row * d - first.skip;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int c = threadIdx.x + j * nt;
-                if (c < vecs) {
-                    const uint32_t dst = base + slot * 2 * row_bytes + c * 16;
-                    copy_async(dst, s + row * d + c * V);
-                    copy_async(dst + row_bytes, d_y + row * d + c * V);
+                if (c >= vecs) continue;
+                const int to = slot * 2 * row_bytes + c * 16;
+                const int64_t e = at + c * V;
+                if (AL || e + V <= total) {
+                    copy_async(base + to, s + e);
+                    copy_async(base + to + row_bytes, d_y + e);
+                } else {  // the arrays' last vector
+                    const Row<T, AL> last(row, d);
+                    *reinterpret_cast<uint4*>(ring + to) = last.load(s, c, total);
+                    *reinterpret_cast<uint4*>(ring + to + row_bytes) = last.load(d_y, c, total);
                 }
             }
         }
         copy_commit();
     };
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i) fetch(blockIdx.x + i * stride, i);
+    for (int i = 0; i < kDepth - 1; ++i) fetch(blockIdx.x + i * stride, i);
     float acc[VPT][V];
+    uint4 wv[kKeep ? VPT : 1];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
+    for (int j = 0; j < VPT; ++j) {
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[j][k] = 0.0f;
+        const int c = threadIdx.x + j * nt;
+        if constexpr (kKeep) wv[j] = c < vecs ? first.weight(weight, c) : zero;
+    }
     const float inv_d = 1.0f / (float)d;
     int slot = 0, turn = 0;
     for (int64_t row = blockIdx.x; row < rows; row += stride, turn ^= 1) {
-        uint4 av[VPT];
+        Row<T, AL> here = first;
+        here.at = row * d - first.skip;
+        uint4 av[VPT], sv[kKeep ? VPT : 1], yv[kKeep ? VPT : 1];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = threadIdx.x + j * nt;
-            av[j] = add && c < vecs ? *reinterpret_cast<const uint4*>(d_s + row * d + c * V)
-                                    : make_uint4(0u, 0u, 0u, 0u);
+            av[j] = add && c < vecs ? here.load(d_s, c, total) : zero;
         }
-        if constexpr (D == 1) fetch(row, 0);
-        copy_wait<D == 1 ? 0 : D - 2>();
+        copy_wait<kDepth - 2>();
         const uint8_t* mine = ring + slot * 2 * row_bytes;
+        const auto read = [&](int c, bool second) {
+            return here.mask(*reinterpret_cast<const uint4*>(mine + (second ? row_bytes : 0) + c * 16), c);
+        };
         float sq = 0.0f, gs = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = threadIdx.x + j * nt;
+            if constexpr (kKeep) sv[j] = yv[j] = zero;
             if (c >= vecs) continue;
+            const uint4 a = read(c, false), b = read(c, true);
+            if constexpr (kKeep) {
+                sv[j] = a;
+                yv[j] = b;
+            }
             float fs[V], fy[V], fw[V];
-            unpack(*reinterpret_cast<const uint4*>(mine + c * 16), fs, no);
-            unpack(*reinterpret_cast<const uint4*>(mine + row_bytes + c * 16), fy, no);
-            unpack(ld_ro(weight + c * V), fw, no);
+            unpack(a, fs, no);
+            unpack(b, fy, no);
+            unpack(kKeep ? wv[kKeep ? j : 0] : here.weight(weight, c), fw, no);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 sq = fmaf(fs[k], fs[k], sq);
@@ -506,7 +505,7 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
         }
         team_reduce<0, false>(sq, gs, red[turn]);
         // into the place of the row before this one, used up before the barrier
-        if constexpr (D > 1) fetch(row + (D - 1) * stride, slot == 0 ? D - 1 : slot - 1);
+        fetch(row + (kDepth - 1) * stride, slot == 0 ? kDepth - 1 : slot - 1);
         const float r = 1.0f / sqrtf(fmaf(sq, inv_d, eps));
         const float back = gs * inv_d * r * r;  // times s: what the bracket takes off
 #pragma unroll
@@ -514,19 +513,19 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
             const int c = threadIdx.x + j * nt;
             if (c >= vecs) continue;
             float fs[V], fy[V], fw[V], fa[V];
-            unpack(*reinterpret_cast<const uint4*>(mine + c * 16), fs, no);
-            unpack(*reinterpret_cast<const uint4*>(mine + row_bytes + c * 16), fy, no);
+            unpack(kKeep ? sv[kKeep ? j : 0] : read(c, false), fs, no);
+            unpack(kKeep ? yv[kKeep ? j : 0] : read(c, true), fy, no);
 #pragma unroll
             for (int k = 0; k < V; ++k) acc[j][k] = fmaf(fy[k], fs[k] * r, acc[j][k]);
             if (!d_x) continue;
-            unpack(ld_ro(weight + c * V), fw, no);
+            unpack(kKeep ? wv[kKeep ? j : 0] : here.weight(weight, c), fw, no);
             unpack(av[j], fa, no);
 #pragma unroll
             for (int k = 0; k < V; ++k)
                 fa[k] = fmaf(r, fmaf(-back, fs[k], fy[k] * fw[k]), fa[k]);
-            *reinterpret_cast<uint4*>(d_x + row * d + c * V) = pack(fa, no);
+            here.store(d_x, c, pack(fa, no));
         }
-        if (++slot == D) slot = 0;
+        if (++slot == kDepth) slot = 0;
     }
     copy_wait<0>();
     if (!part) return;
@@ -535,181 +534,73 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
         const int c = threadIdx.x + j * nt;
         if (c >= vecs) continue;
 #pragma unroll
-        for (int k = 0; k < V; ++k) part[(int64_t)blockIdx.x * d + c * V + k] = acc[j][k];
+        for (int k = 0; k < V; ++k)
+            if (first.has(c, k)) part[(int64_t)blockIdx.x * d + c * V + k - first.skip] = acc[j][k];
     }
 }
 
-// Rows that start within a vector: the ring holds the whole vectors that cover a row, and a
-// thread reads the elements of its columns, the same in every row.
-template <typename T>
-struct Window {
-    int bytes;  // of a slot's array
-    __device__ __forceinline__ explicit Window(int d) : bytes((d * (int)sizeof(T) + 15 + 15) / 16 * 16) {}
-    // bytes of the row before its first element
-    __device__ __forceinline__ static int skip(int64_t row, int d) {
-        return (int)((row * d * (int64_t)sizeof(T)) & 15);
-    }
-    // copies the vectors; those that reach past the array's end go by element
-    __device__ __forceinline__ void fetch(uint32_t dst, uint8_t* to, const T* p, int64_t row, int d,
-                                          int64_t rows) const {
-        const int64_t b0 = row * d * (int64_t)sizeof(T), from = b0 & ~(int64_t)15;
-        const int64_t end = b0 + d * (int64_t)sizeof(T), total = rows * d * (int64_t)sizeof(T);
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(p);
-        for (int64_t at = from + threadIdx.x * 16; at < end; at += blockDim.x * 16) {
-            if (at + 16 <= total) {
-                copy_async(dst + (uint32_t)(at - from), src + at);
-            } else {
-                for (int64_t e = at; e < end; e += sizeof(T))
-                    *reinterpret_cast<T*>(to + (e - from)) = *reinterpret_cast<const T*>(src + e);
-            }
-        }
-    }
-};
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kRingThreads, 2)
-rmsnorm_window_kernel(const T* x, const T* residual, const T* __restrict__ weight, float eps, T* s_out,
-                      T* y, uint8_t* codes, float* __restrict__ scales, int64_t rows, int d) {
-    extern __shared__ __align__(16) uint8_t ring[];
+// Rows too wide for a ring of three (fp32 rows of more than 8192): straight from memory, twice
+// -- the second time from L2 -- by element where vectors do not tile them.
+template <typename T, int W, int EPT>
+__global__ void __launch_bounds__(1024)
+rmsnorm_backward_wide_kernel(const T* d_y, const T* s, const T* __restrict__ weight, float eps,
+                             const T* d_s, T* d_x, float* __restrict__ part, int64_t rows, int d) {
     __shared__ float2 red[2][32];
     pdl_wait();
     pdl_trigger();
-    const Window<T> win(d);
-    const int arrays = residual ? 2 : 1;
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
-    const int64_t stride = gridDim.x;
-    auto fetch = [&](int64_t row, int slot) {
-        if (row < rows) {
-            const int at = slot * arrays * win.bytes;
-            win.fetch(base + at, ring + at, x, row, d, rows);
-            if (residual) win.fetch(base + at + win.bytes, ring + at + win.bytes, residual, row, d, rows);
-        }
-        copy_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < D - 1; ++i) fetch(blockIdx.x + i * stride, i);
-    const float inv_d = 1.0f / (float)d;
-    int slot = 0, turn = 0;
-    for (int64_t row = blockIdx.x; row < rows; row += stride, turn ^= 1) {
-        if constexpr (D == 1) {
-            __syncthreads();  // everyone is done with the last row
-            fetch(row, 0);
-            copy_wait<0>();
-        } else {
-            copy_wait<D - 2>();
-        }
-        __syncthreads();  // everyone's copies of this row are there (and the last row is done with)
-        if constexpr (D > 1) fetch(row + (D - 1) * stride, slot == 0 ? D - 1 : slot - 1);
-        const uint8_t* at = ring + slot * arrays * win.bytes + Window<T>::skip(row, d);
-        const T* px = reinterpret_cast<const T*>(at);
-        const T* pr = reinterpret_cast<const T*>(at + win.bytes);
-        const auto value = [&](int c) {  // as the residual stream holds it
-            float v = Elem<T>::to_f32(px[c]);
-            if (residual) v = Elem<T>::to_f32(Elem<T>::from_f32(v + Elem<T>::to_f32(pr[c])));
-            return v;
-        };
-        float sum = 0.0f, top = 0.0f;
-#pragma unroll 4
-        for (int c = threadIdx.x; c < d; c += blockDim.x) {
-            const float v = value(c);
-            sum = fmaf(v, v, sum);
-            if (codes) top = fmaxf(top, fabsf(v * Elem<T>::to_f32(__ldg(weight + c))));
-        }
-        team_reduce<0, true>(sum, top, red[turn]);
-        const float r = 1.0f / sqrtf(fmaf(sum, inv_d, eps));
-        const float most = top * r;
-        const float scale = most > 0.0f ? most / 448.0f : 1.0f;
-        const float inv_scale = 1.0f / scale;
-        if (codes && threadIdx.x == 0) scales[row] = scale;
-        const int64_t e = row * d;
-#pragma unroll 4
-        for (int c = threadIdx.x; c < d; c += blockDim.x) {
-            const float v = value(c);
-            if (s_out) s_out[e + c] = Elem<T>::from_f32(v);
-            const float o = v * r * Elem<T>::to_f32(__ldg(weight + c));
-            if (y) y[e + c] = Elem<T>::from_f32(o);
-            if (codes) codes[e + c] = __nv_cvt_float_to_fp8(o * inv_scale, __NV_SATFINITE, __NV_E4M3);
-        }
-        if (++slot == D) slot = 0;
-    }
-    copy_wait<0>();
-}
-
-template <typename T, int EPT, int D>
-__global__ void __launch_bounds__(kRingThreads, EPT <= 16 ? 2 : 1)
-rmsnorm_backward_window_kernel(const T* d_y, const T* s, const T* __restrict__ weight, float eps,
-                               const T* d_s, T* d_x, float* __restrict__ part, int64_t rows, int d) {
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float2 red[2][32];
-    pdl_wait();
-    pdl_trigger();
-    const Window<T> win(d);
-    const bool add = d_s && d_x;
+    using R = typename Raw<T, W>::type;
     const int nt = blockDim.x;
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
-    const int64_t stride = gridDim.x;
-    auto fetch = [&](int64_t row, int slot) {
-        if (row < rows) {
-            const int at = slot * 3 * win.bytes;
-            win.fetch(base + at, ring + at, s, row, d, rows);
-            win.fetch(base + at + win.bytes, ring + at + win.bytes, d_y, row, d, rows);
-            if (add)
-                win.fetch(base + at + 2 * win.bytes, ring + at + 2 * win.bytes, d_s, row, d, rows);
-        }
-        copy_commit();
-    };
+    float acc[EPT][W];
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i) fetch(blockIdx.x + i * stride, i);
-    float acc[EPT];
+    for (int j = 0; j < EPT; ++j)
 #pragma unroll
-    for (int j = 0; j < EPT; ++j) acc[j] = 0.0f;
+        for (int k = 0; k < W; ++k) acc[j][k] = 0.0f;
     const float inv_d = 1.0f / (float)d;
-    int slot = 0, turn = 0;
-    for (int64_t row = blockIdx.x; row < rows; row += stride, turn ^= 1) {
-        if constexpr (D == 1) {
-            __syncthreads();  // everyone is done with the last row
-            fetch(row, 0);
-            copy_wait<0>();
-        } else {
-            copy_wait<D - 2>();
-        }
-        __syncthreads();  // everyone's copies of this row are there (and the last row is done with)
-        if constexpr (D > 1) fetch(row + (D - 1) * stride, slot == 0 ? D - 1 : slot - 1);
-        const uint8_t* at = ring + slot * 3 * win.bytes + Window<T>::skip(row, d);
-        const T* ps = reinterpret_cast<const T*>(at);
-        const T* py = reinterpret_cast<const T*>(at + win.bytes);
-        const T* pa = reinterpret_cast<const T*>(at + 2 * win.bytes);
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
         float sq = 0.0f, gs = 0.0f;
-#pragma unroll
+#pragma unroll 4
         for (int j = 0; j < EPT; ++j) {
-            const int c = threadIdx.x + j * nt;
+            const int c = (threadIdx.x + j * nt) * W;
             if (c >= d) continue;
-            const float fs = Elem<T>::to_f32(ps[c]);
-            sq = fmaf(fs, fs, sq);
-            gs = fmaf(Elem<T>::to_f32(py[c]) * Elem<T>::to_f32(__ldg(weight + c)), fs, gs);
+            float fs[W], fy[W], fw[W];
+            open<T, W>(*reinterpret_cast<const R*>(s + row * d + c), fs);
+            open<T, W>(*reinterpret_cast<const R*>(d_y + row * d + c), fy);
+            open<T, W>(__ldg(reinterpret_cast<const R*>(weight + c)), fw);
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                sq = fmaf(fs[k], fs[k], sq);
+                gs = fmaf(fy[k] * fw[k], fs[k], gs);
+            }
         }
         team_reduce<0, false>(sq, gs, red[turn]);
         const float r = 1.0f / sqrtf(fmaf(sq, inv_d, eps));
         const float back = gs * inv_d * r * r;
 #pragma unroll
         for (int j = 0; j < EPT; ++j) {
-            const int c = threadIdx.x + j * nt;
+            const int c = (threadIdx.x + j * nt) * W;
             if (c >= d) continue;
-            const float fs = Elem<T>::to_f32(ps[c]), fy = Elem<T>::to_f32(py[c]);
-            acc[j] = fmaf(fy, fs * r, acc[j]);
+            float fs[W], fy[W], fw[W], fa[W];
+            open<T, W>(*reinterpret_cast<const R*>(s + row * d + c), fs);
+            open<T, W>(*reinterpret_cast<const R*>(d_y + row * d + c), fy);
+#pragma unroll
+            for (int k = 0; k < W; ++k) acc[j][k] = fmaf(fy[k], fs[k] * r, acc[j][k]);
             if (!d_x) continue;
-            const float g = fy * Elem<T>::to_f32(__ldg(weight + c));
-            d_x[row * d + c] = Elem<T>::from_f32(
-                fmaf(r, fmaf(-back, fs, g), add ? Elem<T>::to_f32(pa[c]) : 0.0f));
+            open<T, W>(__ldg(reinterpret_cast<const R*>(weight + c)), fw);
+            open<T, W>(d_s ? *reinterpret_cast<const R*>(d_s + row * d + c) : R{}, fa);
+#pragma unroll
+            for (int k = 0; k < W; ++k) fa[k] = fmaf(r, fmaf(-back, fs[k], fy[k] * fw[k]), fa[k]);
+            if constexpr (W == 1) d_x[row * d + c] = Elem<T>::from_f32(fa[0]);
+            else *reinterpret_cast<uint4*>(d_x + row * d + c) = pack(fa, (const T*)nullptr);
         }
-        if (++slot == D) slot = 0;
     }
-    copy_wait<0>();
     if (!part) return;
 #pragma unroll
     for (int j = 0; j < EPT; ++j) {
-        const int c = threadIdx.x + j * nt;
-        if (c < d) part[(int64_t)blockIdx.x * d + c] = acc[j];
+        const int c = (threadIdx.x + j * nt) * W;
+        if (c >= d) continue;
+#pragma unroll
+        for (int k = 0; k < W; ++k) part[(int64_t)blockIdx.x * d + c + k] = acc[j][k];
     }
 }
 
@@ -740,6 +631,8 @@ int blocks_that_fit(K kernel, int threads, size_t smem) {
     return (n > 0 ? n : 1) * device_sm_count();
 }
 
+int threads_for(int64_t lanes) { return (int)ceil_div(lanes, 32) * 32; }
+
 // launches kernel<..., RES, CODES> by what the call wants
 #define MOE_NORM_FLAGS(GO)                        \
     do {                                          \
@@ -751,7 +644,7 @@ int blocks_that_fit(K kernel, int threads, size_t smem) {
         return GO(false, false);                  \
     } while (0)
 
-template <typename T, int TEAM, int VPT, bool AL>
+template <typename T, int TEAM, bool AL>
 cudaError_t go_teams(const NormArgs& a, cudaStream_t st) {
     const auto go = [&](auto kernel) {
         const int64_t want = ceil_div(a.rows, kTeamThreads / TEAM);
@@ -760,103 +653,50 @@ cudaError_t go_teams(const NormArgs& a, cudaStream_t st) {
                           (const T*)a.x, (const T*)a.residual, (const T*)a.weight, a.eps, (T*)a.s,
                           (T*)a.y, a.codes, a.scales, a.rows, a.d);
     };
-#define MOE_GO(RES, CODES) go(rmsnorm_kernel<T, TEAM, VPT, AL, RES, CODES>)
+#define MOE_GO(RES, CODES) go(rmsnorm_kernel<T, TEAM, AL, RES, CODES>)
     MOE_NORM_FLAGS(MOE_GO);
 #undef MOE_GO
 }
 
-template <typename T, int VPT>
-cudaError_t go_blocks(const NormArgs& a, cudaStream_t st) {
+template <typename T, int VPT, bool AL>
+cudaError_t go_blocks(const NormArgs& a, int nv, cudaStream_t st) {
     const auto go = [&](auto kernel) {
-        const int64_t lanes = ceil_div(a.d, Elem<T>::kPerVec * VPT);
-        return launch_pdl(kernel, dim3((unsigned)a.rows), dim3((unsigned)ceil_div(lanes, 32) * 32), 0, st,
+        return launch_pdl(kernel, dim3((unsigned)a.rows), dim3(threads_for(ceil_div(nv, VPT))), 0, st,
                           (const T*)a.x, (const T*)a.residual, (const T*)a.weight, a.eps, (T*)a.s,
-                          (T*)a.y, a.codes, a.scales, a.d);
+                          (T*)a.y, a.codes, a.scales, a.rows, a.d);
     };
-#define MOE_GO(RES, CODES) go(rmsnorm_block_kernel<T, VPT, RES, CODES>)
+#define MOE_GO(RES, CODES) go(rmsnorm_block_kernel<T, VPT, AL, RES, CODES>)
     MOE_NORM_FLAGS(MOE_GO);
 #undef MOE_GO
 }
 
 template <typename T, bool AL>
 cudaError_t teams_for(const NormArgs& a, int nv, cudaStream_t st) {
-    if (nv <= 4) return go_teams<T, 4, 1, AL>(a, st);
-    if (nv <= 8) return go_teams<T, 8, 1, AL>(a, st);
-    if (nv <= 16) return go_teams<T, 16, 1, AL>(a, st);
-    if (nv <= 32) return go_teams<T, 32, 1, AL>(a, st);
-    return go_teams<T, 32, 2, AL>(a, st);
+    if (nv <= 4) return go_teams<T, 4, AL>(a, st);
+    if (nv <= 8) return go_teams<T, 8, AL>(a, st);
+    if (nv <= 16) return go_teams<T, 16, AL>(a, st);
+    return go_teams<T, 32, AL>(a, st);
 }
 
-int threads_for(int64_t lanes) { return (int)ceil_div(lanes, 32) * 32; }
-
-// Blocks an SM for a ring of `smem` bytes and blocks of `threads`, by what a GB300's SM has.
-int ring_blocks(size_t smem, int threads) {
-    const int by_smem = (int)(kRingSmem / smem), by_threads = 1024 / threads;
-    const int n = by_smem < by_threads ? by_smem : by_threads;
-    return n < 1 ? 1 : n > 16 ? 16 : n;
-}
-
-struct RingPlan {
-    int per_thread, threads, per_sm, depth;  // per_thread: columns
-    size_t smem;
-};
-
-// rows that start within vectors, more than 64 of them
-RingPlan window_plan(int dtype, int d, int arrays) {
-    RingPlan p{};
-    const int size = dtype == MOE_BF16 ? 2 : 4;
-    p.smem = (size_t)arrays * ((d * size + 30) / 16 * 16);
-    p.depth = kDepth * p.smem <= kRingSmem ? kDepth : 1;
-    p.smem *= p.depth;
-    p.per_thread = 4;
-    while (p.per_thread < 32 && d > p.per_thread * 256) p.per_thread *= 2;
-    p.threads = threads_for(ceil_div(d, p.per_thread));
-    p.per_sm = ring_blocks(p.smem, p.threads);
-    return p;
-}
-
-template <typename T>
-cudaError_t go_window(const NormArgs& a, cudaStream_t st) {
-    const RingPlan p = window_plan(a.dtype, a.d, a.residual ? 2 : 1);
-    auto kernel = p.depth == 1 ? rmsnorm_window_kernel<T, 1> : rmsnorm_window_kernel<T, kDepth>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
-    if (e != cudaSuccess) return e;
-    const int64_t wave = blocks_that_fit(kernel, p.threads, p.smem);
-    return launch_pdl(kernel, dim3((unsigned)(a.rows < wave ? a.rows : wave)), dim3(p.threads), p.smem,
-                      st, (const T*)a.x, (const T*)a.residual, (const T*)a.weight, a.eps, (T*)a.s,
-                      (T*)a.y, a.codes, a.scales, a.rows, a.d);
-}
-
-template <typename T, int TEAM, int VPT, int W>
-cudaError_t go_backward(const NormArgs& a, int threads, int blocks, cudaStream_t st) {
-    auto kernel = rmsnorm_backward_kernel<T, TEAM, VPT, W>;
-    const size_t smem = TEAM ? sizeof(float) * kTeamThreads * VPT * W : 0;
-    return launch_pdl(kernel, dim3(blocks), dim3(threads), smem, st, (const T*)a.d_y,
-                      (const T*)a.x, (const T*)a.weight, a.eps, (const T*)a.d_s, (T*)a.d_x, a.part,
-                      a.rows, a.d);
-}
-
-template <typename T>
+template <typename T, bool AL>
 cudaError_t forward(const NormArgs& a, cudaStream_t st) {
-    constexpr int V = Elem<T>::kPerVec;
-    if (a.d % V) {
-        const int nv = (int)ceil_div(a.d, V) + 1;  // vectors that cover a row, wherever it starts
-        return nv <= kTeamVecs ? teams_for<T, false>(a, nv, st) : go_window<T>(a, st);
-    }
-    const int nv = a.d / V;
-    if (nv <= kTeamVecs) return teams_for<T, true>(a, nv, st);
-    if (nv <= 2 * kBlockThreads<2>) return go_blocks<T, 2>(a, st);
-    if (nv <= 4 * kBlockThreads<4>) return go_blocks<T, 4>(a, st);
-    return go_blocks<T, 8>(a, st);
+    // vectors that cover a row, wherever it starts
+    const int nv = (int)ceil_div(a.d, Elem<T>::kPerVec) + (AL ? 0 : 1);
+    if (nv <= kTeamVecs) return teams_for<T, AL>(a, nv, st);
+    if (nv <= 2 * kBlockThreads<2>) return go_blocks<T, 2, AL>(a, nv, st);
+    if (nv <= 4 * kBlockThreads<4>) return go_blocks<T, 4, AL>(a, nv, st);
+    // 16384 fp32 values that start within a vector: 4097
+    return go_blocks<T, AL ? 8 : 9, AL>(a, nv, st);
 }
 
 // 16-byte vectors tile the rows
 bool whole_vectors(int dtype, int d) { return d % (dtype == MOE_BF16 ? 8 : 4) == 0; }
 
-// How the backward pass runs: teams within a warp (lanes > 0) of `per_thread` vectors (or
-// elements, where vectors do not tile the rows) a lane, or a ring a block.
+// How the backward pass runs: teams within a warp (lanes > 0) of a vector (or an element,
+// where vectors do not tile the rows) a lane; a ring a block; or, for rows too wide
+// for a ring, neither (smem 0).
 struct BackPlan {
-    int lanes, per_thread, threads, blocks, depth;
+    int lanes, per_thread, threads, blocks;
     size_t smem;
 };
 
@@ -866,38 +706,45 @@ struct BackPlan {
 BackPlan back_plan(int dtype, int64_t rows, int d) {
     BackPlan p{};
     const bool vec = whole_vectors(dtype, d);
-    const int nv = vec ? d / (dtype == MOE_BF16 ? 8 : 4) : d;
+    const int v = dtype == MOE_BF16 ? 8 : 4;
+    const int nt = vec ? d / v : d;                               // a team's
+    const int nv = vec ? d / v : (int)ceil_div(d, v) + 1;         // a block's
     int64_t want = rows, wave;
-    if (nv <= kTeamVecs) {
-        p.lanes = nv <= 4 ? 4 : nv <= 8 ? 8 : nv <= 16 ? 16 : 32;
-        p.per_thread = nv <= 32 ? 1 : 2;
+    if (nt <= kTeamVecs) {
+        p.lanes = nt <= 4 ? 4 : nt <= 8 ? 8 : nt <= 16 ? 16 : 32;
         p.threads = kTeamThreads;
         want = ceil_div(rows, kTeamThreads / p.lanes);
         wave = 152 * 4;
-    } else if (vec) {
-        p.per_thread = nv <= 2 * kRingThreads ? 2 : nv <= 4 * kRingThreads ? 4 : 8;
+    } else if ((size_t)kDepth * 2 * nv * 16 <= kRingSmem) {
+        p.per_thread = nv <= 2 * kBackThreads<2> ? 2 : nv <= 4 * kBackThreads<4> ? 4 : 5;
         p.threads = threads_for(ceil_div(nv, p.per_thread));
-        p.smem = (size_t)(p.per_thread <= 4 ? kDepth : 1) * 2 * nv * 16;
-        wave = 152 * ring_blocks(p.smem, p.threads);
+        p.smem = (size_t)kDepth * 2 * nv * 16;
+        // by what a GB300's SM has
+        const int by_smem = (int)(kRingSmem / p.smem), by_threads = 512 / p.threads;
+        const int n = by_smem < by_threads ? by_smem : by_threads;
+        wave = 152 * (n < 1 ? 1 : n > 16 ? 16 : n);
     } else {
-        const RingPlan w = window_plan(dtype, d, 3);
-        p.per_thread = w.per_thread;
-        p.threads = w.threads;
-        p.smem = w.smem;
-        p.depth = w.depth;
-        wave = 152 * w.per_sm;
+        p.per_thread = vec ? 4 : 16;
+        p.threads = threads_for(ceil_div(nt, p.per_thread));
+        wave = 152;
     }
     p.blocks = (int)(want < wave ? want : wave);
     return p;
 }
 
+template <typename T, int TEAM, int W>
+cudaError_t go_back_teams(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
+    return launch_pdl(rmsnorm_backward_kernel<T, TEAM, W>, dim3(p.blocks), dim3(kTeamThreads),
+                      sizeof(float) * kTeamThreads * W, st, (const T*)a.d_y, (const T*)a.x,
+                      (const T*)a.weight, a.eps, (const T*)a.d_s, (T*)a.d_x, a.part, a.rows, a.d);
+}
+
 template <typename T, int W>
 cudaError_t back_teams(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
-    if (p.lanes == 4) return go_backward<T, 4, 1, W>(a, p.threads, p.blocks, st);
-    if (p.lanes == 8) return go_backward<T, 8, 1, W>(a, p.threads, p.blocks, st);
-    if (p.lanes == 16) return go_backward<T, 16, 1, W>(a, p.threads, p.blocks, st);
-    if (p.per_thread == 1) return go_backward<T, 32, 1, W>(a, p.threads, p.blocks, st);
-    return go_backward<T, 32, 2, W>(a, p.threads, p.blocks, st);
+    if (p.lanes == 4) return go_back_teams<T, 4, W>(a, p, st);
+    if (p.lanes == 8) return go_back_teams<T, 8, W>(a, p, st);
+    if (p.lanes == 16) return go_back_teams<T, 16, W>(a, p, st);
+    return go_back_teams<T, 32, W>(a, p, st);
 }
 
 template <typename T>
@@ -913,24 +760,28 @@ cudaError_t backward(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
                           (const T*)a.x, (const T*)a.weight, a.eps, (const T*)a.d_s, (T*)a.d_x, a.part,
                           a.rows, a.d);
     };
-    if (!vec) {
-        // up to 4096 columns three rows of three arrays fit
-        if (p.per_thread == 4) return go(rmsnorm_backward_window_kernel<T, 4, kDepth>);
-        if (p.per_thread == 8) return go(rmsnorm_backward_window_kernel<T, 8, kDepth>);
-        if (p.per_thread == 16) return go(rmsnorm_backward_window_kernel<T, 16, kDepth>);
-        if (p.depth == 1) return go(rmsnorm_backward_window_kernel<T, 32, 1>);
-        return go(rmsnorm_backward_window_kernel<T, 32, kDepth>);
+    if constexpr (V == 4) {
+        if (p.smem == 0)
+            return vec ? go(rmsnorm_backward_wide_kernel<T, V, 4>)
+                       : go(rmsnorm_backward_wide_kernel<T, 1, 16>);
     }
-    if (p.per_thread == 2) return go(rmsnorm_backward_ring_kernel<T, 2>);
-    if constexpr (V == 4)
-        if (p.per_thread == 8) return go(rmsnorm_backward_ring_kernel<T, 8>);
-    return go(rmsnorm_backward_ring_kernel<T, 4>);
+#define MOE_RING(AL)                                                                  \
+    do {                                                                              \
+        if (p.per_thread == 2) return go(rmsnorm_backward_ring_kernel<T, 2, AL>);     \
+        if (p.per_thread == 4) return go(rmsnorm_backward_ring_kernel<T, 4, AL>);     \
+        return go(rmsnorm_backward_ring_kernel<T, 5, AL>);                            \
+    } while (0)
+    if (vec) MOE_RING(true);
+    MOE_RING(false);
+#undef MOE_RING
 }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t st) {
-    return a.dtype == MOE_BF16 ? forward<bf16>(a, st) : forward<float>(a, st);
+    const bool vec = whole_vectors(a.dtype, a.d);
+    if (a.dtype == MOE_BF16) return vec ? forward<bf16, true>(a, st) : forward<bf16, false>(a, st);
+    return vec ? forward<float, true>(a, st) : forward<float, false>(a, st);
 }
 
 int rmsnorm_backward_blocks(int64_t rows, int d) {
