@@ -363,7 +363,7 @@ __device__ __forceinline__ uint32_t ordered(float key) {
 }
 
 // The whole block chooses every token's experts (the rule of moe_route: the K largest keys,
-// ties to the lower expert) and lists the groups.  `keys`, `scores`: T * E words each.
+// ties to the lower expert) and lists the groups; the caller's barrier follows.  `keys`, `scores`: T * E words each.
 __device__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* keys, float* scores) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int shared = a.Is > 0, slots = a.T * a.K;
@@ -428,6 +428,46 @@ __device__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* keys, float* scores
         }
     }
     __syncthreads();
+    if (slots <= 32) {
+        // a lane a slot; the groups in the order of their first slots
+        if (warp == 0) {
+            const bool on = lane < slots;
+            const int e = on ? ctl->pick[lane] : 0x10000 + lane;
+            const uint32_t peers = __match_any_sync(0xffffffffu, e);
+            const int leader = __ffs(peers) - 1, t = lane / a.K;
+            const uint32_t leaders = __ballot_sync(0xffffffffu, on && leader == lane);
+            const int g = shared + __popc(leaders & ((1u << leader) - 1u));
+            uint32_t mask = 0;  // tokens of the group: slots t K .. t K + K - 1 are token t's
+            for (int q = 0; q < a.T; ++q)
+                if (peers >> (q * a.K) & ((2u << (a.K - 1)) - 1u)) mask |= 1u << q;
+            int n = on && leader == lane ? __popc(mask) : 0;
+            const int own = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, n, o);
+                if (lane >= o) n += v;
+            }
+            const int row0 = __shfl_sync(0xffffffffu, n - own + (shared ? a.T : 0), leader);
+            if (on) {
+                if (leader == lane) {
+                    ctl->expert[g] = (uint16_t)e;
+                    ctl->mask[g] = (uint16_t)mask;
+                    ctl->row0[g] = (uint16_t)row0;
+                }
+                ctl->pick[lane] = (uint16_t)(row0 + __popc(mask & ((1u << t) - 1u)));
+            }
+            if (lane == 0) {
+                ctl->groups = shared + __popc(leaders);
+                if (shared) {
+                    ctl->expert[0] = 0;
+                    ctl->mask[0] = (uint16_t)((1u << a.T) - 1u);
+                    ctl->row0[0] = 0;
+                }
+            }
+        }
+        if (a.xs && threadIdx.x < a.T) ctl->xs[threadIdx.x] = __ldcg(a.xs + threadIdx.x);
+        return;
+    }
     // picked experts before each 32, in every warp's lanes
     const uint32_t word = ctl->present[lane];
     int before = __popc(word);
@@ -1139,7 +1179,7 @@ constexpr int kClaimInts = 64;
 // Parts that K is cut into: enough that every block gets about this many units, were all
 // experts equally likely, with at least this many stages left in each.
 constexpr double kGateUnits = 2, kDownUnits = 3;
-constexpr int kLeastStages = 4;
+constexpr int kLeastStages = 8;
 
 int score_splits(int d) {
     const int n = d / 8 / 96;  // about three 16-byte vectors a lane
