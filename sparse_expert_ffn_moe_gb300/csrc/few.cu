@@ -261,12 +261,18 @@ few_scores_kernel(const bf16* __restrict__ x, const bf16* __restrict__ w_g,
                   float* __restrict__ part, uint8_t* __restrict__ xq, float* __restrict__ xs,
                   int* __restrict__ counters, int n_counters, int T, int d, int E, int splits,
                   int score_blocks) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nvec = d / 8, vps = (nvec + splits - 1) / splits;
+    if (blockIdx.x < score_blocks) {
+        // a hint for the first unit's weights: nothing is read before the wait
+        const int u = blockIdx.x * kScoreWarps + warp, v = u % splits * vps + lane * 8;
+        if (u / splits < E && v < nvec && lane * 8 < vps)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(w_g + (int64_t)(u / splits) * d + v * 8));
+    }
     pdl_wait();
     pdl_trigger();
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_counters; i += gridDim.x * blockDim.x)
         counters[i] = 0;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nvec = d / 8;
     if (blockIdx.x >= score_blocks) {
         __shared__ float red[kScoreWarps];
         const int t = blockIdx.x - score_blocks;
@@ -304,7 +310,7 @@ few_scores_kernel(const bf16* __restrict__ x, const bf16* __restrict__ w_g,
         }
         return;
     }
-    const int chunks = (T + TT - 1) / TT, vps = (nvec + splits - 1) / splits;
+    const int chunks = (T + TT - 1) / TT;
     const int units = chunks * E * splits;
     for (int u = blockIdx.x * kScoreWarps + warp; u < units; u += score_blocks * kScoreWarps) {
         const int s = u % splits, e = (u / splits) % E, t0 = u / (splits * E) * TT;
@@ -526,57 +532,76 @@ __device__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* keys, float* scores
 }
 
 // y of a tile of 128 columns from every part of every row: the shared expert first, then a
-// token's picks in their order.  A warp takes a token, or a strand of its parts where there
-// are fewer tokens than warps.
-__device__ void join_tile(const FewArgs& a, Ctl* ctl, int m, int warp, int lane) {
+// token's picks in their order.  A warp takes EACH tokens side by side, or a strand of a
+// token's parts where there are fewer tokens than warps.
+template <int EACH>
+__device__ __forceinline__ void join_tokens(const FewArgs& a, Ctl* ctl, int m, int warp, int lane) {
     const int shared = a.Is > 0;
     const int c = m * kDownRows + lane * 4;
     const bool in = c < a.d;
     const int strands = a.T == 1 ? 4 : a.T == 2 ? 2 : 1;
     const int n = (shared + a.K) * a.dp;
-    for (int item = warp; item < a.T * strands; item += 4) {
-        const int t = item / strands, q = item % strands;
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (in) {
-#pragma unroll 8
-            for (int i = q; i < n; i += strands) {
-                const int j = i / a.dp - shared;
+    const int t0 = warp / strands, q = warp % strands;  // tokens t0, t0 + 4, ...
+    float4 s[EACH];
+    uint2 r[EACH];
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        s[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        // not through the read-only path: y may be the residual itself
+        const int t = t0 + 4 * k;
+        r[k] = in && a.residual && t < a.T
+                   ? *reinterpret_cast<const uint2*>(a.residual + (int64_t)t * a.d + c) : make_uint2(0u, 0u);
+    }
+    if (in) {
+        const float* yp = a.yp + c;
+#pragma unroll(8 / EACH)
+        for (int i = q; i < n; i += strands) {
+            const int e = a.dp == 1 ? i : i / a.dp, j = e - shared, part = i - e * a.dp;
+#pragma unroll
+            for (int k = 0; k < EACH; ++k) {
+                const int t = min(t0 + 4 * k, a.T - 1);  // past the last token: again, not stored
                 const int row = j < 0 ? t : ctl->pick[t * a.K + j];
                 const float w = j < 0 ? 1.0f : ctl->weight[t * a.K + j];
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                    a.yp + ((int64_t)row * a.dp + i % a.dp) * a.d + c));
-                s.x = fmaf(w, v.x, s.x);
-                s.y = fmaf(w, v.y, s.y);
-                s.z = fmaf(w, v.z, s.z);
-                s.w = fmaf(w, v.w, s.w);
+                const float4 v =
+                    __ldcg(reinterpret_cast<const float4*>(yp + ((int64_t)row * a.dp + part) * a.d));
+                s[k].x = fmaf(w, v.x, s[k].x);
+                s[k].y = fmaf(w, v.y, s[k].y);
+                s[k].z = fmaf(w, v.z, s[k].z);
+                s[k].w = fmaf(w, v.w, s[k].w);
             }
         }
-        if (strands > 1) {  // then every warp has one item
-            *reinterpret_cast<float4*>(&ctl->strand[warp][lane * 4]) = s;
-            finish_sync();
-            if (q == 0)
-                for (int k = 1; k < strands; ++k) {
-                    const float4 v = *reinterpret_cast<const float4*>(&ctl->strand[warp + k][lane * 4]);
-                    s.x += v.x;
-                    s.y += v.y;
-                    s.z += v.z;
-                    s.w += v.w;
-                }
-        }
-        if (!in || q != 0) continue;
-        const int64_t at = (int64_t)t * a.d + c;
-        if (a.residual) {
-            // not through the read-only path: y may be the residual itself
-            const uint2 v = *reinterpret_cast<const uint2*>(a.residual + at);
-            s.x += __uint_as_float(v.x << 16);
-            s.y += __uint_as_float(v.x & 0xffff0000u);
-            s.z += __uint_as_float(v.y << 16);
-            s.w += __uint_as_float(v.y & 0xffff0000u);
-        }
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
-        *reinterpret_cast<uint2*>(a.y + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                                         *reinterpret_cast<const uint32_t*>(&hi));
     }
+    if (strands > 1) {
+        *reinterpret_cast<float4*>(&ctl->strand[warp][lane * 4]) = s[0];
+        finish_sync();
+        if (q != 0) return;
+        for (int k = 1; k < strands; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(&ctl->strand[warp + k][lane * 4]);
+            s[0].x += v.x;
+            s[0].y += v.y;
+            s[0].z += v.z;
+            s[0].w += v.w;
+        }
+    }
+    if (!in) return;
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const int t = t0 + 4 * k;
+        if (t >= a.T) continue;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(s[k].x + __uint_as_float(r[k].x << 16),
+                                                        s[k].y + __uint_as_float(r[k].x & 0xffff0000u));
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(s[k].z + __uint_as_float(r[k].y << 16),
+                                                        s[k].w + __uint_as_float(r[k].y & 0xffff0000u));
+        *reinterpret_cast<uint2*>(a.y + (int64_t)t * a.d + c) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+}
+
+template <int NT>
+__device__ __forceinline__ void join_tile(const FewArgs& a, Ctl* ctl, int m, int warp, int lane) {
+    if constexpr (NT == 16) join_tokens<4>(a, ctl, m, warp, lane);
+    else if (a.T <= 4) join_tokens<1>(a, ctl, m, warp, lane);
+    else join_tokens<2>(a, ctl, m, warp, lane);
 }
 
 // Counts a tile's finished part; true in the four warps of the block that finished the last
@@ -1089,7 +1114,7 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                     if (!last_part(ctl, counter, FMT ? 2 * a.gp : a.gp, r)) continue;
                     finish_h<FMT, NT>(a, ctl, un, r, shared);
                 } else if (last_part(ctl, a.dticket + un.tile, ctl->groups * a.dp, r)) {
-                    join_tile(a, ctl, un.tile, warp & 3, lane);
+                    join_tile<NT>(a, ctl, un.tile, warp & 3, lane);
                 }
             }
         }
@@ -1176,15 +1201,15 @@ cudaError_t go(const FewArgs& a, cudaStream_t st) {
 }
 
 constexpr int kClaimInts = 64;
-// Parts that K is cut into: enough that every block gets about this many units, were all
-// experts equally likely, with at least this many stages left in each.
-constexpr double kGateUnits = 2, kDownUnits = 3;
-constexpr int kLeastStages = 8;
-
 int score_splits(int d) {
     const int n = d / 8 / 96;  // about three 16-byte vectors a lane
     return n < 1 ? 1 : n > kScoreSplits ? kScoreSplits : n;
 }
+
+// Parts that K is cut into: enough that every block gets about this many units, were all
+// experts equally likely, with at least this many stages left in each.
+constexpr double kGateUnits = 2, kDownUnits = 3;
+constexpr int kLeastStages = 8;
 
 int parts_for(double tiles, double units, int64_t k_tiles) {
     const double sms = 152;  // not asked of the device: the workspace query needs none
