@@ -233,10 +233,10 @@ rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, floa
 // of their rows keep the memory busy; blocks that stayed for many rows, with or without a ring
 // of copies ahead, did not (16384 x 7168 bf16 with residual and codes: 178 and 186 us, this
 // 153).  AL: whole vectors tile the rows.
-template <int VPT> constexpr int kBlockThreads = VPT <= 4 ? 256 : 512;
+constexpr int kBlockThreads = 512;  // most threads of a block
 
 template <typename T, int VPT, bool AL, bool RES, bool CODES>
-__global__ void __launch_bounds__(kBlockThreads<VPT>, VPT <= 4 ? 4 : 1)
+__global__ void __launch_bounds__(kBlockThreads, VPT <= 2 ? 4 : VPT <= 4 ? 2 : 1)
 rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight, float eps, T* s_out,
                      T* y, uint8_t* codes, float* __restrict__ scales, int64_t rows, int d) {
     constexpr int V = Elem<T>::kPerVec;
@@ -683,10 +683,19 @@ cudaError_t forward(const NormArgs& a, cudaStream_t st) {
     // vectors that cover a row, wherever it starts
     const int nv = (int)ceil_div(a.d, Elem<T>::kPerVec) + (AL ? 0 : 1);
     if (nv <= kTeamVecs) return teams_for<T, AL>(a, nv, st);
-    if (nv <= 2 * kBlockThreads<2>) return go_blocks<T, 2, AL>(a, nv, st);
-    if (nv <= 4 * kBlockThreads<4>) return go_blocks<T, 4, AL>(a, nv, st);
-    // 16384 fp32 values that start within a vector: 4097
-    return go_blocks<T, AL ? 8 : 9, AL>(a, nv, st);
+    // Two vectors a thread, so that registers allow four blocks of 512; four a thread where a
+    // row is one array in and one out (16384 x 7168 bf16: 69 us against 77; with a residual 135
+    // against 134, rows of 2049 fp32 values 75 against 72).
+    if (AL && !a.residual && !a.codes && nv > kBlockThreads && nv <= 2 * kBlockThreads)
+        return go_blocks<T, 4, AL>(a, nv, st);
+    if (nv <= 2 * kBlockThreads) return go_blocks<T, 2, AL>(a, nv, st);
+    if constexpr (Elem<T>::kPerVec == 4) {
+        // 16384 values that start within a vector: 4097
+        if (nv > 4 * kBlockThreads) return go_blocks<T, AL ? 8 : 9, AL>(a, nv, st);
+        return go_blocks<T, 4, AL>(a, nv, st);
+    } else {
+        return go_blocks<T, AL ? 4 : 5, AL>(a, nv, st);
+    }
 }
 
 // 16-byte vectors tile the rows
