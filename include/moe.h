@@ -535,10 +535,11 @@ moe_status moe_combine_backward(const moe_shape *shape, const void *d_y,
  * residual itself, not x.  The intermediates are finer than moe_forward's: sums,
  * expert outputs and the combine stay in fp32, h is read as planes of 16 (bf16
  * weights) or 12 bits (8-bit weights), x exactly -- with 8-bit weights down to
- * 2^-23 of the token's largest value.
+ * 2^-21 of the token's largest value.
  * The same bits on every run.  No call waits for a part of the grid that is not
  * running, so calls on several streams (each with its own workspace) may overlap.
- * A token whose row is not finite spoils no other token.  Graph capturable.
+ * A token whose row is not finite shows it and spoils no other token.  Graph
+ * capturable.
  * Workspace: moe_few_workspace_bytes (0 for an invalid shape or T > 16); its error
  * word is cleared first, a wait that ran out is recorded there (MOE_ERR_TIMEOUT).
  */

@@ -516,8 +516,11 @@ def moe_forward_few_fp8_blocks(shape, x, w_g, bias, w: moe_fp8_experts, residual
              residual, y, workspace, stream)
 
 
+_ROW_DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+
+
 def _norm_dtype(x, name: str):
-    dtype = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}.get(x.dtype)
+    dtype = _ROW_DTYPES.get(x.dtype)
     if dtype is None:
         raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, not {x.dtype}")
     return dtype

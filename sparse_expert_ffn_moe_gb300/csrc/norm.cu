@@ -624,13 +624,6 @@ rmsnorm_dw_kernel(const float* __restrict__ part, int n, int d, float* __restric
     if (cx == 0 && blockIdx.x * 32 + ry < d) d_weight[blockIdx.x * 32 + ry] = v;
 }
 
-template <typename K>
-int blocks_that_fit(K kernel, int threads, size_t smem) {
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess) n = 1;
-    return (n > 0 ? n : 1) * device_sm_count();
-}
-
 int threads_for(int64_t lanes) { return (int)ceil_div(lanes, 32) * 32; }
 
 // launches kernel<..., RES, CODES> by what the call wants
@@ -648,7 +641,7 @@ template <typename T, int TEAM, bool AL>
 cudaError_t go_teams(const NormArgs& a, cudaStream_t st) {
     const auto go = [&](auto kernel) {
         const int64_t want = ceil_div(a.rows, kTeamThreads / TEAM);
-        const int64_t wave = blocks_that_fit(kernel, kTeamThreads, 0);
+        const int64_t wave = (int64_t)device_sm_count() * (2048 / kTeamThreads);
         return launch_pdl(kernel, dim3((unsigned)(want < wave ? want : wave)), dim3(kTeamThreads), 0, st,
                           (const T*)a.x, (const T*)a.residual, (const T*)a.weight, a.eps, (T*)a.s,
                           (T*)a.y, a.codes, a.scales, a.rows, a.d);
@@ -762,9 +755,11 @@ cudaError_t backward(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
     const bool vec = whole_vectors(a.dtype, a.d);
     if (p.lanes) return vec ? back_teams<T, V>(a, p, st) : back_teams<T, 1>(a, p, st);
     const auto go = [&](auto kernel) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
-        if (e != cudaSuccess) return e;
+        if (p.smem > 48 * 1024) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+            if (e != cudaSuccess) return e;
+        }
         return launch_pdl(kernel, dim3(p.blocks), dim3(p.threads), p.smem, st, (const T*)a.d_y,
                           (const T*)a.x, (const T*)a.weight, a.eps, (const T*)a.d_s, (T*)a.d_x, a.part,
                           a.rows, a.d);
@@ -798,10 +793,13 @@ int rmsnorm_backward_blocks(int64_t rows, int d) {
     return a > b ? a : b;
 }
 
-cudaError_t launch_rmsnorm_backward(const NormArgs& a, cudaStream_t st) {
+cudaError_t launch_rmsnorm_backward(const NormArgs& args, cudaStream_t st) {
+    NormArgs a = args;
     const BackPlan p = back_plan(a.dtype, a.rows, a.d);
+    const bool one = p.blocks == 1;  // its partial row is the sum
+    if (one && a.part) a.part = a.d_weight;
     const cudaError_t e = a.dtype == MOE_BF16 ? backward<bf16>(a, p, st) : backward<float>(a, p, st);
-    if (e != cudaSuccess || !a.part) return e;
+    if (e != cudaSuccess || !a.part || one) return e;
     return launch_pdl(rmsnorm_dw_kernel, dim3((unsigned)ceil_div(a.d, 32)), dim3(1024), 0, st,
                       (const float*)a.part, p.blocks, a.d, a.d_weight);
 }

@@ -70,8 +70,8 @@ def matrix(c, n, e=None):
 def layer(c):
     """(y, bound of its error): with M the magnitudes that a sum adds, a sum on the tensor
     cores is off by (n / 16 + 32) 2^-23 M (an add a product of 16 terms, the parts and planes
-    after it, each losing at most a last place); x 2^-22 of the row's largest value under 8-bit
-    weights; SiLU 2^-20 of it; h 2^-16 (bf16) or 2^-12 of its value and, with 8-bit weights,
+    after it, each losing at most a last place); x 2^-21 of the row's largest value under 8-bit
+    weights (half a step of the second plane, 2^-10 / 16, of a scale below 1 / 224 of it); SiLU 2^-20 of it; h 2^-16 (bf16) or 2^-12 of its value and, with 8-bit weights,
     2^-21 of the largest of its 128 (448 steps of a scale, the third plane's half step 2^-10
     finer by 16^2); a routing weight 2^-18; y rounded once, 2^-8."""
     x, T = c["x"].double(), c["T"]
@@ -93,7 +93,7 @@ def layer(c):
         cx = (c["d"] / 16 + 32) * 2.0 ** -23
         off_x = xr.abs() * cx
         if eight:
-            off_x = off_x + xr.abs().amax(1, keepdim=True) * 2.0 ** -22
+            off_x = off_x + xr.abs().amax(1, keepdim=True) * 2.0 ** -21
         dg, du = off_x @ gate.abs().T, off_x @ up.abs().T
         n = h.shape[1]
         dh = 1.1 * u.abs() * dg + act.abs() * du + h.abs() * 2.0 ** -20
