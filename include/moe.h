@@ -567,13 +567,15 @@ moe_status moe_forward_few_fp8_blocks(const moe_shape *shape, const void *x, con
  *            stream holds it; x itself without a residual)
  *   r      = 1 / sqrt(mean of s^2 + eps)                      (fp32)
  *   y      = s * r * weight                                   (fp32, rounded once)
- *   scales = max|y| / 448 of the row before its rounding (1 for a row of zeros),
+ *   scales = max|y| / 448 of the row before its rounding (1 for a row of zeros,
+ *            2^-126 at least),
  *   codes  = E4M3 nearest to y / scale -- the row format of the W8A8 calls
  * weight [cols] has the rows' dtype.  residual, s, y and codes may be NULL, not
  * both y and codes; codes and scales [rows] (fp32) go together.  s may be x or
  * residual itself, and y may be x; other overlaps are not allowed.  All
  * pointers 16-byte aligned.  The squares are summed in fp32: rows whose mean
- * square plus eps is a normal fp32 number.  eps is finite and not negative.
+ * square plus eps is a normal fp32 number, and with codes whose products
+ * s * weight are finite ones.  eps is finite and not negative.
  * A row with a NaN or an infinity spoils no other row.
  * Limits: rows < 2^31, 1 <= cols <= 16384 (any width; multiples of 16 bytes are
  * fastest).  rows == 0 is a no-op.  No workspace.

@@ -8,11 +8,12 @@
 // A row is read once and stays in registers between the sums and the stores:
 // sum(s^2) and max|s w| come from one reduction (max|y| = r max|s w|), so a row
 // costs its bytes and one block barrier.  A row goes to a team of threads: 4 to
-// 32 lanes of a warp (rows of at most 128 16-byte vectors), else a whole block.
+// 32 lanes of a warp (rows of at most 32 16-byte vectors), else a whole block.
 //
 // Rows that no 16-byte vector tiles (width odd, say) are read through the
 // aligned vectors that cover them; the two at the ends go by element.
 #include <cuda_fp8.h>
+#include <float.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -144,6 +145,12 @@ __device__ __forceinline__ void team_reduce(float& a, float& b, float2* red) {
     }
 }
 
+// The codes' scale of a row, at least the least normal number, so that its inverse is finite
+// (rows of denormal numbers would be NaN otherwise).
+__device__ __forceinline__ float row_scale(float most) {
+    return most > 0.0f ? fmaxf(most / 448.0f, FLT_MIN) : 1.0f;
+}
+
 // E4M3 codes of the values over the scale, four to a word
 template <int N>
 __device__ __forceinline__ void to_codes(const float (&f)[N], float inv_scale, uint32_t (&c)[N / 4]) {
@@ -217,7 +224,7 @@ rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, floa
         if (!live) continue;  // the last turn of a block of teams
         const float r = 1.0f / sqrtf(fmaf(sum, inv_d, eps));
         const float most = top * r;
-        const float scale = most > 0.0f ? most / 448.0f : 1.0f;
+        const float scale = row_scale(most);
         const float inv_scale = 1.0f / scale;
         if (CODES && lane == 0) scales[at] = scale;
         if (lane >= row.vecs) continue;
@@ -295,7 +302,7 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
     team_reduce<0, true>(sum, top, red);
     const float r = 1.0f / sqrtf(fmaf(sum, 1.0f / (float)d, eps));
     const float most = top * r;
-    const float scale = most > 0.0f ? most / 448.0f : 1.0f;
+    const float scale = row_scale(most);
     const float inv_scale = 1.0f / scale;
     if (CODES && threadIdx.x == 0) scales[blockIdx.x] = scale;
 #pragma unroll

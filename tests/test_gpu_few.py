@@ -12,7 +12,8 @@ SHAPES = [
     (1, 128, 1, 1, 128, 0), (1, 256, 8, 2, 512, 0), (2, 384, 6, 2, 256, 128),
     (3, 256, 5, 3, 384, 128), (8, 1024, 64, 6, 640, 1280), (16, 512, 16, 4, 256, 512),
     (4, 128, 40, 32, 128, 128), (13, 1152, 7, 7, 256, 896), (5, 128, 1024, 8, 128, 128),
-    (16, 2048, 64, 8, 1408, 0), (9, 640, 3, 1, 2048, 384), (8, 256, 64, 16, 1408, 128)]
+    (16, 2048, 64, 8, 1408, 0), (9, 640, 3, 1, 2048, 384), (8, 256, 64, 16, 1408, 128),
+    (16, 128, 1024, 32, 128, 128), (2, 16384, 2, 1, 128, 128), (2, 128, 2, 2, 16384, 16384)]
 # widths that are odd numbers of 64: bf16 weights alone
 ODD = [(1, 64, 1, 1, 64, 0), (3, 192, 5, 3, 320, 64), (16, 448, 300, 3, 64, 192),
        (7, 2112, 9, 4, 1344, 2688), (12, 64, 4, 2, 192, 0), (8, 192, 64, 16, 1472, 64),

@@ -112,6 +112,29 @@ def test_rows_of_zeros_and_of_infinities(moe, dtype, d):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [40, 7168, 1001])
+def test_rows_of_denormal_numbers(moe, dtype, d):
+    """Their scale is 2^-126, their codes are finite and within half the least step (2^-10)
+    of it, or half a step of the value."""
+    x = (torch.randn(9, d, generator=torch.Generator().manual_seed(d)) * 1e-40).to(DT[dtype])
+    x[3] = 0
+    x[:, 1] = 0
+    w = torch.ones(d).to(DT[dtype])
+    codes = torch.zeros(9, d, dtype=torch.uint8, device="cuda")
+    sc = torch.zeros(9, device="cuda")
+    moe.moe_rmsnorm(x.cuda(), None, w.cuda(), 1e-6, None, None, codes, sc)
+    torch.cuda.synchronize()
+    low = 2.0 ** -126
+    want = torch.full((9,), low)
+    want[3] = 1.0
+    assert torch.equal(sc.cpu(), want)
+    v = codes.view(torch.float8_e4m3fn).cpu().double() * low
+    y = ref.norm(x, w, 1e-6)
+    # 2^-149: the product's own rounding among denormal numbers, thrice
+    assert ((v - y).abs() <= 2.0 ** -4 * y.abs() + 2.0 ** -10 * low + 3 * 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,d", [(9, 7168), (300, 200), (11, 999)])
 def test_in_place(moe, dtype, T, d):
     """s in the residual's or x's place, y in x's: the bits of separate buffers."""
