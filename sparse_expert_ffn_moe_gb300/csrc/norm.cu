@@ -39,10 +39,22 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8], const bf16*) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// element k of a vector, as its bits
+template <typename T> struct Bits;
+template <> struct Bits<float> { using type = uint32_t; };
+template <> struct Bits<bf16> { using type = uint16_t; };
+template <typename T>
+__device__ __forceinline__ typename Bits<T>::type elem_of(const uint4& v, int k) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(T) == 4) return u[k];
+    else return (uint16_t)(u[k / 2] >> (16 * (k & 1)));
+}
+
 // A row that starts `skip` elements into a vector: vector c of the row is elements
 // c V - skip .. of it, those outside [0, d) not the row's.
 template <typename T, bool AL>
 struct Row {
+    using B = typename Bits<T>::type;
     static constexpr int V = Elem<T>::kPerVec;
     int64_t at;  // the first vector, in elements of the array; a multiple of V
     int skip, d, vecs;
@@ -52,83 +64,93 @@ struct Row {
         at = a - skip;
         vecs = AL ? d_ / V : (skip + d_ + V - 1) / V;
     }
-    __device__ __forceinline__ bool whole(int c) const {
-        return AL || (c * V >= skip && c * V + V <= skip + d);
+    // The i-th of the row's vectors, its ends last: what they cost more is paid by one warp.
+    __device__ __forceinline__ int place(int i) const { return AL ? i : i + 1 < vecs ? i + 1 : 0; }
+    // The vectors but for the ends: whole, and those of the weight that they cover are too.
+    __device__ __forceinline__ bool inner(int c) const {
+        return AL || (unsigned)(c - 1) < (unsigned)max(vecs - 3, 0);
     }
     __device__ __forceinline__ bool has(int c, int k) const {
         return AL || (c * V + k >= skip && c * V + k < skip + d);
     }
-    // vector c of p, elements that are not the row's 0; `total`: elements of the array
-    __device__ __forceinline__ uint4 load(const T* p, int c, int64_t total) const {
-        if (AL) return *reinterpret_cast<const uint4*>(p + at + c * V);
-        const int64_t e = at + c * V;
-        if (e + V > total) {  // the array's last vector
-            float f[V];
-#pragma unroll
-            for (int k = 0; k < V; ++k) f[k] = has(c, k) ? Elem<T>::to_f32(p[e + k]) : 0.0f;
-            return pack(f, (const T*)nullptr);
-        }
-        return mask(*reinterpret_cast<const uint4*>(p + e), c);
+    // vector c of p, with elements of the rows beside it; `total`: elements of the array
+    __device__ __forceinline__ uint4 covering(const T* p, int c, int64_t total) const {
+        if (inner(c) || at + c * V + V <= total) return *reinterpret_cast<const uint4*>(p + at + c * V);
+        return gather(p + at + c * V, c);  // the array's last vector
     }
-    __device__ __forceinline__ uint4 mask(const uint4& v, int c) const {
-        if (whole(c)) return v;
-        float f[V];
-        unpack(v, f, (const T*)nullptr);
+    // elements of the vector that are the row's one by one, 0 for the others
+    __device__ __forceinline__ uint4 gather(const T* p, int c) const {
+        uint32_t u[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int k = 0; k < V; ++k) f[k] = has(c, k) ? f[k] : 0.0f;
-        return pack(f, (const T*)nullptr);
+        for (int k = 0; k < V; ++k) {
+            const uint32_t e = has(c, k) ? *reinterpret_cast<const B*>(p + k) : 0u;
+            if constexpr (V == 4) u[k] = e;
+            else u[k / 2] |= e << (16 * (k & 1));
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    // elements that are not the row's 0
+    __device__ __forceinline__ uint4 mask(const uint4& v, int c) const {
+        if (inner(c)) return v;
+        uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            if constexpr (V == 4) u[k] = has(c, k) ? u[k] : 0u;
+            else u[k / 2] &= has(c, k) ? 0xffffffffu : k & 1 ? 0xffffu : 0xffff0000u;
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    __device__ __forceinline__ uint4 load(const T* p, int c, int64_t total) const {
+        return mask(covering(p, c, total), c);
     }
     __device__ __forceinline__ void store(T* p, int c, const uint4& v) const {
-        if (whole(c)) {
+        if (inner(c)) {
             *reinterpret_cast<uint4*>(p + at + c * V) = v;
             return;
         }
-        float f[V];
-        unpack(v, f, (const T*)nullptr);
+        B* q = reinterpret_cast<B*>(p + at + c * V);
 #pragma unroll
         for (int k = 0; k < V; ++k)
-            if (has(c, k)) p[at + c * V + k] = Elem<T>::from_f32(f[k]);
+            if (has(c, k)) q[k] = elem_of<T>(v, k);
     }
-    // vector i of the weight itself, 0 past its end
-    __device__ __forceinline__ uint4 weight_vec(const T* w, int i) const {
-        if (i < 0 || i * V >= d) return make_uint4(0u, 0u, 0u, 0u);
-        if (i * V + V <= d) return ld_ro(w + i * V);
-        float f[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) f[k] = i * V + k < d ? Elem<T>::to_f32(__ldg(w + i * V + k)) : 0.0f;
-        return pack(f, (const T*)nullptr);
-    }
-    // the weights of vector c: `skip` elements of the vector before, then the next
+    // the weights of vector c: `skip` elements of the weight's vector before, then the next
     __device__ __forceinline__ uint4 weight(const T* w, int c) const {
         if (AL) return ld_ro(w + c * V);
-        const uint4 a = weight_vec(w, c - 1), b = weight_vec(w, c);
+        if (!inner(c)) return gather(w + c * V - skip, c);
+        const uint4 a = ld_ro(w + (c - 1) * V), b = ld_ro(w + c * V);
+        if (skip == 0) return b;
         uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        // x from element V - skip on: by 4, 2 and 1 words, and half a word of bf16
-        const int by = (V - skip) * (int)sizeof(T);  // bytes, 2 .. 16
-#pragma unroll
-        for (int q = 0; q < 4; ++q) x[q] = by & 16 ? x[q + 4] : x[q];
+        // x from element V - skip on: by two words, one, and half a word of bf16
+        const int by = (V - skip) * (int)sizeof(T);  // bytes, 2 .. 14
 #pragma unroll
         for (int q = 0; q < 6; ++q) x[q] = by & 8 ? x[q + 2] : x[q];
 #pragma unroll
         for (int q = 0; q < 5; ++q) x[q] = by & 4 ? x[q + 1] : x[q];
         if constexpr (sizeof(T) == 2)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[q] = by & 2 ? __funnelshift_r(x[q], x[q + 1], 16) : x[q];
+            for (int q = 0; q < 4; ++q) x[q] = __funnelshift_r(x[q], x[q + 1], (by & 2) * 8);
         return make_uint4(x[0], x[1], x[2], x[3]);
     }
 };
 
-// (sum, max) or (sum, sum) over the team, in every thread.  TEAM 0: the block, through
-// `red` (one of two buffers in turn, so that one barrier a row is enough).
-template <int TEAM, bool MAX>
+// What a team sums beside a: nothing, the largest of b, or b.
+enum { kAlone, kMax, kSum };
+template <int WITH>
+__device__ __forceinline__ void fold(float& a, float& b, int o) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    if constexpr (WITH != kAlone) {
+        const float t = __shfl_xor_sync(0xffffffffu, b, o);
+        b = WITH == kMax ? fmaxf(b, t) : b + t;
+    }
+}
+
+// Over the team, in every thread.  TEAM 0: the block, through `red` (one of two buffers in
+// turn, so that one barrier a row is enough).
+template <int TEAM, int WITH>
 __device__ __forceinline__ void team_reduce(float& a, float& b, float2* red) {
     constexpr int W = TEAM ? TEAM : 32;
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        const float t = __shfl_xor_sync(0xffffffffu, b, o);
-        b = MAX ? fmaxf(b, t) : b + t;
-    }
+    for (int o = W / 2; o > 0; o >>= 1) fold<WITH>(a, b, o);
     if constexpr (TEAM == 0) {
         const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
         if (lane == 0) red[threadIdx.x >> 5] = make_float2(a, b);
@@ -137,11 +159,7 @@ __device__ __forceinline__ void team_reduce(float& a, float& b, float2* red) {
         a = v.x;
         b = v.y;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            const float t = __shfl_xor_sync(0xffffffffu, b, o);
-            b = MAX ? fmaxf(b, t) : b + t;
-        }
+        for (int o = 16; o > 0; o >>= 1) fold<WITH>(a, b, o);
     }
 }
 
@@ -171,7 +189,7 @@ __device__ __forceinline__ void store_codes(uint8_t* codes, const Row<T, AL>& ro
     uint32_t q[V / 4];
     to_codes(f, inv_scale, q);
     uint8_t* p = codes + row.at + c * V;
-    if (row.whole(c)) {
+    if (row.inner(c)) {
         if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[V / 4 - 1]);
         else *reinterpret_cast<uint32_t*>(p) = q[0];
     } else {
@@ -201,11 +219,12 @@ rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, floa
     for (int64_t it = 0; it < turns; ++it, at += stride) {
         const Row<T, AL> row(at, d);
         const bool live = at < rows;
+        const int c = row.place(lane);
         const bool mine = live && lane < row.vecs;
-        uint4 sv = mine ? row.load(x, lane, total) : zero;
+        uint4 sv = mine ? row.load(x, c, total) : zero;
         float f[V], g[V];
         if constexpr (RES) {
-            const uint4 rv = mine ? row.load(residual, lane, total) : zero;
+            const uint4 rv = mine ? row.load(residual, c, total) : zero;
             unpack(sv, f, no);
             unpack(rv, g, no);
 #pragma unroll
@@ -213,59 +232,64 @@ rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, floa
             sv = pack(f, no);
         }
         unpack(sv, f, no);
-        unpack(lane < row.vecs ? row.weight(weight, lane) : zero, g, no);
+        unpack(lane < row.vecs ? row.weight(weight, c) : zero, g, no);
         float sum = 0.0f, top = 0.0f;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             sum = fmaf(f[k], f[k], sum);
             if (CODES) top = fmaxf(top, fabsf(f[k] * g[k]));
         }
-        team_reduce<TEAM, true>(sum, top, nullptr);
+        team_reduce<TEAM, CODES ? kMax : kAlone>(sum, top, nullptr);
         if (!live) continue;  // the last turn of a block of teams
-        const float r = 1.0f / sqrtf(fmaf(sum, inv_d, eps));
+        const float r = rsqrtf(fmaf(sum, inv_d, eps));
         const float most = top * r;
         const float scale = row_scale(most);
         const float inv_scale = 1.0f / scale;
         if (CODES && lane == 0) scales[at] = scale;
         if (lane >= row.vecs) continue;
-        if (s_out) row.store(s_out, lane, sv);
+        if (s_out) row.store(s_out, c, sv);
 #pragma unroll
         for (int k = 0; k < V; ++k) f[k] = f[k] * r * g[k];
-        if (y) row.store(y, lane, pack(f, no));
-        if constexpr (CODES) store_codes(codes, row, lane, f, inv_scale);
+        if (y) row.store(y, c, pack(f, no));
+        if constexpr (CODES) store_codes(codes, row, c, f, inv_scale);
     }
 }
 
-// A wide row: a block of its own, which ends with it.  Many small blocks in different parts
-// of their rows keep the memory busy; blocks that stayed for many rows, with or without a ring
-// of copies ahead, did not (16384 x 7168 bf16 with residual and codes: 178 and 186 us, this
-// 153).  AL: whole vectors tile the rows.
+// A wide row: a block of its own (or, up to kWarpVecs vectors, a warp), which ends with it.  Many
+// small blocks in different parts of their rows keep the memory busy; blocks that stayed for many
+// rows, with or without a ring of copies ahead, did not (16384 x 7168 bf16 with residual and
+// codes: 178 and 186 us, this 153).  AL: whole vectors tile the rows.
 constexpr int kBlockThreads = 512;  // most threads of a block
+constexpr int kWarpVecs = 128;      // widest row of a warp
+constexpr int kWarpRows = 8;        // most rows of a block of such warps
 
-template <typename T, int VPT, bool AL, bool RES, bool CODES>
-__global__ void __launch_bounds__(kBlockThreads, VPT <= 2 ? 4 : VPT <= 4 ? 2 : 1)
+template <typename T, int VPT, bool AL, bool RES, bool CODES, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kBlockThreads,
+                                  WARP ? (VPT <= 2 ? 8 : 4) : VPT <= 2 ? 4 : VPT <= 4 ? 2 : 1)
 rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight, float eps, T* s_out,
                      T* y, uint8_t* codes, float* __restrict__ scales, int64_t rows, int d) {
     constexpr int V = Elem<T>::kPerVec;
     __shared__ float2 red[32];
     pdl_wait();
     pdl_trigger();
-    const int nt = blockDim.x;
+    const int nt = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t at = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    if (WARP && at >= rows) return;
     const int64_t total = rows * d;
-    const Row<T, AL> row(blockIdx.x, d);
+    const Row<T, AL> row(at, d);
     const T* const no = nullptr;
     uint4 sv[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int c = threadIdx.x + j * nt;
-        sv[j] = c < row.vecs ? row.load(x, c, total) : make_uint4(0u, 0u, 0u, 0u);
+        const int i = tid + j * nt, c = row.place(i);
+        sv[j] = i < row.vecs ? row.load(x, c, total) : make_uint4(0u, 0u, 0u, 0u);
     }
     if constexpr (RES) {
         uint4 rv[VPT];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = threadIdx.x + j * nt;
-            rv[j] = c < row.vecs ? row.load(residual, c, total) : make_uint4(0u, 0u, 0u, 0u);
+            const int i = tid + j * nt, c = row.place(i);
+            rv[j] = i < row.vecs ? row.load(residual, c, total) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -279,36 +303,36 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
         if (s_out) {  // may be x or the residual: this thread's values, read above
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int c = threadIdx.x + j * nt;
-                if (c < row.vecs) row.store(s_out, c, sv[j]);
+                const int i = tid + j * nt, c = row.place(i);
+                if (i < row.vecs) row.store(s_out, c, sv[j]);
             }
         }
     }
     float sum = 0.0f, top = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int c = threadIdx.x + j * nt;
+        const int i = tid + j * nt, c = row.place(i);
         float f[V], g[V];
         unpack(sv[j], f, no);
 #pragma unroll
         for (int k = 0; k < V; ++k) sum = fmaf(f[k], f[k], sum);
         if constexpr (CODES) {
-            if (c >= row.vecs) continue;
+            if (i >= row.vecs) continue;
             unpack(row.weight(weight, c), g, no);
 #pragma unroll
             for (int k = 0; k < V; ++k) top = fmaxf(top, fabsf(f[k] * g[k]));
         }
     }
-    team_reduce<0, true>(sum, top, red);
-    const float r = 1.0f / sqrtf(fmaf(sum, 1.0f / (float)d, eps));
+    team_reduce<WARP ? 32 : 0, CODES ? kMax : kAlone>(sum, top, red);
+    const float r = rsqrtf(fmaf(sum, 1.0f / (float)d, eps));
     const float most = top * r;
     const float scale = row_scale(most);
     const float inv_scale = 1.0f / scale;
-    if (CODES && threadIdx.x == 0) scales[blockIdx.x] = scale;
+    if (CODES && tid == 0) scales[at] = scale;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int c = threadIdx.x + j * nt;
-        if (c >= row.vecs) continue;
+        const int i = tid + j * nt, c = row.place(i);
+        if (i >= row.vecs) continue;
         float f[V], g[V];
         unpack(sv[j], f, no);
         unpack(row.weight(weight, c), g, no);
@@ -326,78 +350,106 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
 // g = d_y w, xh = s r:   d_x = d_s + r (g - xh mean(g xh)),   d_w = sum over rows of d_y xh
 // From sum(s^2) and sum(g s), one reduction a row.  A thread keeps its columns for all
 // of its block's rows, so d_w is summed in registers, once per block over its teams,
-// and then by rmsnorm_dw_kernel over the blocks, always in the same order.
-// W elements a load: a 16-byte vector, or 1 for rows that vectors do not tile (the
-// columns of a thread have to be the same in every row).
-template <typename T, int W> struct Raw { using type = uint4; };
-template <typename T> struct Raw<T, 1> { using type = T; };
-
-template <typename T, int W>
-__device__ __forceinline__ void open(const typename Raw<T, W>::type& v, float (&f)[W]) {
-    if constexpr (W == 1) f[0] = Elem<T>::to_f32(v);
-    else unpack(v, f, (const T*)nullptr);
-}
-
-template <typename T, int TEAM, int W>
-__global__ void __launch_bounds__(kTeamThreads)
+// and then by rmsnorm_dw_kernel over the blocks, always in the same order.  Rows that
+// start within vectors (AL false) go to teams and blocks by where they start.
+template <typename T, int TEAM, int VPT, bool AL>
+__global__ void __launch_bounds__(kTeamThreads, VPT == 1 ? 3 : 2)
 rmsnorm_backward_kernel(const T* d_y, const T* s, const T* __restrict__ weight, float eps,
                         const T* d_s, T* d_x, float* __restrict__ part, int64_t rows, int d) {
-    using R = typename Raw<T, W>::type;
-    constexpr int per_block = kTeamThreads / TEAM, kCols = TEAM * W;
-    extern __shared__ float acc_sm[];  // [team of the block][columns of a team]
+    constexpr int V = Elem<T>::kPerVec, per_block = kTeamThreads / TEAM;
+    static_assert(per_block % V == 0, "a team's rows all start at the same place of a vector");
+    extern __shared__ float acc_sm[];  // [team of the block][d]
     pdl_wait();
     pdl_trigger();
-    const int team = threadIdx.x / TEAM, c = threadIdx.x % TEAM * W;
-    const int64_t stride = (int64_t)gridDim.x * per_block;
+    const int team = threadIdx.x / TEAM, lane = threadIdx.x % TEAM;
+    const int64_t stride = (int64_t)gridDim.x * per_block, total = rows * d;
     const int64_t first = (int64_t)blockIdx.x * per_block;
     const int64_t turns = first < rows ? (rows - first + stride - 1) / stride : 0;
     int64_t row = first + team;
-    const R zero = R{};
-    float fw[W], acc[W];
-    open<T, W>(c < d ? __ldg(reinterpret_cast<const R*>(weight + c)) : zero, fw);
+    Row<T, AL> here(row, d);
+    const T* const no = nullptr;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint4 wv[VPT], sv[VPT], yv[VPT], av[VPT];
+    float acc[VPT][V];
 #pragma unroll
-    for (int k = 0; k < W; ++k) acc[k] = 0.0f;
-    R sv, yv, av;
-    const auto fetch = [&](int64_t at) {
-        const bool go = at < rows && c < d;
-        sv = go ? *reinterpret_cast<const R*>(s + at * d + c) : zero;
-        yv = go ? *reinterpret_cast<const R*>(d_y + at * d + c) : zero;
-        av = go && d_s && d_x ? *reinterpret_cast<const R*>(d_s + at * d + c) : zero;
+    for (int j = 0; j < VPT; ++j) {
+        const int i = lane + j * TEAM;
+        wv[j] = i < here.vecs ? here.weight(weight, here.place(i)) : zero;
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[j][k] = 0.0f;
+    }
+    const bool add = d_s && d_x;
+    const auto fetch = [&](const Row<T, AL>& r, bool live) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = lane + j * TEAM, c = r.place(i);
+            const bool go = live && i < r.vecs;
+            sv[j] = go ? r.covering(s, c, total) : zero;
+            yv[j] = go ? r.covering(d_y, c, total) : zero;
+            av[j] = go && add ? r.covering(d_s, c, total) : zero;
+        }
     };
-    fetch(row);
+    fetch(here, row < rows);
     const float inv_d = 1.0f / (float)d;
     for (int64_t it = 0; it < turns; ++it, row += stride) {
-        float fs[W], fy[W], fa[W];
-        open<T, W>(sv, fs);
-        open<T, W>(yv, fy);
-        open<T, W>(av, fa);
-        if (it + 1 < turns) fetch(row + stride);  // in flight over this row
+        uint4 ms[VPT], my[VPT], ma[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = here.place(lane + j * TEAM);
+            ms[j] = here.mask(sv[j], c);
+            my[j] = here.mask(yv[j], c);
+            ma[j] = av[j];
+        }
+        Row<T, AL> next = here;
+        next.at += stride * d;
+        if (it + 1 < turns) fetch(next, row + stride < rows);  // in flight over this row
         float sq = 0.0f, gs = 0.0f;
 #pragma unroll
-        for (int k = 0; k < W; ++k) {
-            sq = fmaf(fs[k], fs[k], sq);
-            gs = fmaf(fy[k] * fw[k], fs[k], gs);
+        for (int j = 0; j < VPT; ++j) {
+            float fs[V], fy[V], fw[V];
+            unpack(ms[j], fs, no);
+            unpack(my[j], fy, no);
+            unpack(wv[j], fw, no);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                sq = fmaf(fs[k], fs[k], sq);
+                gs = fmaf(fy[k] * fw[k], fs[k], gs);
+            }
         }
-        team_reduce<TEAM, false>(sq, gs, nullptr);
-        if (row >= rows || c >= d) continue;
+        team_reduce<TEAM, kSum>(sq, gs, nullptr);
         const float r = 1.0f / sqrtf(fmaf(sq, inv_d, eps));
         const float back = gs * inv_d * r * r;  // times s: what the bracket takes off
 #pragma unroll
-        for (int k = 0; k < W; ++k) {
-            acc[k] = fmaf(fy[k], fs[k] * r, acc[k]);
-            fa[k] = fmaf(r, fmaf(-back, fs[k], fy[k] * fw[k]), fa[k]);
+        for (int j = 0; j < VPT; ++j) {
+            const int i = lane + j * TEAM;
+            if (row >= rows || i >= here.vecs) continue;
+            float fs[V], fy[V], fw[V], fa[V];
+            unpack(ms[j], fs, no);
+            unpack(my[j], fy, no);
+            unpack(wv[j], fw, no);
+            unpack(ma[j], fa, no);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                acc[j][k] = fmaf(fy[k], fs[k] * r, acc[j][k]);
+                fa[k] = fmaf(r, fmaf(-back, fs[k], fy[k] * fw[k]), fa[k]);
+            }
+            if (d_x) here.store(d_x, here.place(i), pack(fa, no));
         }
-        if (!d_x) continue;
-        if constexpr (W == 1) d_x[row * d + c] = Elem<T>::from_f32(fa[0]);
-        else *reinterpret_cast<uint4*>(d_x + row * d + c) = pack(fa, (const T*)nullptr);
+        here = next;
     }
     if (!part) return;
 #pragma unroll
-    for (int k = 0; k < W; ++k) acc_sm[team * kCols + c + k] = acc[k];
+    for (int j = 0; j < VPT; ++j) {
+        const int i = lane + j * TEAM, c = here.place(i);
+        if (i >= here.vecs) continue;
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (here.has(c, k)) acc_sm[team * d + c * V + k - here.skip] = acc[j][k];
+    }
     __syncthreads();
     for (int col = threadIdx.x; col < d; col += kTeamThreads) {
         float t = 0.0f;
-        for (int q = 0; q < per_block; ++q) t += acc_sm[q * kCols + col];
+        for (int q = 0; q < per_block; ++q) t += acc_sm[q * d + col];
         part[(int64_t)blockIdx.x * d + col] = t;
     }
 }
@@ -421,7 +473,7 @@ constexpr size_t kRingSmem = 220 * 1024;  // of an SM, for the rings of its bloc
 // to registers, asked for before the row's sums.  A thread's columns are the same in every
 // row: rows that start within vectors (AL false) go to blocks by where they start (the grid
 // is then a multiple of V, or has a row a block).
-template <int VPT> constexpr int kBackThreads = VPT <= 4 ? 256 : 512;
+template <int VPT> constexpr int kBackThreads = VPT == 2 ? 320 : VPT == 4 ? 256 : 512;
 
 template <typename T, int VPT, bool AL>
 __global__ void __launch_bounds__(kBackThreads<VPT>, VPT <= 4 ? 2 : 1)
@@ -446,17 +498,16 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
             const int64_t at = row * d - first.skip;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int c = threadIdx.x + j * nt;
-                if (c >= vecs) continue;
+                const int i = threadIdx.x + j * nt, c = first.place(i);
+                if (i >= vecs) continue;
                 const int to = slot * 2 * row_bytes + c * 16;
                 const int64_t e = at + c * V;
-                if (AL || e + V <= total) {
+                if (first.inner(c) || e + V <= total) {
                     copy_async(base + to, s + e);
                     copy_async(base + to + row_bytes, d_y + e);
                 } else {  // the arrays' last vector
-                    const Row<T, AL> last(row, d);
-                    *reinterpret_cast<uint4*>(ring + to) = last.load(s, c, total);
-                    *reinterpret_cast<uint4*>(ring + to + row_bytes) = last.load(d_y, c, total);
+                    *reinterpret_cast<uint4*>(ring + to) = first.gather(s + e, c);
+                    *reinterpret_cast<uint4*>(ring + to + row_bytes) = first.gather(d_y + e, c);
                 }
             }
         }
@@ -470,8 +521,8 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
     for (int j = 0; j < VPT; ++j) {
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[j][k] = 0.0f;
-        const int c = threadIdx.x + j * nt;
-        if constexpr (kKeep) wv[j] = c < vecs ? first.weight(weight, c) : zero;
+        const int i = threadIdx.x + j * nt, c = first.place(i);
+        if constexpr (kKeep) wv[j] = i < vecs ? first.weight(weight, c) : zero;
     }
     const float inv_d = 1.0f / (float)d;
     int slot = 0, turn = 0;
@@ -481,8 +532,8 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
         uint4 av[VPT], sv[kKeep ? VPT : 1], yv[kKeep ? VPT : 1];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = threadIdx.x + j * nt;
-            av[j] = add && c < vecs ? here.load(d_s, c, total) : zero;
+            const int i = threadIdx.x + j * nt, c = first.place(i);
+            av[j] = add && i < vecs ? here.covering(d_s, c, total) : zero;
         }
         copy_wait<kDepth - 2>();
         const uint8_t* mine = ring + slot * 2 * row_bytes;
@@ -492,9 +543,9 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
         float sq = 0.0f, gs = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = threadIdx.x + j * nt;
+            const int i = threadIdx.x + j * nt, c = first.place(i);
             if constexpr (kKeep) sv[j] = yv[j] = zero;
-            if (c >= vecs) continue;
+            if (i >= vecs) continue;
             const uint4 a = read(c, false), b = read(c, true);
             if constexpr (kKeep) {
                 sv[j] = a;
@@ -510,15 +561,15 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
                 gs = fmaf(fy[k] * fw[k], fs[k], gs);
             }
         }
-        team_reduce<0, false>(sq, gs, red[turn]);
+        team_reduce<0, kSum>(sq, gs, red[turn]);
         // into the place of the row before this one, used up before the barrier
         fetch(row + (kDepth - 1) * stride, slot == 0 ? kDepth - 1 : slot - 1);
         const float r = 1.0f / sqrtf(fmaf(sq, inv_d, eps));
         const float back = gs * inv_d * r * r;  // times s: what the bracket takes off
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = threadIdx.x + j * nt;
-            if (c >= vecs) continue;
+            const int i = threadIdx.x + j * nt, c = first.place(i);
+            if (i >= vecs) continue;
             float fs[V], fy[V], fw[V], fa[V];
             unpack(kKeep ? sv[kKeep ? j : 0] : read(c, false), fs, no);
             unpack(kKeep ? yv[kKeep ? j : 0] : read(c, true), fy, no);
@@ -538,12 +589,22 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
     if (!part) return;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int c = threadIdx.x + j * nt;
-        if (c >= vecs) continue;
+        const int i = threadIdx.x + j * nt, c = first.place(i);
+        if (i >= vecs) continue;
 #pragma unroll
         for (int k = 0; k < V; ++k)
             if (first.has(c, k)) part[(int64_t)blockIdx.x * d + c * V + k - first.skip] = acc[j][k];
     }
+}
+
+// W elements a load: a 16-byte vector, or one.
+template <typename T, int W> struct Raw { using type = uint4; };
+template <typename T> struct Raw<T, 1> { using type = T; };
+
+template <typename T, int W>
+__device__ __forceinline__ void open(const typename Raw<T, W>::type& v, float (&f)[W]) {
+    if constexpr (W == 1) f[0] = Elem<T>::to_f32(v);
+    else unpack(v, f, (const T*)nullptr);
 }
 
 // Rows too wide for a ring of three (fp32 rows of more than 8192): straight from memory, twice
@@ -580,7 +641,7 @@ rmsnorm_backward_wide_kernel(const T* d_y, const T* s, const T* __restrict__ wei
                 gs = fmaf(fy[k] * fw[k], fs[k], gs);
             }
         }
-        team_reduce<0, false>(sq, gs, red[turn]);
+        team_reduce<0, kSum>(sq, gs, red[turn]);
         const float r = 1.0f / sqrtf(fmaf(sq, inv_d, eps));
         const float back = gs * inv_d * r * r;
 #pragma unroll
@@ -658,14 +719,17 @@ cudaError_t go_teams(const NormArgs& a, cudaStream_t st) {
 #undef MOE_GO
 }
 
-template <typename T, int VPT, bool AL>
+template <typename T, int VPT, bool AL, bool WARP = false>
 cudaError_t go_blocks(const NormArgs& a, int nv, cudaStream_t st) {
     const auto go = [&](auto kernel) {
-        return launch_pdl(kernel, dim3((unsigned)a.rows), dim3(threads_for(ceil_div(nv, VPT))), 0, st,
+        // few rows of a warp each go to as many blocks
+        const int64_t per = WARP ? ceil_div(a.rows, 152) : 1, n = per < kWarpRows ? per : kWarpRows;
+        const int threads = WARP ? 32 * (int)n : threads_for(ceil_div(nv, VPT));
+        return launch_pdl(kernel, dim3((unsigned)ceil_div(a.rows, n)), dim3(threads), 0, st,
                           (const T*)a.x, (const T*)a.residual, (const T*)a.weight, a.eps, (T*)a.s,
                           (T*)a.y, a.codes, a.scales, a.rows, a.d);
     };
-#define MOE_GO(RES, CODES) go(rmsnorm_block_kernel<T, VPT, AL, RES, CODES>)
+#define MOE_GO(RES, CODES) go(rmsnorm_block_kernel<T, VPT, AL, RES, CODES, WARP>)
     MOE_NORM_FLAGS(MOE_GO);
 #undef MOE_GO
 }
@@ -683,6 +747,8 @@ cudaError_t forward(const NormArgs& a, cudaStream_t st) {
     // vectors that cover a row, wherever it starts
     const int nv = (int)ceil_div(a.d, Elem<T>::kPerVec) + (AL ? 0 : 1);
     if (nv <= kTeamVecs) return teams_for<T, AL>(a, nv, st);
+    if (nv <= kWarpVecs / 2) return go_blocks<T, 2, AL, true>(a, nv, st);
+    if (nv <= kWarpVecs) return go_blocks<T, 4, AL, true>(a, nv, st);
     // Two vectors a thread, so that registers allow four blocks of 512; four a thread where a
     // row is one array in and one out (16384 x 7168 bf16: 69 us against 77; with a residual 135
     // against 134, rows of 2049 fp32 values 75 against 72).
@@ -701,9 +767,8 @@ cudaError_t forward(const NormArgs& a, cudaStream_t st) {
 // 16-byte vectors tile the rows
 bool whole_vectors(int dtype, int d) { return d % (dtype == MOE_BF16 ? 8 : 4) == 0; }
 
-// How the backward pass runs: teams within a warp (lanes > 0) of a vector (or an element,
-// where vectors do not tile the rows) a lane; a ring a block; or, for rows too wide
-// for a ring, neither (smem 0).
+// How the backward pass runs: teams within a warp (lanes > 0) of one or two vectors a lane;
+// a ring a block; or, for rows too wide for a ring, neither (smem 0).
 struct BackPlan {
     int lanes, per_thread, threads, blocks;
     size_t smem;
@@ -716,51 +781,52 @@ BackPlan back_plan(int dtype, int64_t rows, int d) {
     BackPlan p{};
     const bool vec = whole_vectors(dtype, d);
     const int v = dtype == MOE_BF16 ? 8 : 4;
-    const int nt = vec ? d / v : d;                               // a team's
-    const int nv = vec ? d / v : (int)ceil_div(d, v) + 1;         // a block's
+    const int nv = vec ? d / v : (int)ceil_div(d, v) + 1;
     int64_t want = rows, wave;
-    if (nt <= kTeamVecs) {
-        p.lanes = nt <= 4 ? 4 : nt <= 8 ? 8 : nt <= 16 ? 16 : 32;
+    if (nv <= 2 * kTeamVecs) {
+        p.lanes = nv <= 4 ? 4 : nv <= 8 ? 8 : nv <= 16 ? 16 : 32;
+        p.per_thread = nv <= kTeamVecs ? 1 : 2;
         p.threads = kTeamThreads;
         want = ceil_div(rows, kTeamThreads / p.lanes);
-        wave = 152 * 4;
+        wave = 152 * (p.per_thread == 1 ? 3 : 2);
     } else if ((size_t)kDepth * 2 * nv * 16 <= kRingSmem) {
         p.per_thread = nv <= 2 * kBackThreads<2> ? 2 : nv <= 4 * kBackThreads<4> ? 4 : 5;
         p.threads = threads_for(ceil_div(nv, p.per_thread));
         p.smem = (size_t)kDepth * 2 * nv * 16;
         // by what a GB300's SM has
-        const int by_smem = (int)(kRingSmem / p.smem), by_threads = 512 / p.threads;
+        const int by_smem = (int)(kRingSmem / p.smem), by_threads = (p.per_thread == 2 ? 640 : 512) / p.threads;
         const int n = by_smem < by_threads ? by_smem : by_threads;
         wave = 152 * (n < 1 ? 1 : n > 16 ? 16 : n);
     } else {
         p.per_thread = vec ? 4 : 16;
-        p.threads = threads_for(ceil_div(nt, p.per_thread));
+        p.threads = threads_for(ceil_div(vec ? nv : d, p.per_thread));
         wave = 152;
     }
     p.blocks = (int)(want < wave ? want : wave);
     return p;
 }
 
-template <typename T, int TEAM, int W>
+template <typename T, int TEAM, int VPT, bool AL>
 cudaError_t go_back_teams(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
-    return launch_pdl(rmsnorm_backward_kernel<T, TEAM, W>, dim3(p.blocks), dim3(kTeamThreads),
-                      sizeof(float) * kTeamThreads * W, st, (const T*)a.d_y, (const T*)a.x,
+    return launch_pdl(rmsnorm_backward_kernel<T, TEAM, VPT, AL>, dim3(p.blocks), dim3(kTeamThreads),
+                      sizeof(float) * (kTeamThreads / TEAM) * a.d, st, (const T*)a.d_y, (const T*)a.x,
                       (const T*)a.weight, a.eps, (const T*)a.d_s, (T*)a.d_x, a.part, a.rows, a.d);
 }
 
-template <typename T, int W>
+template <typename T, bool AL>
 cudaError_t back_teams(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
-    if (p.lanes == 4) return go_back_teams<T, 4, W>(a, p, st);
-    if (p.lanes == 8) return go_back_teams<T, 8, W>(a, p, st);
-    if (p.lanes == 16) return go_back_teams<T, 16, W>(a, p, st);
-    return go_back_teams<T, 32, W>(a, p, st);
+    if (p.lanes == 4) return go_back_teams<T, 4, 1, AL>(a, p, st);
+    if (p.lanes == 8) return go_back_teams<T, 8, 1, AL>(a, p, st);
+    if (p.lanes == 16) return go_back_teams<T, 16, 1, AL>(a, p, st);
+    if (p.per_thread == 1) return go_back_teams<T, 32, 1, AL>(a, p, st);
+    return go_back_teams<T, 32, 2, AL>(a, p, st);
 }
 
 template <typename T>
 cudaError_t backward(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
     constexpr int V = Elem<T>::kPerVec;
     const bool vec = whole_vectors(a.dtype, a.d);
-    if (p.lanes) return vec ? back_teams<T, V>(a, p, st) : back_teams<T, 1>(a, p, st);
+    if (p.lanes) return vec ? back_teams<T, true>(a, p, st) : back_teams<T, false>(a, p, st);
     const auto go = [&](auto kernel) {
         if (p.smem > 48 * 1024) {
             const cudaError_t e =
