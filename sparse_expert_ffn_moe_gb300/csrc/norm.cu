@@ -56,11 +56,12 @@ template <typename T, bool AL>
 struct Row {
     using B = typename Bits<T>::type;
     static constexpr int V = Elem<T>::kPerVec;
+    static constexpr uint32_t kAll = (1u << V) - 1u;
     int64_t at;  // the first vector, in elements of the array; a multiple of V
     int skip, d, vecs;
     __device__ __forceinline__ Row(int64_t row, int d_) : d(d_) {
         const int64_t a = row * d_;
-        skip = AL ? 0 : (int)(a % V);
+        skip = AL ? 0 : (int)a & (V - 1);
         at = a - skip;
         vecs = AL ? d_ / V : (skip + d_ + V - 1) / V;
     }
@@ -73,17 +74,29 @@ struct Row {
     __device__ __forceinline__ bool has(int c, int k) const {
         return AL || (c * V + k >= skip && c * V + k < skip + d);
     }
+    // The same as bits.  The forward pass, which asks several times, keeps them (100000 rows of
+    // 777 bf16 values with codes 145 us, asking for each element 186); the backward pass, short
+    // of registers, does not (20011 x 4097 bf16: 127 us, with bits 133).
+    __device__ __forceinline__ uint32_t own(int c) const {
+        if (AL) return kAll;
+        const int lo = skip - c * V, hi = lo + d;
+        return kAll << max(lo, 0) & (hi < V ? (1u << max(hi, 0)) - 1u : kAll);
+    }
     // vector c of p, with elements of the rows beside it; `total`: elements of the array
     __device__ __forceinline__ uint4 covering(const T* p, int c, int64_t total) const {
         if (inner(c) || at + c * V + V <= total) return *reinterpret_cast<const uint4*>(p + at + c * V);
         return gather(p + at + c * V, c);  // the array's last vector
     }
-    // elements of the vector that are the row's one by one, 0 for the others
+    // the row's elements of a vector one by one, 0 for the others
     __device__ __forceinline__ uint4 gather(const T* p, int c) const {
+        return gather_if(p, [&](int k) { return has(c, k); });
+    }
+    template <typename Has>
+    __device__ __forceinline__ static uint4 gather_if(const T* p, Has mine) {
         uint32_t u[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const uint32_t e = has(c, k) ? *reinterpret_cast<const B*>(p + k) : 0u;
+            const uint32_t e = mine(k) ? *reinterpret_cast<const B*>(p + k) : 0u;
             if constexpr (V == 4) u[k] = e;
             else u[k / 2] |= e << (16 * (k & 1));
         }
@@ -92,26 +105,35 @@ struct Row {
     // elements that are not the row's 0
     __device__ __forceinline__ uint4 mask(const uint4& v, int c) const {
         if (inner(c)) return v;
+        return mask_if(v, [&](int k) { return has(c, k); });
+    }
+    __device__ __forceinline__ static uint4 mask_own(const uint4& v, uint32_t m) {
+        if (AL || m == kAll) return v;
+        return mask_if(v, [&](int k) { return (m >> k & 1u) != 0u; });
+    }
+    template <typename Has>
+    __device__ __forceinline__ static uint4 mask_if(const uint4& v, Has mine) {
         uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            if constexpr (V == 4) u[k] = has(c, k) ? u[k] : 0u;
-            else u[k / 2] &= has(c, k) ? 0xffffffffu : k & 1 ? 0xffffu : 0xffff0000u;
+            if constexpr (V == 4) u[k] = mine(k) ? u[k] : 0u;
+            else u[k / 2] &= mine(k) ? 0xffffffffu : k & 1 ? 0xffffu : 0xffff0000u;
         }
         return make_uint4(u[0], u[1], u[2], u[3]);
     }
-    __device__ __forceinline__ uint4 load(const T* p, int c, int64_t total) const {
-        return mask(covering(p, c, total), c);
-    }
     __device__ __forceinline__ void store(T* p, int c, const uint4& v) const {
-        if (inner(c)) {
-            *reinterpret_cast<uint4*>(p + at + c * V) = v;
-            return;
-        }
-        B* q = reinterpret_cast<B*>(p + at + c * V);
+        if (inner(c)) *reinterpret_cast<uint4*>(p + at + c * V) = v;
+        else store_if(p + at + c * V, v, [&](int k) { return has(c, k); });
+    }
+    __device__ __forceinline__ void store_own(T* p, int c, uint32_t m, const uint4& v) const {
+        if (AL || m == kAll) *reinterpret_cast<uint4*>(p + at + c * V) = v;
+        else store_if(p + at + c * V, v, [&](int k) { return (m >> k & 1u) != 0u; });
+    }
+    template <typename Has>
+    __device__ __forceinline__ static void store_if(T* p, const uint4& v, Has mine) {
 #pragma unroll
         for (int k = 0; k < V; ++k)
-            if (has(c, k)) q[k] = elem_of<T>(v, k);
+            if (mine(k)) reinterpret_cast<B*>(p)[k] = elem_of<T>(v, k);
     }
     // the weights of vector c: `skip` elements of the weight's vector before, then the next
     __device__ __forceinline__ uint4 weight(const T* w, int c) const {
@@ -130,6 +152,10 @@ struct Row {
 #pragma unroll
             for (int q = 0; q < 4; ++q) x[q] = __funnelshift_r(x[q], x[q + 1], (by & 2) * 8);
         return make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    __device__ __forceinline__ uint4 weight_own(const T* w, int c, uint32_t m) const {
+        if (inner(c)) return weight(w, c);
+        return gather_if(w + c * V - skip, [&](int k) { return (m >> k & 1u) != 0u; });
     }
 };
 
@@ -183,19 +209,19 @@ __device__ __forceinline__ void to_codes(const float (&f)[N], float inv_scale, u
 }
 
 template <typename T, bool AL>
-__device__ __forceinline__ void store_codes(uint8_t* codes, const Row<T, AL>& row, int c,
+__device__ __forceinline__ void store_codes(uint8_t* codes, const Row<T, AL>& row, int c, uint32_t m,
                                             const float (&f)[Row<T, AL>::V], float inv_scale) {
     constexpr int V = Row<T, AL>::V;
     uint32_t q[V / 4];
     to_codes(f, inv_scale, q);
     uint8_t* p = codes + row.at + c * V;
-    if (row.inner(c)) {
+    if (AL || m == row.kAll) {
         if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[V / 4 - 1]);
         else *reinterpret_cast<uint32_t*>(p) = q[0];
     } else {
 #pragma unroll
         for (int k = 0; k < V; ++k)
-            if (row.has(c, k)) p[k] = (uint8_t)(q[k / 4] >> (8 * (k & 3)));
+            if (m >> k & 1u) p[k] = (uint8_t)(q[k / 4] >> (8 * (k & 3)));
     }
 }
 
@@ -220,19 +246,21 @@ rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, floa
         const Row<T, AL> row(at, d);
         const bool live = at < rows;
         const int c = row.place(lane);
+        const uint32_t own = row.own(c);
         const bool mine = live && lane < row.vecs;
-        uint4 sv = mine ? row.load(x, c, total) : zero;
+        uint4 sv = mine ? row.covering(x, c, total) : zero;
         float f[V], g[V];
         if constexpr (RES) {
-            const uint4 rv = mine ? row.load(residual, c, total) : zero;
+            const uint4 rv = mine ? row.covering(residual, c, total) : zero;
             unpack(sv, f, no);
             unpack(rv, g, no);
 #pragma unroll
             for (int k = 0; k < V; ++k) f[k] += g[k];
             sv = pack(f, no);
         }
+        sv = row.mask_own(sv, own);
         unpack(sv, f, no);
-        unpack(lane < row.vecs ? row.weight(weight, c) : zero, g, no);
+        unpack(lane < row.vecs ? row.weight_own(weight, c, own) : zero, g, no);
         float sum = 0.0f, top = 0.0f;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -247,11 +275,11 @@ rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ weight, floa
         const float inv_scale = 1.0f / scale;
         if (CODES && lane == 0) scales[at] = scale;
         if (lane >= row.vecs) continue;
-        if (s_out) row.store(s_out, c, sv);
+        if (s_out) row.store_own(s_out, c, own, sv);
 #pragma unroll
         for (int k = 0; k < V; ++k) f[k] = f[k] * r * g[k];
-        if (y) row.store(y, c, pack(f, no));
-        if constexpr (CODES) store_codes(codes, row, c, f, inv_scale);
+        if (y) row.store_own(y, c, own, pack(f, no));
+        if constexpr (CODES) store_codes(codes, row, c, own, f, inv_scale);
     }
 }
 
@@ -265,7 +293,8 @@ constexpr int kWarpRows = 8;        // most rows of a block of such warps
 
 template <typename T, int VPT, bool AL, bool RES, bool CODES, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kBlockThreads,
-                                  WARP ? (VPT <= 2 ? 8 : 4) : VPT <= 2 ? 4 : VPT <= 4 ? 2 : 1)
+                                  WARP ? (VPT <= 2 ? (AL ? 8 : 6) : 4)
+                                       : VPT <= 2 ? (AL || sizeof(T) == 4 ? 4 : 3) : VPT <= 4 ? 2 : 1)
 rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight, float eps, T* s_out,
                      T* y, uint8_t* codes, float* __restrict__ scales, int64_t rows, int d) {
     constexpr int V = Elem<T>::kPerVec;
@@ -279,17 +308,19 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
     const Row<T, AL> row(at, d);
     const T* const no = nullptr;
     uint4 sv[VPT];
+    uint32_t own[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int i = tid + j * nt, c = row.place(i);
-        sv[j] = i < row.vecs ? row.load(x, c, total) : make_uint4(0u, 0u, 0u, 0u);
+        own[j] = row.own(c);
+        sv[j] = i < row.vecs ? row.covering(x, c, total) : make_uint4(0u, 0u, 0u, 0u);
     }
     if constexpr (RES) {
         uint4 rv[VPT];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int i = tid + j * nt, c = row.place(i);
-            rv[j] = i < row.vecs ? row.load(residual, c, total) : make_uint4(0u, 0u, 0u, 0u);
+            rv[j] = i < row.vecs ? row.covering(residual, c, total) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -304,7 +335,7 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int i = tid + j * nt, c = row.place(i);
-                if (i < row.vecs) row.store(s_out, c, sv[j]);
+                if (i < row.vecs) row.store_own(s_out, c, own[j], sv[j]);
             }
         }
     }
@@ -313,12 +344,13 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
     for (int j = 0; j < VPT; ++j) {
         const int i = tid + j * nt, c = row.place(i);
         float f[V], g[V];
+        sv[j] = row.mask_own(sv[j], own[j]);
         unpack(sv[j], f, no);
 #pragma unroll
         for (int k = 0; k < V; ++k) sum = fmaf(f[k], f[k], sum);
         if constexpr (CODES) {
             if (i >= row.vecs) continue;
-            unpack(row.weight(weight, c), g, no);
+            unpack(row.weight_own(weight, c, own[j]), g, no);
 #pragma unroll
             for (int k = 0; k < V; ++k) top = fmaxf(top, fabsf(f[k] * g[k]));
         }
@@ -335,13 +367,13 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
         if (i >= row.vecs) continue;
         float f[V], g[V];
         unpack(sv[j], f, no);
-        unpack(row.weight(weight, c), g, no);
+        unpack(row.weight_own(weight, c, own[j]), g, no);
 #pragma unroll
         for (int k = 0; k < V; ++k) f[k] = f[k] * r * g[k];
-        if (!RES && s_out) row.store(s_out, c, sv[j]);
-        if (y) row.store(y, c, pack(f, no));
+        if (!RES && s_out) row.store_own(s_out, c, own[j], sv[j]);
+        if (y) row.store_own(y, c, own[j], pack(f, no));
         if constexpr (CODES) {
-            store_codes(codes, row, c, f, inv_scale);
+            store_codes(codes, row, c, own[j], f, inv_scale);
         }
     }
 }
@@ -352,8 +384,8 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
 // of its block's rows, so d_w is summed in registers, once per block over its teams,
 // and then by rmsnorm_dw_kernel over the blocks, always in the same order.  Rows that
 // start within vectors (AL false) go to teams and blocks by where they start.
-template <typename T, int TEAM, int VPT, bool AL>
-__global__ void __launch_bounds__(kTeamThreads, VPT == 1 ? 3 : 2)
+template <typename T, int TEAM, bool AL>
+__global__ void __launch_bounds__(kTeamThreads, 3)
 rmsnorm_backward_kernel(const T* d_y, const T* s, const T* __restrict__ weight, float eps,
                         const T* d_s, T* d_x, float* __restrict__ part, int64_t rows, int d) {
     constexpr int V = Elem<T>::kPerVec, per_block = kTeamThreads / TEAM;
@@ -367,84 +399,57 @@ rmsnorm_backward_kernel(const T* d_y, const T* s, const T* __restrict__ weight, 
     const int64_t turns = first < rows ? (rows - first + stride - 1) / stride : 0;
     int64_t row = first + team;
     Row<T, AL> here(row, d);
+    const bool mine = lane < here.vecs;
+    const int c = here.place(lane);
     const T* const no = nullptr;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    uint4 wv[VPT], sv[VPT], yv[VPT], av[VPT];
-    float acc[VPT][V];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int i = lane + j * TEAM;
-        wv[j] = i < here.vecs ? here.weight(weight, here.place(i)) : zero;
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[j][k] = 0.0f;
-    }
     const bool add = d_s && d_x;
-    const auto fetch = [&](const Row<T, AL>& r, bool live) {
+    const uint4 wv = mine ? here.weight(weight, c) : zero;
+    float acc[V];
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int i = lane + j * TEAM, c = r.place(i);
-            const bool go = live && i < r.vecs;
-            sv[j] = go ? r.covering(s, c, total) : zero;
-            yv[j] = go ? r.covering(d_y, c, total) : zero;
-            av[j] = go && add ? r.covering(d_s, c, total) : zero;
-        }
+    for (int k = 0; k < V; ++k) acc[k] = 0.0f;
+    uint4 sv, yv, av;
+    const auto fetch = [&](const Row<T, AL>& r, bool live) {
+        sv = live && mine ? r.covering(s, c, total) : zero;
+        yv = live && mine ? r.covering(d_y, c, total) : zero;
+        av = live && mine && add ? r.covering(d_s, c, total) : zero;
     };
     fetch(here, row < rows);
     const float inv_d = 1.0f / (float)d;
     for (int64_t it = 0; it < turns; ++it, row += stride) {
-        uint4 ms[VPT], my[VPT], ma[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = here.place(lane + j * TEAM);
-            ms[j] = here.mask(sv[j], c);
-            my[j] = here.mask(yv[j], c);
-            ma[j] = av[j];
-        }
+        const uint4 ms = here.mask(sv, c), my = here.mask(yv, c), ma = av;
         Row<T, AL> next = here;
         next.at += stride * d;
         if (it + 1 < turns) fetch(next, row + stride < rows);  // in flight over this row
+        float fs[V], fy[V], fw[V], fa[V];
+        unpack(ms, fs, no);
+        unpack(my, fy, no);
+        unpack(wv, fw, no);
         float sq = 0.0f, gs = 0.0f;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            float fs[V], fy[V], fw[V];
-            unpack(ms[j], fs, no);
-            unpack(my[j], fy, no);
-            unpack(wv[j], fw, no);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                sq = fmaf(fs[k], fs[k], sq);
-                gs = fmaf(fy[k] * fw[k], fs[k], gs);
-            }
+        for (int k = 0; k < V; ++k) {
+            sq = fmaf(fs[k], fs[k], sq);
+            gs = fmaf(fy[k] * fw[k], fs[k], gs);
         }
         team_reduce<TEAM, kSum>(sq, gs, nullptr);
         const float r = 1.0f / sqrtf(fmaf(sq, inv_d, eps));
         const float back = gs * inv_d * r * r;  // times s: what the bracket takes off
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int i = lane + j * TEAM;
-            if (row >= rows || i >= here.vecs) continue;
-            float fs[V], fy[V], fw[V], fa[V];
-            unpack(ms[j], fs, no);
-            unpack(my[j], fy, no);
-            unpack(wv[j], fw, no);
-            unpack(ma[j], fa, no);
+        if (row < rows && mine) {
+            unpack(ma, fa, no);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                acc[j][k] = fmaf(fy[k], fs[k] * r, acc[j][k]);
+                acc[k] = fmaf(fy[k], fs[k] * r, acc[k]);
                 fa[k] = fmaf(r, fmaf(-back, fs[k], fy[k] * fw[k]), fa[k]);
             }
-            if (d_x) here.store(d_x, here.place(i), pack(fa, no));
+            if (d_x) here.store(d_x, c, pack(fa, no));
         }
         here = next;
     }
     if (!part) return;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int i = lane + j * TEAM, c = here.place(i);
-        if (i >= here.vecs) continue;
+    if (mine) {
 #pragma unroll
         for (int k = 0; k < V; ++k)
-            if (here.has(c, k)) acc_sm[team * d + c * V + k - here.skip] = acc[j][k];
+            if (here.has(c, k)) acc_sm[team * d + c * V + k - here.skip] = acc[k];
     }
     __syncthreads();
     for (int col = threadIdx.x; col < d; col += kTeamThreads) {
@@ -470,24 +475,33 @@ constexpr int kDepth = 3;  // rows in a ring
 constexpr size_t kRingSmem = 220 * 1024;  // of an SM, for the rings of its blocks
 
 // s and d_y come by way of the ring, where each thread copies and reads its own; d_s straight
-// to registers, asked for before the row's sums.  A thread's columns are the same in every
-// row: rows that start within vectors (AL false) go to blocks by where they start (the grid
-// is then a multiple of V, or has a row a block).
-template <int VPT> constexpr int kBackThreads = VPT == 2 ? 320 : VPT == 4 ? 256 : 512;
+// to registers, asked for before the row's sums.  WARP: rows of up to kWarpVecs / 2 vectors, a
+// warp each, with a ring of its own and no barrier.  A thread's columns are the same in every row:
+// rows that start within vectors (AL false) go to blocks and warps by where they start (the rows
+// of a turn are then a multiple of V, or all rows).
+template <int VPT> constexpr int kBackThreads = VPT == 2 ? 320 : 512;
 
-template <typename T, int VPT, bool AL>
-__global__ void __launch_bounds__(kBackThreads<VPT>, VPT <= 4 ? 2 : 1)
+constexpr int kBackWarps = 4;  // of a block of rows of a warp each
+constexpr int kBackBlocks = 5;  // such blocks an SM
+
+template <typename T, int VPT, bool AL, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kBackWarps : kBackThreads<VPT>,
+                                  WARP ? kBackBlocks : VPT == 2 ? 2 : 1)
 rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ weight, float eps,
                              const T* d_s, T* d_x, float* __restrict__ part, int64_t rows, int d) {
     constexpr int V = Elem<T>::kPerVec;
     constexpr bool kKeep = VPT <= 4;  // a row's values stay in registers between sums and stores
-    extern __shared__ __align__(16) uint8_t ring[];
+    extern __shared__ __align__(16) uint8_t rings[];
     __shared__ float2 red[2][32];
     pdl_wait();
     pdl_trigger();
-    const int nt = blockDim.x;
-    const int64_t stride = gridDim.x, total = rows * d;
-    const Row<T, AL> first(blockIdx.x, d);
+    const int nt = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int warp = WARP ? threadIdx.x >> 5 : 0, per = WARP ? kBackWarps : 1;
+    const int64_t row0 = (int64_t)blockIdx.x * per + warp, stride = (int64_t)gridDim.x * per;
+    const int64_t total = rows * d;
+    const int room = kDepth * 2 * 16 * (AL ? d / V : (d + V - 1) / V + 1);  // bytes of a ring
+    uint8_t* ring = rings + warp * room;
+    const Row<T, AL> first(row0, d);
     const int vecs = first.vecs, row_bytes = vecs * 16;
     const bool add = d_s && d_x;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
@@ -498,7 +512,7 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
             const int64_t at = row * d - first.skip;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int i = threadIdx.x + j * nt, c = first.place(i);
+                const int i = tid + j * nt, c = first.place(i);
                 if (i >= vecs) continue;
                 const int to = slot * 2 * row_bytes + c * 16;
                 const int64_t e = at + c * V;
@@ -514,25 +528,25 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
         copy_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) fetch(blockIdx.x + i * stride, i);
+    for (int i = 0; i < kDepth - 1; ++i) fetch(row0 + i * stride, i);
     float acc[VPT][V];
     uint4 wv[kKeep ? VPT : 1];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[j][k] = 0.0f;
-        const int i = threadIdx.x + j * nt, c = first.place(i);
+        const int i = tid + j * nt, c = first.place(i);
         if constexpr (kKeep) wv[j] = i < vecs ? first.weight(weight, c) : zero;
     }
     const float inv_d = 1.0f / (float)d;
     int slot = 0, turn = 0;
-    for (int64_t row = blockIdx.x; row < rows; row += stride, turn ^= 1) {
+    for (int64_t row = row0; row < rows; row += stride, turn ^= 1) {
         Row<T, AL> here = first;
         here.at = row * d - first.skip;
         uint4 av[VPT], sv[kKeep ? VPT : 1], yv[kKeep ? VPT : 1];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int i = threadIdx.x + j * nt, c = first.place(i);
+            const int i = tid + j * nt, c = first.place(i);
             av[j] = add && i < vecs ? here.covering(d_s, c, total) : zero;
         }
         copy_wait<kDepth - 2>();
@@ -543,7 +557,7 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
         float sq = 0.0f, gs = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int i = threadIdx.x + j * nt, c = first.place(i);
+            const int i = tid + j * nt, c = first.place(i);
             if constexpr (kKeep) sv[j] = yv[j] = zero;
             if (i >= vecs) continue;
             const uint4 a = read(c, false), b = read(c, true);
@@ -561,14 +575,14 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
                 gs = fmaf(fy[k] * fw[k], fs[k], gs);
             }
         }
-        team_reduce<0, kSum>(sq, gs, red[turn]);
+        team_reduce<WARP ? 32 : 0, kSum>(sq, gs, red[turn]);
         // into the place of the row before this one, used up before the barrier
         fetch(row + (kDepth - 1) * stride, slot == 0 ? kDepth - 1 : slot - 1);
         const float r = 1.0f / sqrtf(fmaf(sq, inv_d, eps));
         const float back = gs * inv_d * r * r;  // times s: what the bracket takes off
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int i = threadIdx.x + j * nt, c = first.place(i);
+            const int i = tid + j * nt, c = first.place(i);
             if (i >= vecs) continue;
             float fs[V], fy[V], fw[V], fa[V];
             unpack(kKeep ? sv[kKeep ? j : 0] : read(c, false), fs, no);
@@ -587,13 +601,27 @@ rmsnorm_backward_ring_kernel(const T* d_y, const T* s, const T* __restrict__ wei
     }
     copy_wait<0>();
     if (!part) return;
+    float* sums = part + (int64_t)blockIdx.x * d;
+    if constexpr (WARP) {  // the warps' sums in the place of their rings (fewer bytes)
+        __syncwarp();
+        sums = reinterpret_cast<float*>(ring);
+    }
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int i = threadIdx.x + j * nt, c = first.place(i);
+        const int i = tid + j * nt, c = first.place(i);
         if (i >= vecs) continue;
 #pragma unroll
         for (int k = 0; k < V; ++k)
-            if (first.has(c, k)) part[(int64_t)blockIdx.x * d + c * V + k - first.skip] = acc[j][k];
+            if (first.has(c, k)) sums[c * V + k - first.skip] = acc[j][k];
+    }
+    if constexpr (WARP) {
+        __syncthreads();
+        for (int col = threadIdx.x; col < d; col += 32 * kBackWarps) {
+            float t = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kBackWarps; ++q) t += reinterpret_cast<const float*>(rings + q * room)[col];
+            part[(int64_t)blockIdx.x * d + col] = t;
+        }
     }
 }
 
@@ -767,10 +795,11 @@ cudaError_t forward(const NormArgs& a, cudaStream_t st) {
 // 16-byte vectors tile the rows
 bool whole_vectors(int dtype, int d) { return d % (dtype == MOE_BF16 ? 8 : 4) == 0; }
 
-// How the backward pass runs: teams within a warp (lanes > 0) of one or two vectors a lane;
-// a ring a block; or, for rows too wide for a ring, neither (smem 0).
+// How the backward pass runs: teams within a warp (lanes > 0) of a vector a lane; a ring a
+// warp or a block; or, for rows too wide for a ring, neither (smem 0).
 struct BackPlan {
     int lanes, per_thread, threads, blocks;
+    bool warps;
     size_t smem;
 };
 
@@ -783,12 +812,18 @@ BackPlan back_plan(int dtype, int64_t rows, int d) {
     const int v = dtype == MOE_BF16 ? 8 : 4;
     const int nv = vec ? d / v : (int)ceil_div(d, v) + 1;
     int64_t want = rows, wave;
-    if (nv <= 2 * kTeamVecs) {
+    if (nv <= kTeamVecs) {
         p.lanes = nv <= 4 ? 4 : nv <= 8 ? 8 : nv <= 16 ? 16 : 32;
-        p.per_thread = nv <= kTeamVecs ? 1 : 2;
         p.threads = kTeamThreads;
         want = ceil_div(rows, kTeamThreads / p.lanes);
-        wave = 152 * (p.per_thread == 1 ? 3 : 2);
+        wave = 152 * 3;
+    } else if (nv <= kWarpVecs / 2) {  // four vectors a lane spill: 777 bf16 values 231 us, in a block 150
+        p.warps = true;
+        p.per_thread = 2;
+        p.threads = 32 * kBackWarps;
+        p.smem = (size_t)kBackWarps * kDepth * 2 * nv * 16;
+        want = ceil_div(rows, kBackWarps);
+        wave = 152 * kBackBlocks;
     } else if ((size_t)kDepth * 2 * nv * 16 <= kRingSmem) {
         p.per_thread = nv <= 2 * kBackThreads<2> ? 2 : nv <= 4 * kBackThreads<4> ? 4 : 5;
         p.threads = threads_for(ceil_div(nv, p.per_thread));
@@ -806,20 +841,19 @@ BackPlan back_plan(int dtype, int64_t rows, int d) {
     return p;
 }
 
-template <typename T, int TEAM, int VPT, bool AL>
+template <typename T, int TEAM, bool AL>
 cudaError_t go_back_teams(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
-    return launch_pdl(rmsnorm_backward_kernel<T, TEAM, VPT, AL>, dim3(p.blocks), dim3(kTeamThreads),
+    return launch_pdl(rmsnorm_backward_kernel<T, TEAM, AL>, dim3(p.blocks), dim3(kTeamThreads),
                       sizeof(float) * (kTeamThreads / TEAM) * a.d, st, (const T*)a.d_y, (const T*)a.x,
                       (const T*)a.weight, a.eps, (const T*)a.d_s, (T*)a.d_x, a.part, a.rows, a.d);
 }
 
 template <typename T, bool AL>
 cudaError_t back_teams(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
-    if (p.lanes == 4) return go_back_teams<T, 4, 1, AL>(a, p, st);
-    if (p.lanes == 8) return go_back_teams<T, 8, 1, AL>(a, p, st);
-    if (p.lanes == 16) return go_back_teams<T, 16, 1, AL>(a, p, st);
-    if (p.per_thread == 1) return go_back_teams<T, 32, 1, AL>(a, p, st);
-    return go_back_teams<T, 32, 2, AL>(a, p, st);
+    if (p.lanes == 4) return go_back_teams<T, 4, AL>(a, p, st);
+    if (p.lanes == 8) return go_back_teams<T, 8, AL>(a, p, st);
+    if (p.lanes == 16) return go_back_teams<T, 16, AL>(a, p, st);
+    return go_back_teams<T, 32, AL>(a, p, st);
 }
 
 template <typename T>
@@ -842,11 +876,12 @@ cudaError_t backward(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
             return vec ? go(rmsnorm_backward_wide_kernel<T, V, 4>)
                        : go(rmsnorm_backward_wide_kernel<T, 1, 16>);
     }
-#define MOE_RING(AL)                                                                  \
-    do {                                                                              \
-        if (p.per_thread == 2) return go(rmsnorm_backward_ring_kernel<T, 2, AL>);     \
-        if (p.per_thread == 4) return go(rmsnorm_backward_ring_kernel<T, 4, AL>);     \
-        return go(rmsnorm_backward_ring_kernel<T, 5, AL>);                            \
+#define MOE_RING(AL)                                                                         \
+    do {                                                                                     \
+        if (p.warps) return go(rmsnorm_backward_ring_kernel<T, 2, AL, true>);                \
+        if (p.per_thread == 2) return go(rmsnorm_backward_ring_kernel<T, 2, AL, false>);     \
+        if (p.per_thread == 4) return go(rmsnorm_backward_ring_kernel<T, 4, AL, false>);     \
+        return go(rmsnorm_backward_ring_kernel<T, 5, AL, false>);                            \
     } while (0)
     if (vec) MOE_RING(true);
     MOE_RING(false);
