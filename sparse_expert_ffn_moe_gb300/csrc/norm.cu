@@ -7,11 +7,18 @@
 //
 // A row is read once and stays in registers between the sums and the stores:
 // sum(s^2) and max|s w| come from one reduction (max|y| = r max|s w|), so a row
-// costs its bytes and one block barrier.  A row goes to a team of threads: 4 to
-// 32 lanes of a warp (rows of at most 32 16-byte vectors), else a whole block.
+// costs its bytes and one block barrier at most.  A row goes to 4 to 32 lanes of a
+// warp (rows of at most 32 16-byte vectors), to a warp (128), else to a block.
 //
 // Rows that no 16-byte vector tiles (width odd, say) are read through the
-// aligned vectors that cover them; the two at the ends go by element.
+// aligned vectors that cover them; those at the ends are stored by element, by one
+// warp of the row.
+//
+// Measured (GB300, a CUDA graph's time a call; floor: the bytes at the measured copy's
+// 6788 GB/s): 16384 x 7168 bf16 with residual, both outputs 152 us (floor 156), one array in
+// and out 69 (69); 131072 x 512 78 (79); 20011 x 2049 fp32 57 (48), 100000 x 777 bf16 with
+// codes 143 (103); 8 x 7168 2.6 (0.07: a launch).  Backward: 16384 x 7168 bf16 140 (138),
+// 20011 x 2049 fp32 105 (97), 100000 x 333 bf16 72 (29).
 #include <cuda_fp8.h>
 #include <float.h>
 
@@ -355,7 +362,10 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
             for (int k = 0; k < V; ++k) top = fmaxf(top, fabsf(f[k] * g[k]));
         }
     }
-    team_reduce<WARP ? 32 : 0, CODES ? kMax : kAlone>(sum, top, red);
+    // A block's reduction carries the maximum even where nobody asks for it: the few steps longer
+    // between a row's loads and its stores keep the memory busier (16384 x 7168 bf16, one array
+    // in and one out: 69 us against 74; no other form differs).
+    team_reduce<WARP ? 32 : 0, CODES || !WARP ? kMax : kAlone>(sum, top, red);
     const float r = rsqrtf(fmaf(sum, 1.0f / (float)d, eps));
     const float most = top * r;
     const float scale = row_scale(most);
@@ -775,11 +785,14 @@ cudaError_t forward(const NormArgs& a, cudaStream_t st) {
     // vectors that cover a row, wherever it starts
     const int nv = (int)ceil_div(a.d, Elem<T>::kPerVec) + (AL ? 0 : 1);
     if (nv <= kTeamVecs) return teams_for<T, AL>(a, nv, st);
+    // A warp a row (131072 x 512 bf16: 78 us, in blocks of 32 threads 133; 100000 x 512 fp32 with
+    // codes 67 and 102), but for a few rows, where two warps share the latency (8 x 512 fp32:
+    // 2.1 us against 2.5).
     if (nv <= kWarpVecs / 2) return go_blocks<T, 2, AL, true>(a, nv, st);
-    if (nv <= kWarpVecs) return go_blocks<T, 4, AL, true>(a, nv, st);
+    if (nv <= kWarpVecs && a.rows > 8 * 152) return go_blocks<T, 4, AL, true>(a, nv, st);
     // Two vectors a thread, so that registers allow four blocks of 512; four a thread where a
-    // row is one array in and one out (16384 x 7168 bf16: 69 us against 77; with a residual 135
-    // against 134, rows of 2049 fp32 values 75 against 72).
+    // row is one array in and one out (16384 x 7168 bf16: 69 us against 75; with a residual 135
+    // against 134).
     if (AL && !a.residual && !a.codes && nv > kBlockThreads && nv <= 2 * kBlockThreads)
         return go_blocks<T, 4, AL>(a, nv, st);
     if (nv <= 2 * kBlockThreads) return go_blocks<T, 2, AL>(a, nv, st);
