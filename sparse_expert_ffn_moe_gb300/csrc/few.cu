@@ -135,7 +135,7 @@ struct Ctl {
     float weight[kMaxSlots];
     float xs[kMaxT];              // scales of x
     float top[4][kMaxT];
-    float hscale[2][4 * kMaxT];   // of a stage of h: [K tile][token], two in turn
+    alignas(16) float hscale[2][kTiles * 16];  // of a stage of h: [K tile][token], two in turn
     alignas(16) float strand[4][128];  // read and written as float4
 };
 
@@ -718,26 +718,70 @@ __device__ __forceinline__ void load_cols(uint32_t at, uint32_t (&v)[N]) {
     }
 }
 
-// The planes of down sums joined, W columns a plane: of one accumulator (bf16) or of each K
-// tile's (8-bit: two finer planes, the next columns are not read).
-template <int FMT, int W, int NT>
-__device__ __forceinline__ void down_cols(uint32_t at, float (&v)[FMT ? kTiles : 1][NT]) {
-    constexpr int N = FMT ? 4 * W : 2 * W, L = FMT && W == 16 ? 48 : N;
-    uint32_t c[FMT ? kTiles : 1][L];
+// ---- two fp32 values in a 64-bit register: one instruction works on both -----
+typedef uint64_t f2;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ f2 pack2(uint32_t lo, uint32_t hi) {
+    return pack2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void unpack2(const f2 (&v)[N / 2], float (&f)[N]) {
 #pragma unroll
-    for (int i = 0; i < (FMT ? kTiles : 1); ++i) load_cols(at + i * N, c[i]);
+    for (int t = 0; t < N / 2; ++t)
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(f[2 * t]), "=f"(f[2 * t + 1]) : "l"(v[t]));
+}
+
+// A down unit's bf16 sums: hi and lo plane, W columns each.
+template <int W, int NT>
+__device__ __forceinline__ void down_sums(uint32_t at, float (&s)[NT]) {
+    uint32_t c[2 * W];
+    load_cols(at, c);
     ptx::tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < (FMT ? kTiles : 1); ++i)
+    for (int t = 0; t < W; ++t) s[t] = __uint_as_float(c[t]) + __uint_as_float(c[W + t]);
+}
+
+// The K tiles of a stage added to a down unit's 8-bit sums: three planes of W columns joined,
+// times h's scales (16 a tile) and, FMT 2, the weights'.  For the first N tokens alone: most
+// groups have one or two (sums of all 16 in single instructions cost E4M3, T = 16 530 us, these
+// 494; block scales, T = 13 470 and 447).  `release`: the
+// accumulators are read.
+template <int FMT, int W, int N, int NT, typename Release>
+__device__ __forceinline__ void add_down(uint32_t at, const float* hs, const float (&bs)[kTiles],
+                                         int tiles, f2 (&s)[NT / 2], Release release) {
+    uint32_t c[kTiles][W == 16 ? 48 : 32];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            v[i][t] = 0.0f;
-            if (t >= W) continue;
-            const float hi = __uint_as_float(c[i][t % W]), lo = __uint_as_float(c[i][W + t % W]);
-            if constexpr (FMT)
-                v[i][t] = fmaf(fmaf(__uint_as_float(c[i][2 * W + t % W]), 0.0625f, lo), 0.0625f, hi);
-            else v[i][t] = hi + lo;
+    for (int i = 0; i < kTiles; ++i) load_cols(at + i * 4 * W, c[i]);
+    ptx::tmem_ld_wait();
+    release();
+    const f2 finer = pack2(0.0625f, 0.0625f);
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+        if (i >= tiles) continue;  // not written
+#pragma unroll
+        for (int t = 0; t < N / 2; ++t) {
+            const float2 q = *reinterpret_cast<const float2*>(hs + 16 * i + 2 * t);
+            f2 h = pack2(q.x, q.y);
+            if constexpr (FMT == 2) h = mul2(h, pack2(bs[i], bs[i]));
+            const f2 mid = fma2(pack2(c[i][2 * W + 2 * t], c[i][2 * W + 2 * t + 1]), finer,
+                                pack2(c[i][W + 2 * t], c[i][W + 2 * t + 1]));
+            s[t] = fma2(fma2(mid, finer, pack2(c[i][2 * t], c[i][2 * t + 1])), h, s[t]);
         }
+    }
 }
 
 template <int FMT, int NT>
@@ -984,9 +1028,9 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                 const int row0 = ctl->row0[un.group];
                 const int I = sh ? a.Is : a.I;
                 if (!un.down) {
-                    float s[NT];
+                    f2 sums2[NT / 2];
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) s[t] = 0.0f;
+                    for (int t = 0; t < NT / 2; ++t) sums2[t] = 0u;
                     const bool up = r >= kGateRows;
                     const int step = FMT == 2 ? kTiles : un.n;
                     // the thread's row scale, or its blocks' scales along K (asked for a stage ahead)
@@ -1017,15 +1061,19 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                         for (int i = 0; i < (FMT == 2 ? kTiles : 1); ++i) {
                             if (FMT == 2 && k + i >= un.n) continue;  // not written
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                float x = __uint_as_float(v[i][t]);
-                                if constexpr (FMT) x = fmaf(__uint_as_float(v[i][NT + t]), 0.0625f, x);
-                                s[t] = FMT == 2 ? fmaf(x, bs[i], s[t]) : x;
+                            for (int t = 0; t < NT / 2; ++t) {
+                                f2 x = pack2(v[i][2 * t], v[i][2 * t + 1]);
+                                if constexpr (FMT)
+                                    x = fma2(pack2(v[i][NT + 2 * t], v[i][NT + 2 * t + 1]),
+                                             pack2(0.0625f, 0.0625f), x);
+                                sums2[t] = FMT == 2 ? fma2(x, pack2(bs[i], bs[i]), sums2[t]) : x;
                             }
                         }
                         if constexpr (FMT == 2) ask(k + step);
                     }
                     if (!ok) break;
+                    float s[NT];
+                    unpack2(sums2, s);
                     int c = 0;
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
@@ -1040,8 +1088,11 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                     const int w = NT == 8 || tokens <= 8 ? 8 : 16;
                     const int col = un.tile * kDownRows + r;
                     float s[NT];
+                    f2 sums2[NT / 2];
 #pragma unroll
                     for (int t = 0; t < NT; ++t) s[t] = 0.0f;
+#pragma unroll
+                    for (int t = 0; t < NT / 2; ++t) sums2[t] = 0u;
                     const int step = FMT ? kTiles : un.n;
                     float rs = 1.0f, bs[kTiles], hv = 0.0f;
                     const float* sp = FMT ? (sh ? a.ss_down : a.s_down) : nullptr;
@@ -1074,29 +1125,27 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                             }
                         }
                         const uint32_t at = tmem + lanes + buf * 128;
-                        float v[FMT ? kTiles : 1][NT];
-                        if (w == 8) down_cols<FMT, 8, NT>(at, v);
-                        else if constexpr (NT == 16) down_cols<FMT, 16, NT>(at, v);
-                        ptx::tc_fence_before();
-                        release(&ctl->tempty[buf]);
-                        if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
-#pragma unroll
-                        for (int i = 0; i < (FMT ? kTiles : 1); ++i) {
-                            if (FMT && k + i >= un.n) continue;  // not written
-                            const float b = FMT == 2 ? bs[i] : 1.0f;
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                if constexpr (FMT) {
-                                    if (t < tokens)
-                                        s[t] = fmaf(v[i][t], ctl->hscale[turn][16 * i + t] * b, s[t]);
-                                } else {
-                                    s[t] = v[i][t];
-                                }
-                            }
+                        const auto read = [&]() {
+                            ptx::tc_fence_before();
+                            release(&ctl->tempty[buf]);
+                            if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
+                        };
+                        if constexpr (FMT == 0) {
+                            if (w == 8) down_sums<8>(at, s);
+                            else if constexpr (NT == 16) down_sums<16>(at, s);
+                            read();
+                        } else {
+                            const float* hsc = ctl->hscale[turn];
+                            const int tiles = un.n - k;
+                            if (tokens <= 2) add_down<FMT, 8, 2, NT>(at, hsc, bs, tiles, sums2, read);
+                            else if (w == 8) add_down<FMT, 8, 8, NT>(at, hsc, bs, tiles, sums2, read);
+                            else if constexpr (NT == 16)
+                                add_down<FMT, 16, 16, NT>(at, hsc, bs, tiles, sums2, read);
                         }
                         if constexpr (FMT) ask(k + step);
                     }
                     if (!ok) break;
+                    if constexpr (FMT) unpack2(sums2, s);
                     if (col < a.d) {
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
