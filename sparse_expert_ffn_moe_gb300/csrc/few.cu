@@ -76,6 +76,7 @@ constexpr int kTiles = 2;      // K tiles of a stage
 constexpr int kWTile = 16384;  // bytes of a weight tile: 128 rows x 128 bytes
 constexpr int kABytes = kTiles * kWTile;
 constexpr int kMaxStages = 5;
+constexpr int kChunk = 16;     // K tiles whose scales of h are fetched at once
 constexpr int kHint = 4096;    // bytes of an L2 prefetch
 constexpr int64_t kHintMost = 8 << 20;  // of each of two matrices
 
@@ -135,7 +136,7 @@ struct Ctl {
     float weight[kMaxSlots];
     float xs[kMaxT];              // scales of x
     float top[4][kMaxT];
-    alignas(16) float hscale[2][kTiles * 16];  // of a stage of h: [K tile][token], two in turn
+    alignas(16) float hscale[2][kChunk * 16];  // of K tiles of h: [tile][token], two chunks in turn
     alignas(16) float strand[4][128];  // read and written as float4
 };
 
@@ -1003,6 +1004,36 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
             const int good = lane == 0 ? (int)wait_bounded(bar, parity, ctl, a, where) : 0;
             return ptx::named_bar_and(sums ? 1 : 2, 128, __shfl_sync(0xffffffffu, good, 0) != 0);
         };
+        // a warp's own wait, in loops over stages: its role votes at the ends of units and chunks
+        const auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
+            const int good = lane == 0 ? (int)wait_bounded(bar, parity, ctl, a, where) : 0;
+            __syncwarp();
+            return __shfl_sync(0xffffffffu, good, 0) != 0;
+        };
+        const auto joined = [](const auto& v, int t) {  // x's two planes, tokens 2 t and 2 t + 1
+            return fma2(pack2(v[NT + 2 * t], v[NT + 2 * t + 1]), pack2(0.0625f, 0.0625f),
+                        pack2(v[2 * t], v[2 * t + 1]));
+        };
+        // a K tile's block scale: all of a warp's rows have the same, a lane holds every 32nd
+        struct BlockScales {
+            const float* p;
+            int n, lane;
+            float now, next;
+            __device__ __forceinline__ float at(int k) const {
+                return k + lane < n ? __ldg(p + k + lane) : 0.0f;
+            }
+            __device__ __forceinline__ BlockScales(const float* p_, int n_, int lane_)
+                : p(p_), n(n_), lane(lane_), now(at(0)), next(at(32)) {}
+            // of the tiles from k on; every stage in turn
+            __device__ __forceinline__ void stage(int k, float (&b)[kTiles]) {
+                if (k > 0 && (k & 31) == 0) {
+                    now = next;
+                    next = at(k + 32);
+                }
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) b[i] = __shfl_sync(0xffffffffu, now, (k & 31) + i);
+            }
+        };
         const auto release = [&](uint64_t* bar) {
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar);
@@ -1032,44 +1063,52 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
 #pragma unroll
                     for (int t = 0; t < NT / 2; ++t) sums2[t] = 0u;
                     const bool up = r >= kGateRows;
-                    const int step = FMT == 2 ? kTiles : un.n;
-                    // the thread's row scale, or its blocks' scales along K (asked for a stage ahead)
+                    // the thread's row scale, or its blocks' along K
                     const float* sp = FMT ? (up ? (sh ? a.ss_up : a.s_up) : (sh ? a.ss_gate : a.s_gate))
                                           : nullptr;
-                    float rs = 1.0f, bs[kTiles];
+                    float rs = 1.0f;
                     if constexpr (FMT == 1)
                         rs = __ldg(sp + (int64_t)e * I + un.tile * kGateRows + r % kGateRows);
-                    if constexpr (FMT == 2)
-                        sp += ((int64_t)e * (I / 128) + un.tile / 2) * (a.d / 128) + un.k0;
-                    const auto ask = [&](int k) {
+                    if constexpr (FMT == 2) {
+                        BlockScales scales(sp + ((int64_t)e * (I / 128) + un.tile / 2) * (a.d / 128) + un.k0,
+                                           un.n, lane);
+                        for (int k = 0; k < un.n; k += kTiles) {
+                            if (!wait(&ctl->tfull[buf], bphase, 41)) { ok = false; break; }
+                            ptx::tc_fence_after();
+                            const uint32_t at = tmem + lanes + buf * 128;
+                            uint32_t v[kTiles][C::kXCols];
 #pragma unroll
-                        for (int i = 0; i < kTiles; ++i) bs[i] = k + i < un.n ? __ldg(sp + k + i) : 0.0f;
-                    };
-                    if constexpr (FMT == 2) ask(0);
-                    for (int k = 0; k < un.n; k += step) {
-                        if (!pass(&ctl->tfull[buf], bphase, 41)) { ok = false; break; }
+                            for (int i = 0; i < kTiles; ++i) load_cols(at + i * C::kXCols, v[i]);
+                            ptx::tmem_ld_wait();
+                            ptx::tc_fence_before();
+                            release(&ctl->tempty[buf]);
+                            if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
+                            float bs[kTiles];
+                            scales.stage(k, bs);
+#pragma unroll
+                            for (int i = 0; i < kTiles; ++i) {
+                                if (k + i >= un.n) continue;  // not written
+#pragma unroll
+                                for (int t = 0; t < NT / 2; ++t)
+                                    sums2[t] = fma2(joined(v[i], t), pack2(bs[i], bs[i]), sums2[t]);
+                            }
+                        }
+                        ok = ptx::named_bar_and(1, 128, ok);
+                    } else if (un.n > 0) {
+                        ok = pass(&ctl->tfull[buf], bphase, 41);
+                        if (!ok) break;
                         ptx::tc_fence_after();
-                        const uint32_t at = tmem + lanes + buf * 128;
-                        uint32_t v[FMT == 2 ? kTiles : 1][C::kXCols];
-#pragma unroll
-                        for (int i = 0; i < (FMT == 2 ? kTiles : 1); ++i) load_cols(at + i * C::kXCols, v[i]);
+                        uint32_t v[C::kXCols];
+                        load_cols(tmem + lanes + buf * 128, v);
                         ptx::tmem_ld_wait();
                         ptx::tc_fence_before();
                         release(&ctl->tempty[buf]);
                         if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
 #pragma unroll
-                        for (int i = 0; i < (FMT == 2 ? kTiles : 1); ++i) {
-                            if (FMT == 2 && k + i >= un.n) continue;  // not written
-#pragma unroll
-                            for (int t = 0; t < NT / 2; ++t) {
-                                f2 x = pack2(v[i][2 * t], v[i][2 * t + 1]);
-                                if constexpr (FMT)
-                                    x = fma2(pack2(v[i][NT + 2 * t], v[i][NT + 2 * t + 1]),
-                                             pack2(0.0625f, 0.0625f), x);
-                                sums2[t] = FMT == 2 ? fma2(x, pack2(bs[i], bs[i]), sums2[t]) : x;
-                            }
+                        for (int t = 0; t < NT / 2; ++t) {
+                            if constexpr (FMT) sums2[t] = joined(v, t);
+                            else sums2[t] = pack2(v[2 * t], v[2 * t + 1]);
                         }
-                        if constexpr (FMT == 2) ask(k + step);
                     }
                     if (!ok) break;
                     float s[NT];
@@ -1093,56 +1132,65 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                     for (int t = 0; t < NT; ++t) s[t] = 0.0f;
 #pragma unroll
                     for (int t = 0; t < NT / 2; ++t) sums2[t] = 0u;
-                    const int step = FMT ? kTiles : un.n;
-                    float rs = 1.0f, bs[kTiles], hv = 0.0f;
-                    const float* sp = FMT ? (sh ? a.ss_down : a.s_down) : nullptr;
-                    if constexpr (FMT == 1) rs = __ldg(sp + (int64_t)e * a.d + col);  // d a multiple of 128
-                    if constexpr (FMT == 2)
-                        sp += ((int64_t)e * (a.d / 128) + un.tile) * (I / 128) + un.k0;
-                    // scales of the stage from K tile k: h's go through shared memory (thread
-                    // 16 i + c: tile k + i, token c), asked for a stage ahead
-                    const float* hs = FMT ? (sh ? a.hs_s : a.hs) + un.k0 +
-                                                (int64_t)(row0 - (sh || !shared ? 0 : a.T)) * (I / 128)
-                                          : nullptr;
-                    const auto ask = [&](int k) {
-                        const int i = r >> 4, c = r & 15;
-                        hv = i < kTiles && k + i < un.n && c < tokens
-                                 ? __ldcg(hs + (int64_t)c * (I / 128) + k + i) : 0.0f;
-                        if constexpr (FMT == 2)
-#pragma unroll
-                            for (int j = 0; j < kTiles; ++j) bs[j] = k + j < un.n ? __ldg(sp + k + j) : 0.0f;
+                    float rs = 1.0f;
+                    const auto read = [&]() {
+                        ptx::tc_fence_before();
+                        release(&ctl->tempty[buf]);
+                        if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
                     };
-                    int turn = 0;
-                    for (int k = 0; k < un.n; k += step, turn ^= 1) {
-                        if (FMT && k > 0 && r < 16 * kTiles) ctl->hscale[turn][r] = hv;
-                        if (!pass(&ctl->tfull[buf], bphase, 42)) { ok = false; break; }
-                        ptx::tc_fence_after();
-                        if constexpr (FMT) {
-                            if (k == 0) {  // h is done: a product with it is
-                                ask(0);
-                                if (r < 16 * kTiles) ctl->hscale[turn][r] = hv;
-                                asm volatile("bar.sync 1, 128;" ::: "memory");
-                            }
-                        }
-                        const uint32_t at = tmem + lanes + buf * 128;
-                        const auto read = [&]() {
-                            ptx::tc_fence_before();
-                            release(&ctl->tempty[buf]);
-                            if (++buf == kBufs) { buf = 0; bphase ^= 1u; }
-                        };
-                        if constexpr (FMT == 0) {
+                    if constexpr (FMT == 0) {
+                        if (un.n > 0) {
+                            ok = pass(&ctl->tfull[buf], bphase, 42);
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                            const uint32_t at = tmem + lanes + buf * 128;
                             if (w == 8) down_sums<8>(at, s);
                             else if constexpr (NT == 16) down_sums<16>(at, s);
                             read();
-                        } else {
-                            const float* hsc = ctl->hscale[turn];
+                        }
+                    } else {
+                        const float* sp = sh ? a.ss_down : a.s_down;
+                        if constexpr (FMT == 1) rs = __ldg(sp + (int64_t)e * a.d + col);  // d a multiple of 128
+                        BlockScales scales(FMT == 2 ? sp + ((int64_t)e * (a.d / 128) + un.tile) * (I / 128) + un.k0
+                                                    : nullptr,
+                                           FMT == 2 ? un.n : 0, lane);
+                        // h's scales go through shared memory, a chunk of K tiles at a time, asked
+                        // for a chunk ahead (the first once a product shows that h is done)
+                        const float* hs = (sh ? a.hs_s : a.hs) + un.k0 +
+                                          (int64_t)(row0 - (sh || !shared ? 0 : a.T)) * (I / 128);
+                        float hv[kChunk * 16 / 128];
+                        const auto ask = [&](int k) {
+#pragma unroll
+                            for (int q = 0; q < kChunk * 16 / 128; ++q) {
+                                const int i = (r + 128 * q) >> 4, c = r & 15;
+                                hv[q] = k + i < un.n && c < tokens
+                                            ? __ldcg(hs + (int64_t)c * (I / 128) + k + i) : 0.0f;
+                            }
+                        };
+                        for (int k = 0; k < un.n; k += kTiles) {
+                            // a warp whose wait ran out goes on to the vote without its sums
+                            if (ok) ok = wait(&ctl->tfull[buf], bphase, 42);
+                            ptx::tc_fence_after();
+                            float* hsc = ctl->hscale[k / kChunk & 1] + k % kChunk * 16;
+                            if (k % kChunk == 0) {
+                                if (k == 0) ask(0);
+#pragma unroll
+                                for (int q = 0; q < kChunk * 16 / 128; ++q) hsc[r + 128 * q] = hv[q];
+                                ok = ptx::named_bar_and(1, 128, ok);
+                                if (!ok) break;
+                                if (k + kChunk < un.n) ask(k + kChunk);
+                            }
+                            if (!ok) continue;
+                            float bs[kTiles] = {};
+                            if constexpr (FMT == 2) scales.stage(k, bs);
+                            const uint32_t at = tmem + lanes + buf * 128;
                             const int tiles = un.n - k;
                             if (tokens <= 2) add_down<FMT, 8, 2, NT>(at, hsc, bs, tiles, sums2, read);
                             else if (w == 8) add_down<FMT, 8, 8, NT>(at, hsc, bs, tiles, sums2, read);
                             else if constexpr (NT == 16)
                                 add_down<FMT, 16, 16, NT>(at, hsc, bs, tiles, sums2, read);
                         }
-                        if constexpr (FMT) ask(k + step);
+                        ok = ptx::named_bar_and(1, 128, ok);
                     }
                     if (!ok) break;
                     if constexpr (FMT) unpack2(sums2, s);
