@@ -43,9 +43,9 @@
 //
 // Measured (GB300, a CUDA graph's time a call; floor: the picked experts' bytes at the
 // measured copy's 6788 GB/s): 256 experts of 7168 x 2048, K = 8, and a shared one, bf16:
-// T = 1 127 us (floor 117), T = 8 607 (617), T = 16 905 (941); E4M3 T = 8 326 (309);
-// block scales, T = 13 469 (422).  Small layers are a chain of joints: eight experts of
-// 2048 x 768 32 us (floor 11), two of 256 x 512 16 us.  Tried and slower: units of 16 or
+// T = 1 126 us (floor 117), T = 8 607 (617), T = 16 921 (941); E4M3 T = 1 72 (59), T = 8
+// 319 (309), T = 16 492 (471); block scales, T = 13 447 (422).  Small layers are a chain of
+// joints: eight experts of 2048 x 768 31 us (floor 11), two of 256 x 512 15 us.  Tried and slower: units of 16 or
 // 32 rows, which leave the products' other rows empty (T = 1 209 and 146 us against 131);
 // units a quarter as long with more parts (T = 1 160); two accumulators in turn (+ 2 %);
 // claims of several units at a time (177); the sums' warps counting parts themselves.
@@ -379,65 +379,125 @@ __device__ __forceinline__ uint32_t ordered(float key) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// The weights of a token's picks, a lane each: a / (sum + 1e-6) or softmax over the keys, as
+// numerator and sum.  The lanes that have a pick divide and no others: zeros take the
+// division's slow path, whose code has to be fetched (0.6 to 1 us a call).
+__device__ __forceinline__ float pick_weight(const FewArgs& a, float s, int e, int lane, float& sum) {
+    const float b = a.bias ? __ldg(a.bias + e) : 0.0f;
+    const float first = __shfl_sync(0xffffffffu, s + b, 0);
+    float w = 0.0f;
+    if (lane < a.K) w = a.sigmoid ? 1.0f / (1.0f + expf(-s)) : expf(s + b - first);
+    sum = warp_sum(w) + (a.sigmoid ? 1e-6f : 0.0f);
+    return w;
+}
+
+// A warp's K rounds: lane j gets the j-th pick.  A lane has the experts lane, lane + 32, ...; its
+// best one that is not taken (0: none; a key of 0, a NaN of all ones, was stored as 1).  The
+// first eight stay in registers, more are read again after each pick.
+__device__ __forceinline__ int rounds(uint32_t* key, int E, int K, int lane) {
+    uint32_t k8[8], best = 0u;
+    int at = 0;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) k8[m] = lane + 32 * m < E ? key[lane + 32 * m] : 0u;
+    const auto rescan = [&]() {
+        best = 0u;
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+            if (k8[m] > best) {
+                best = k8[m];
+                at = lane + 32 * m;
+            }
+#pragma unroll 4
+        for (int e = lane + 256; e < E; e += 32)
+            if (key[e] > best) {
+                best = key[e];
+                at = e;
+            }
+    };
+    rescan();
+    int mine = 0;
+    for (int j = 0; j < K; ++j) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        const int e = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7fffffff);
+        if (lane == j) mine = e;
+        if ((e & 31) == lane) {
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+                if (e == lane + 32 * m) k8[m] = 0u;
+            if (e >= 256) key[e] = 0u;
+            rescan();
+        }
+    }
+    return mine;
+}
+
+// One token: each pick is a group of its own, and the finishing warps turn the scores in
+// ctl->weight into weights.  Up to 128 experts an expert's place is the number of experts before
+// it, which all threads count at once (128 experts, K = 8: 31.4 us a call, by rounds 32.5; 256
+// experts, E4M3: 75.5, by rounds 73.6).
+__device__ __forceinline__ void choose_one(const FewArgs& a, Ctl* ctl, uint32_t* keys,
+                                           const float* scores) {
+    const int shared = a.Is > 0;
+    const auto pick = [&](int j, int e) {
+        ctl->expert[shared + j] = (uint16_t)e;
+        ctl->weight[j] = scores[e];
+    };
+    if (a.E <= 128) {
+        for (int e = threadIdx.x; e < a.E; e += kThreads) {
+            const uint32_t key = keys[e];
+            int before = 0;
+            // ties go to the lower expert: those below e need only reach its key
+#pragma unroll 4
+            for (int q = 0; q < a.E / 4; ++q) {
+                const uint4 k = reinterpret_cast<const uint4*>(keys)[q];
+                const int at = 4 * q;
+                before += k.x > key - (at < e) ? 1 : 0;
+                before += k.y > key - (at + 1 < e) ? 1 : 0;
+                before += k.z > key - (at + 2 < e) ? 1 : 0;
+                before += k.w > key - (at + 3 < e) ? 1 : 0;
+            }
+            for (int o = a.E / 4 * 4; o < a.E; ++o) before += keys[o] > key - (o < e) ? 1 : 0;
+            if (before < a.K) pick(before, e);
+        }
+    } else if (threadIdx.x < 32) {
+        const int mine = rounds(keys, a.E, a.K, threadIdx.x);
+        if (threadIdx.x < a.K) pick(threadIdx.x, mine);
+    }
+    const int g = (int)threadIdx.x - 64;
+    if (g >= 0 && g < shared + a.K) {
+        ctl->mask[g] = 1;
+        ctl->row0[g] = (uint16_t)g;
+        if (g < shared) ctl->expert[g] = 0;
+        else ctl->pick[g - shared] = (uint16_t)g;
+    }
+    if (threadIdx.x == 128) {
+        ctl->groups = shared + a.K;
+        if (a.xs) ctl->xs[0] = __ldcg(a.xs);
+    }
+}
+
 // The whole block chooses every token's experts (the rule of moe_route: the K largest keys,
 // ties to the lower expert) and lists the groups; the caller's barrier follows.  `keys`, `scores`: T * E words each.
-__device__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* keys, float* scores) {
+template <bool ONE>
+__device__ __forceinline__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* keys, float* scores) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int shared = a.Is > 0, slots = a.T * a.K;
-    if (threadIdx.x < 32) ctl->present[threadIdx.x] = 0u;
-    for (int i = threadIdx.x; i <= kMaxGroups; i += kThreads) ctl->mask[i] = 0;
+    if constexpr (!ONE) {
+        if (threadIdx.x < 32) ctl->present[threadIdx.x] = 0u;
+        for (int i = threadIdx.x; i <= kMaxGroups; i += kThreads) ctl->mask[i] = 0;
+    }
     for (int i = threadIdx.x; i < a.T * a.E; i += kThreads) {
         const int e = i % a.E;
         const float s = score_of(a, i / a.E, e), b = a.bias ? __ldg(a.bias + e) : 0.0f;
         scores[i] = s;
-        keys[i] = ordered(a.sigmoid ? 1.0f / (1.0f + expf(-s)) + b : s + b);
+        keys[i] = max(ordered(a.sigmoid ? 1.0f / (1.0f + expf(-s)) + b : s + b), 1u);  // 0: taken
     }
     __syncthreads();
+    if constexpr (ONE) return choose_one(a, ctl, keys, scores);
     for (int t = warp; t < a.T; t += kThreads / 32) {
-        // A lane has the experts lane, lane + 32, ...; its best one that is not taken (0: none;
-        // no key is 0, which would be a NaN of all ones: it is read as 1).  The first eight
-        // stay in registers, more are read again after each pick.
-        uint32_t* key = keys + t * a.E;
-        uint32_t k8[8], best = 0u;
-        int at = 0;
-#pragma unroll
-        for (int m = 0; m < 8; ++m) k8[m] = lane + 32 * m < a.E ? max(key[lane + 32 * m], 1u) : 0u;
-        const auto rescan = [&]() {
-            best = 0u;
-#pragma unroll
-            for (int m = 0; m < 8; ++m)
-                if (k8[m] > best) {
-                    best = k8[m];
-                    at = lane + 32 * m;
-                }
-#pragma unroll 4
-            for (int e = lane + 256; e < a.E; e += 32)
-                if (key[e] > best) {
-                    best = key[e];
-                    at = e;
-                }
-        };
-        for (int e = lane + 256; e < a.E; e += 32) key[e] = max(key[e], 1u);
-        rescan();
-        int mine = 0;  // lane j: the j-th pick
-        for (int j = 0; j < a.K; ++j) {
-            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-            const int e = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7fffffff);
-            if (lane == j) mine = e;
-            if ((e & 31) == lane) {
-#pragma unroll
-                for (int m = 0; m < 8; ++m)
-                    if (e == lane + 32 * m) k8[m] = 0u;
-                if (e >= 256) key[e] = 0u;
-                rescan();
-            }
-        }
-        // weights: a / (sum + 1e-6) or softmax over the picked keys
-        const float s = scores[t * a.E + mine], b = a.bias ? __ldg(a.bias + mine) : 0.0f;
-        const float first = __shfl_sync(0xffffffffu, s + b, 0);
-        float w = 0.0f;
-        if (lane < a.K) w = a.sigmoid ? 1.0f / (1.0f + expf(-s)) : expf(s + b - first);
-        const float sum = warp_sum(w) + (a.sigmoid ? 1e-6f : 0.0f);
+        const int mine = rounds(keys + t * a.E, a.E, a.K, lane);
+        float sum;
+        const float w = pick_weight(a, scores[t * a.E + mine], mine, lane, sum);
         if (lane < a.K) {
             ctl->pick[t * a.K + lane] = (uint16_t)mine;
             ctl->weight[t * a.K + lane] = w / sum;
@@ -785,7 +845,7 @@ __device__ __forceinline__ void add_down(uint32_t at, const float* hs, const flo
     }
 }
 
-template <int FMT, int NT>
+template <int FMT, int NT, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1)
 few_experts_kernel(const __grid_constant__ FewArgs a) {
     using C = Cfg<FMT, NT>;
@@ -830,7 +890,7 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
     pdl_trigger();
     // thread 0's first claim: asked for here, answered while the experts are chosen
     int claim = threadIdx.x == 0 ? atomicAdd(a.claim, 1) : 0;
-    choose(a, ctl, reinterpret_cast<uint32_t*>(ring),
+    choose<ONE>(a, ctl, reinterpret_cast<uint32_t*>(ring),
            reinterpret_cast<float*>(ring) + a.T * a.E);
     // the ring held keys: order them before the copies that overwrite them
     ptx::fence_proxy_async_smem();
@@ -1208,6 +1268,17 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
             // ---------------------------------------------- finishing
             // Its own warps, so that the fence and the count of a part (microseconds while
             // the memory is busy) hold up neither the sums nor the stream.
+            if constexpr (ONE) {
+                if (warp == 8) {
+                    const bool on = lane < a.K;
+                    float sum;
+                    const float w = pick_weight(a, on ? ctl->weight[lane] : 0.0f,
+                                                on ? ctl->expert[shared + lane] : 0, lane, sum);
+                    __syncwarp();
+                    if (on) ctl->weight[lane] = w / sum;
+                }
+                finish_sync();
+            }
             while (pass(&ctl->summed[slot], qphase, 50)) {
                 const int uid = ctl->queue[slot];
                 release(&ctl->qempty[slot]);
@@ -1288,14 +1359,15 @@ bool rows_map(CUtensorMap* m, const void* base, int size, int64_t planes, int64_
                     {cols * size, rows * cols * size, 128}, {128 / size, box, (int)planes, q});
 }
 
-template <int FMT, int NT>
+// ONE: T = 1, of its own, for its choice is another and its code is read anew by every call
+template <int FMT, int NT, bool ONE = false>
 cudaError_t go(const FewArgs& a, cudaStream_t st) {
     using C = Cfg<FMT, NT>;
     constexpr size_t smem = 1024 + (size_t)C::kStages * C::kStage + sizeof(Ctl);
     static_assert(smem <= 232448, "shared memory exceeds the per-block limit");
     static_assert(8u * kMaxT * 1024 <= (size_t)C::kStages * C::kStage, "keys and scores fit the ring");
     static_assert(sizeof(FewArgs) <= 4000, "the arguments fit the launch");
-    cudaError_t e = cudaFuncSetAttribute(few_experts_kernel<FMT, NT>,
+    cudaError_t e = cudaFuncSetAttribute(few_experts_kernel<FMT, NT, ONE>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // no more blocks than units, were every pick another expert's
@@ -1303,7 +1375,7 @@ cudaError_t go(const FewArgs& a, cudaStream_t st) {
     const int64_t units = a.gp * (a.Is + groups * a.I) / kGateRows +
                           a.dp * (groups + (a.Is > 0)) * ceil_div(a.d, kDownRows);
     const int sms = device_sm_count();
-    return launch_pdl(few_experts_kernel<FMT, NT>, dim3((unsigned)(units < sms ? units : sms)),
+    return launch_pdl(few_experts_kernel<FMT, NT, ONE>, dim3((unsigned)(units < sms ? units : sms)),
                       dim3(kThreads), smem, st, a);
 }
 
@@ -1439,6 +1511,7 @@ cudaError_t launch_few(const moe_shape& s, int fmt, const FewCall& c, void* work
     else MOE_SCORES(8);
 #undef MOE_SCORES
     if (e != cudaSuccess) return e;
+    if (T == 1) return fmt == 0 ? go<0, 8, true>(a, st) : fmt == 1 ? go<1, 8, true>(a, st) : go<2, 8, true>(a, st);
     if (fmt == 0) return nt == 8 ? go<0, 8>(a, st) : go<0, 16>(a, st);
     if (fmt == 1) return nt == 8 ? go<1, 8>(a, st) : go<1, 16>(a, st);
     return nt == 8 ? go<2, 8>(a, st) : go<2, 16>(a, st);
