@@ -93,6 +93,35 @@ def test_all_tokens_at_the_same_experts(moe, fmt, T):
     assert (y == y[0]).all()
 
 
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("E", [102, 127, 200, 300])
+def test_ties_go_to_the_lower_expert(moe, E, T):
+    """Scores that are all equal choose what a bias that falls from expert to expert does (the
+    sigmoid router's bias is not in its weights)."""
+    c = ref.inputs(T, 128, E, 5, 128, 128, "sigmoid", "bf16", E + T)
+    c["w_g"].zero_()
+    c["bias"] = 0.01 * torch.arange(E, 0, -1)
+    _, y = _check(moe, c)
+    c["bias"] = None
+    tied = Layer(moe, c, 255)()
+    torch.cuda.synchronize()
+    assert torch.equal(tied, y)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("E", [24, 150])
+def test_one_token_that_is_not_finite(moe, fmt, E):
+    """Its row is NaN, the call ends without an error and the next one is right."""
+    c = ref.inputs(1, 256, E, 4, 256, 128, "softmax", fmt, E)
+    layer, y = _check(moe, c)
+    bad = torch.full_like(layer.g["x"], float("nan"))
+    out = layer(x=bad)
+    again = layer()
+    torch.cuda.synchronize()
+    assert moe.moe_get_device_error(layer.ws) == 0
+    assert torch.isnan(out).all() and torch.equal(again, y)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T", [1, 8, 16])
 def test_same_bits_on_every_run(moe, fmt, T):
