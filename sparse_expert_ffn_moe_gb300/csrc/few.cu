@@ -476,24 +476,10 @@ __device__ __forceinline__ void choose_one(const FewArgs& a, Ctl* ctl, uint32_t*
     }
 }
 
-// The whole block chooses every token's experts (the rule of moe_route: the K largest keys,
-// ties to the lower expert) and lists the groups; the caller's barrier follows.  `keys`, `scores`: T * E words each.
-template <bool ONE>
-__device__ __forceinline__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* keys, float* scores) {
+__device__ __forceinline__ void choose_many(const FewArgs& a, Ctl* ctl, uint32_t* keys,
+                                            const float* scores) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int shared = a.Is > 0, slots = a.T * a.K;
-    if constexpr (!ONE) {
-        if (threadIdx.x < 32) ctl->present[threadIdx.x] = 0u;
-        for (int i = threadIdx.x; i <= kMaxGroups; i += kThreads) ctl->mask[i] = 0;
-    }
-    for (int i = threadIdx.x; i < a.T * a.E; i += kThreads) {
-        const int e = i % a.E;
-        const float s = score_of(a, i / a.E, e), b = a.bias ? __ldg(a.bias + e) : 0.0f;
-        scores[i] = s;
-        keys[i] = max(ordered(a.sigmoid ? 1.0f / (1.0f + expf(-s)) + b : s + b), 1u);  // 0: taken
-    }
-    __syncthreads();
-    if constexpr (ONE) return choose_one(a, ctl, keys, scores);
     for (int t = warp; t < a.T; t += kThreads / 32) {
         const int mine = rounds(keys + t * a.E, a.E, a.K, lane);
         float sum;
@@ -600,6 +586,26 @@ __device__ __forceinline__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* key
                                                             ((1u << (f / a.K)) - 1u)));
     }
     if (a.xs && threadIdx.x < a.T) ctl->xs[threadIdx.x] = __ldcg(a.xs + threadIdx.x);
+}
+
+// The whole block chooses every token's experts (the rule of moe_route: the K largest keys,
+// ties to the lower expert) and lists the groups; the caller's barrier follows.  `keys`,
+// `scores`: T * E words each.
+template <bool ONE>
+__device__ __forceinline__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* keys, float* scores) {
+    if constexpr (!ONE) {
+        if (threadIdx.x < 32) ctl->present[threadIdx.x] = 0u;
+        for (int i = threadIdx.x; i <= kMaxGroups; i += kThreads) ctl->mask[i] = 0;
+    }
+    for (int i = threadIdx.x; i < a.T * a.E; i += kThreads) {
+        const int e = i % a.E;
+        const float s = score_of(a, i / a.E, e), b = a.bias ? __ldg(a.bias + e) : 0.0f;
+        scores[i] = s;
+        keys[i] = max(ordered(a.sigmoid ? 1.0f / (1.0f + expf(-s)) + b : s + b), 1u);  // 0: taken
+    }
+    __syncthreads();
+    if constexpr (ONE) choose_one(a, ctl, keys, scores);
+    else choose_many(a, ctl, keys, scores);
 }
 
 // y of a tile of 128 columns from every part of every row: the shared expert first, then a
@@ -1380,8 +1386,12 @@ cudaError_t go(const FewArgs& a, cudaStream_t st) {
 }
 
 constexpr int kClaimInts = 64;
+// Tokens of a warp of launch 1: fewer where that leaves less than these units, for a warp's
+// loads and sums are a chain that all wait for (64 experts of 2048, T = 3: a token each 60.3 us a
+// call, two 60.7, four 62; 256 experts of 7168, E4M3, T = 8: four 312 us, eight 314).
+constexpr int kScoreUnits = 4096;
 int score_splits(int d) {
-    const int n = d / 8 / 96;  // about three 16-byte vectors a lane
+    const int n = d / 8 / 32;  // a 16-byte vector a lane, or more in rows wider than 2048
     return n < 1 ? 1 : n > kScoreSplits ? kScoreSplits : n;
 }
 
@@ -1491,8 +1501,10 @@ cudaError_t launch_few(const moe_shape& s, int fmt, const FewCall& c, void* work
     }
     if (!ok) return cudaErrorInvalidValue;
 
-    const int tt = T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8;
-    const int units = (int)ceil_div(T, tt) * s.E * w.splits;
+    const auto units_of = [&](int tokens) { return (int)ceil_div(T, tokens) * s.E * w.splits; };
+    int tt = T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8;
+    while (tt > 1 && units_of(tt) < kScoreUnits) tt /= 2;
+    const int units = units_of(tt);
     int blocks = (int)ceil_div(units, kScoreWarps);
     const int most = 8 * device_sm_count();
     if (blocks > most) blocks = most;
