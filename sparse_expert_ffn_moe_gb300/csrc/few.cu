@@ -43,12 +43,13 @@
 //
 // Measured (GB300, a CUDA graph's time a call; floor: the picked experts' bytes at the
 // measured copy's 6788 GB/s): 256 experts of 7168 x 2048, K = 8, and a shared one, bf16:
-// T = 1 126 us (floor 117), T = 8 607 (617), T = 16 921 (941); E4M3 T = 1 72 (59), T = 8
-// 319 (309), T = 16 492 (471); block scales, T = 13 447 (422).  Small layers are a chain of
-// joints: eight experts of 2048 x 768 31 us (floor 11), two of 256 x 512 15 us.  Tried and slower: units of 16 or
-// 32 rows, which leave the products' other rows empty (T = 1 209 and 146 us against 131);
-// units a quarter as long with more parts (T = 1 160); two accumulators in turn (+ 2 %);
-// claims of several units at a time (177); the sums' warps counting parts themselves.
+// T = 1 126 us (floor 117), T = 8 603 (617), T = 16 920 (941); E4M3 T = 1 72 (59), T = 8
+// 318 (309), T = 16 492 (471); block scales, T = 13 446 (422).  Small layers are a chain of
+// joints: eight experts of 2048 x 768 31 us (floor 11), two of 256 x 512 14 us.  Tried and
+// slower: units of 16 or 32 rows, which leave the products' other rows empty (T = 1 209 and
+// 146 us against 131); units a quarter as long with more parts (T = 1 160); two accumulators
+// in turn (+ 2 %); claims of several units at a time (177); the sums' warps counting parts
+// themselves.
 #include <cuda.h>
 #include <cuda_fp8.h>
 #include <math.h>
@@ -1391,7 +1392,9 @@ constexpr int kClaimInts = 64;
 // call, two 60.7, four 62; 256 experts of 7168, E4M3, T = 8: four 312 us, eight 314).
 constexpr int kScoreUnits = 4096;
 int score_splits(int d) {
-    const int n = d / 8 / 32;  // a 16-byte vector a lane, or more in rows wider than 2048
+    // a 16-byte vector a lane, or more in rows wider than 2048 (64 experts of 2048, T = 3: 62 us
+    // a call, with three vectors 64)
+    const int n = d / 8 / 32;
     return n < 1 ? 1 : n > kScoreSplits ? kScoreSplits : n;
 }
 
