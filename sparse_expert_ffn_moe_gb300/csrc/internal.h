@@ -320,7 +320,7 @@ struct FewCall {
 cudaError_t launch_few(const moe_shape& s, int fmt, const FewCall& c, void* workspace,
                        cudaStream_t st);
 
-// ffn_tc.cu: the driver's tensor-map encoder (NULL if it cannot be found), the bound on
+// ffn_tc.cu: CUDA's tensor-map encoder (NULL if it cannot be found), the bound on
 // device waits and the switch of the tests that makes one run out
 void* tensor_map_encoder();
 unsigned long long tc_timeout_ns();
