@@ -4,7 +4,8 @@
 Tolerances, with u = 2^-24 (half a step of fp32) and h = eps / 2 of the rows' type:
   s        the fp32 sum rounded once: equal bits.
   y        a thread adds <= 72 squares, then 10 lane and warp steps: < 96 u of the mean,
-           half of it in the root, 4 roundings more: 64 u, and h of the rounded value.
+           half of it in the root, the root 2 last places (4 u), 4 roundings more: 64 u, and h of
+           the rounded value.
   scales   as y: 64 u.
   codes    half a step of E4M3: 2^-4 of a normal value, 2^-10 scales of a small one,
            and the 64 u of y and of the scale.
