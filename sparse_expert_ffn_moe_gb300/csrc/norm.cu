@@ -483,6 +483,7 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 constexpr int kDepth = 3;  // rows in a ring
 
 constexpr size_t kRingSmem = 220 * 1024;  // of an SM, for the rings of its blocks
+constexpr size_t kStaticSmem = 2 * 32 * sizeof(float2);  // beside them, a block's reductions
 
 // s and d_y come by way of the ring, where each thread copies and reads its own; d_s straight
 // to registers, asked for before the row's sums.  WARP: rows of up to kWarpVecs / 2 vectors, a
@@ -875,7 +876,8 @@ cudaError_t backward(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
     const bool vec = whole_vectors(a.dtype, a.d);
     if (p.lanes) return vec ? back_teams<T, true>(a, p, st) : back_teams<T, false>(a, p, st);
     const auto go = [&](auto kernel) {
-        if (p.smem > 48 * 1024) {
+        // a launch has 48 KB without asking, of which static arrays take their part
+        if (p.smem + kStaticSmem > 48 * 1024) {
             const cudaError_t e =
                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
             if (e != cudaSuccess) return e;
