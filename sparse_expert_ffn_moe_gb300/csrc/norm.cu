@@ -876,10 +876,12 @@ cudaError_t backward(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
     const bool vec = whole_vectors(a.dtype, a.d);
     if (p.lanes) return vec ? back_teams<T, true>(a, p, st) : back_teams<T, false>(a, p, st);
     const auto go = [&](auto kernel) {
-        // a launch has 48 KB without asking, of which static arrays take their part
+        // A launch has 48 KB without asking, of which static arrays take their part.  What is
+        // asked for is the same for every call, so calls of several threads do not undo each
+        // other's.
         if (p.smem + kStaticSmem > 48 * 1024) {
-            const cudaError_t e =
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+            const cudaError_t e = cudaFuncSetAttribute(
+                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingSmem);
             if (e != cudaSuccess) return e;
         }
         return launch_pdl(kernel, dim3(p.blocks), dim3(p.threads), p.smem, st, (const T*)a.d_y,

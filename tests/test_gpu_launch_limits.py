@@ -1,13 +1,22 @@
 """Launches whose shared memory passes the 48 KB that a launch has without asking for more."""
+import ctypes
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
+import torch
 
 pytestmark = pytest.mark.gpu
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import sparse_expert_ffn_moe_gb300 as m
+    return m
 
 
 # The norm's backward pass with rings of 48 KB, just below and above: the limit counts the
@@ -36,3 +45,42 @@ def test_first_call_at_48_kb_of_ring(sizes):
     done = subprocess.run([sys.executable, "-c", FIRST.format(root=ROOT, sizes=sizes)],
                           capture_output=True, text=True, timeout=300)
     assert done.returncode == 0 and done.stdout == "fine\n", done.stderr[-2000:]
+
+
+def _side_by_side(calls, n):
+    """Every call n times in a host thread of its own, all at once; what they return but 0."""
+    wrong = []
+
+    def go(call):
+        for _ in range(n):
+            rc = call()
+            if rc:
+                wrong.append(rc)
+
+    threads = [threading.Thread(target=go, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return wrong
+
+
+def _ptr(t):
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def test_threads_whose_rings_differ_in_size(moe):
+    """Calls of several host threads, each on its own stream, of one kernel with rings of
+    different sizes: none may lower the limit that another's launch needs."""
+    keep, calls = [], []
+    for d in (4104, 4608, 5000, 5120):
+        x, w = torch.ones(2, d, device="cuda").bfloat16(), torch.ones(d, device="cuda").bfloat16()
+        dx, dw, ws = torch.empty_like(x), torch.empty(d, device="cuda"), moe.alloc_rmsnorm_workspace(2, d)
+        st = torch.cuda.Stream()
+        args = (2, d, moe.MOE_BF16, _ptr(x), _ptr(x), _ptr(w), 0.0, None, _ptr(dx), _ptr(dw), _ptr(ws),
+                ws.numel(), ctypes.c_void_p(st.cuda_stream))
+        keep.append((x, w, dx, dw, ws, st))
+        calls.append(lambda args=args: moe.library().moe_rmsnorm_backward(*args))
+    torch.cuda.synchronize()
+    assert not _side_by_side(calls, 20000)
