@@ -453,12 +453,15 @@ cudaError_t launch_gemv_t(const FfnGroups& g, const FfnPlanHeader* hdr, const in
     const int max_inter = g.has_shared && g.Is > g.I ? g.Is : g.I;
     const size_t smem_gu = (size_t)MT * g.d * sizeof(T);
     const size_t smem_dn = (size_t)MT * max_inter * sizeof(T);
+    // what the widest layer needs, the same for every call: calls of several threads do not
+    // undo each other's
+    constexpr int most = MT * 16384 * sizeof(T);
     cudaError_t e;
     e = cudaFuncSetAttribute(gemv_gate_up_kernel<T, MT, U>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_gu);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(gemv_down_kernel<T, MT, U>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_dn);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     int occ_gu = 1, occ_dn = 1;
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ_gu, gemv_gate_up_kernel<T, MT, U>, kThreads,
@@ -507,9 +510,11 @@ cudaError_t launch_dispatch_plan_small(const moe_shape& s, const int32_t* topk_i
                                        FfnPlanHeader* hdr, int32_t* gemv_list, int4* mtile_list,
                                        int max_mtiles, int gemv_limit, bool allow_pair,
                                        int small_rows, cudaStream_t st) {
-    const size_t smem = sizeof(int32_t) * (32 * (size_t)s.E + s.E + 1);
+    const auto bytes = [](size_t E) { return sizeof(int32_t) * (33 * E + 1); };
+    const size_t smem = bytes(s.E);
+    // the same for every call, whatever its E
     cudaError_t e = cudaFuncSetAttribute(dispatch_plan_small_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(1024));
     if (e != cudaSuccess) return e;
     return launch_pdl(dispatch_plan_small_kernel, dim3(1), dim3(1024), smem, st, topk_idx,
                       s.T * s.K, s.K, counts, offsets, perm, inv_perm, tok_of, err,

@@ -480,12 +480,17 @@ constexpr int kG8Small = 8;  // rows of the first GEMV list's groups (one MMA co
 // carve-out and ~85% with 115 KB).
 constexpr size_t kG8FastSmem = 120 * 1024;
 
+// What a kernel of R rows a pass asks for: the same for every call, whatever its width, so that
+// calls of several threads do not undo each other's.
+template <int R>
+constexpr int kG8MostSmem = (int)(R > kG8Tok ? kG8FastSmem : kGemv8SmemLimit);
+
 template <int R, bool BLK>
 cudaError_t launch_gu_as(const FfnGroups& g, const FfnPlanHeader* hdr, const int32_t* list, int which,
                          cudaStream_t st) {
     const size_t sm = gemv8_smem(g.d, R);
     cudaError_t e = cudaFuncSetAttribute(gemv8_gate_up_kernel<R, BLK>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kG8MostSmem<R>);
     if (e != cudaSuccess) return e;
     return launch_pdl(gemv8_gate_up_kernel<R, BLK>, dim3(device_sm_count()), dim3(kG8Threads), sm, st, g,
                       hdr, list, which);
@@ -503,7 +508,7 @@ cudaError_t launch_dn_as(const FfnGroups& g, const FfnPlanHeader* hdr, const int
                          int max_inter, cudaStream_t st) {
     const size_t sm = gemv8_smem(max_inter, R);
     cudaError_t e = cudaFuncSetAttribute(gemv8_down_kernel<R, BLK>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kG8MostSmem<R>);
     if (e != cudaSuccess) return e;
     return launch_pdl(gemv8_down_kernel<R, BLK>, dim3(device_sm_count()), dim3(kG8Threads), sm, st, g,
                       hdr, list, which);

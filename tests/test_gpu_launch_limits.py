@@ -84,3 +84,41 @@ def test_threads_whose_rings_differ_in_size(moe):
         calls.append(lambda args=args: moe.library().moe_rmsnorm_backward(*args))
     torch.cuda.synchronize()
     assert not _side_by_side(calls, 20000)
+
+
+# d, E of fp32 layers (rows of x in shared memory), of 8-bit ones (the same as halves), and of
+# layers whose dispatch holds a table of experts
+LAYERS = {"f32": [(7168, 4), (8192, 4), (16384, 4)], "fp8": [(2048, 4), (4096, 4), (8192, 4)],
+          "experts": [(64, 16), (64, 500), (64, 1024)]}
+
+
+@pytest.mark.parametrize("kind", LAYERS)
+def test_threads_whose_layers_differ_in_size(moe, kind):
+    keep, calls = [], []
+    for d, E in LAYERS[kind]:
+        I = 64 if kind == "experts" else 128  # noqa: E741
+        s = moe.make_shape(1, d, E, 1, I, 0, "f32" if kind == "f32" else "bf16")
+        t = torch.float32 if kind == "f32" else torch.bfloat16
+        x, w_g, gate, up = (torch.randn(n, device="cuda").to(t) for n in
+                            ((1, d), (E, d), (E, I, d), (E, I, d)))
+        down, y, ws = torch.randn(E, d, I, device="cuda").to(t), torch.empty_like(x), moe.alloc_workspace(s)
+        st = torch.cuda.Stream()
+        tail = (_ptr(y), _ptr(ws), ws.numel(), ctypes.c_void_p(st.cuda_stream))
+        if kind == "fp8":
+            q = {}
+            for n, w in (("gate", gate), ("up", up), ("down", down)):
+                q["w_" + n] = torch.empty(w.shape, dtype=torch.uint8, device="cuda")
+                q["s_" + n] = torch.empty(w.shape[:-1], device="cuda")
+                moe.moe_quantize_fp8_rows(w, q["w_" + n], q["s_" + n])
+            w8 = moe.make_fp8_experts(q)
+            args = (ctypes.byref(s), _ptr(x), _ptr(w_g), None, ctypes.byref(w8), *tail)
+            call = moe.library().moe_forward_fp8
+            keep.append((q, w8))
+        else:
+            args = (ctypes.byref(s), _ptr(x), _ptr(w_g), None, _ptr(gate), _ptr(up), _ptr(down), None, None,
+                    None, *tail)
+            call = moe.library().moe_forward
+        keep.append((s, x, w_g, gate, up, down, y, ws, st))
+        calls.append(lambda args=args, call=call: call(*args))
+    torch.cuda.synchronize()
+    assert not _side_by_side(calls, 3000)
