@@ -598,7 +598,7 @@ size_t moe_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
  * NULL, not both; the workspace is needed for d_weight alone.  d_x may be d_y,
  * d_s or s itself.  Sums go in a fixed order (no atomics): the same bits on
  * every run.  Limits and alignment as in moe_rmsnorm; with rows == 0 d_weight
- * is zeroed.
+ * is zeroed if it is not NULL, and the other arrays may all be NULL.
  */
 moe_status moe_rmsnorm_backward(int64_t rows, int64_t cols, int32_t dtype, const void *d_y,
                                 const void *s, const void *weight, float eps,

@@ -83,7 +83,8 @@ moe_status moe_rmsnorm(int64_t rows, int64_t cols, int32_t dtype, const void* x,
 
 size_t moe_rmsnorm_workspace_bytes(int64_t rows, int64_t cols) {
     if (check_sizes(rows, cols) != MOE_OK) return 0;
-    const size_t blocks = (size_t)rmsnorm_backward_blocks(rows, (int)cols);
+    // 0 stands for a refusal: no rows, which are a valid call, get a block's room
+    const size_t blocks = rows == 0 ? 1 : (size_t)rmsnorm_backward_blocks(rows, (int)cols);
     return (sizeof(float) * blocks * (size_t)cols + 255) / 256 * 256;
 }
 
@@ -93,12 +94,12 @@ moe_status moe_rmsnorm_backward(int64_t rows, int64_t cols, int32_t dtype, const
                                 void* stream) {
     moe_status st = check_norm(rows, cols, dtype, eps);
     if (st != MOE_OK) return st;
-    if (!d_x && !d_weight) return MOE_ERR_INVALID_ARG;
     if (!good_or_null(d_x) || !good_or_null(d_weight)) return MOE_ERR_INVALID_ARG;
     cudaStream_t cs = (cudaStream_t)stream;
-    if (rows == 0)
+    if (rows == 0)  // arrays without elements may be NULL, d_x among them
         return d_weight ? cuda_status(cudaMemsetAsync(d_weight, 0, sizeof(float) * (size_t)cols, cs))
                         : MOE_OK;
+    if (!d_x && !d_weight) return MOE_ERR_INVALID_ARG;
     if (!good(d_y) || !good(s) || !good(weight) || !good_or_null(d_s)) return MOE_ERR_INVALID_ARG;
     const uint64_t n = (uint64_t)rows * (uint64_t)cols * (dtype == MOE_BF16 ? 2 : 4);
     const uint64_t wn = (uint64_t)cols * (dtype == MOE_BF16 ? 2 : 4), dn = 4 * (uint64_t)cols;
