@@ -532,7 +532,7 @@ moe_status moe_combine_backward(const moe_shape *shape, const void *d_y,
  * of moe_forward, moe_forward_fp8 and moe_forward_fp8_blocks; shape->dtype must be
  * MOE_BF16 (and d, inter, inter_shared multiples of 128 for 8-bit weights), T at
  * most 16, else MOE_ERR_UNSUPPORTED.  residual [T][d] may be NULL; y may be the
- * residual itself, not x.  The intermediates are finer than moe_forward's: sums,
+ * residual itself, and else y and the workspace overlap nothing that is read.  The intermediates are finer than moe_forward's: sums,
  * expert outputs and the combine stay in fp32, h is read as planes of 16 (bf16
  * weights) or 12 bits (8-bit weights), x exactly -- with 8-bit weights down to
  * 2^-21 of the token's largest value.
@@ -595,8 +595,8 @@ size_t moe_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
  *   d_weight = sum over the rows of d_y * h        [cols] fp32
  * d_s (may be NULL) is the gradient that reaches s by the residual stream; d_x
  * is then the gradient of x and of the residual alike.  d_x or d_weight may be
- * NULL, not both; the workspace is needed for d_weight alone.  d_x may be d_y,
- * d_s or s itself.  Sums go in a fixed order (no atomics): the same bits on
+ * NULL, not both; the workspace is needed for d_weight alone, and overlaps no
+ * array.  d_x may be d_y, d_s or s itself.  Sums go in a fixed order (no atomics): the same bits on
  * every run.  Limits and alignment as in moe_rmsnorm; with rows == 0 d_weight
  * is zeroed if it is not NULL, and the other arrays may all be NULL.
  */

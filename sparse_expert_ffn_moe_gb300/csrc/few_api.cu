@@ -18,11 +18,6 @@ moe_status check_few(const moe_shape* shape) {
     return shape->T <= kFewMaxTokens && shape->dtype == MOE_BF16 ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
-bool overlap(const void* p, const void* q, uint64_t n) {
-    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-    return a < b + n && b < a + n;
-}
-
 // what both kinds of call check and enqueue; c has the weights
 moe_status run(const moe_shape& s, int fmt, const FewCall& c, void* workspace, size_t ws_bytes,
                void* stream) {
@@ -44,11 +39,28 @@ moe_status run(const moe_shape& s, int fmt, const FewCall& c, void* workspace, s
         for (const void* p : ss)
             if (shared && !good(p)) return MOE_ERR_INVALID_ARG;
     }
-    // y is written while x is still read; the residual's elements are read where y's are written
-    const uint64_t bytes = 2 * (uint64_t)s.T * (uint64_t)s.d;
-    if (overlap(c.y, c.x, bytes) || (c.residual && c.residual != c.y && overlap(c.y, c.residual, bytes)))
-        return MOE_ERR_INVALID_ARG;
-    if (!good(workspace) || ws_bytes < few_ws(s, fmt).total) return MOE_ERR_WORKSPACE;
+    const size_t need = few_ws(s, fmt).total;
+    if (!good(workspace) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+    // What is written lies apart from what is read.  The residual alone may be y: its elements are
+    // read where y's are written.
+    const uint64_t E = s.E, d = s.d, I = s.inter, Is = s.inter_shared;
+    const uint64_t rows = 2 * (uint64_t)s.T * d, size = fmt ? 1 : 2;
+    const uint64_t up = fmt == 1 ? 4 * I : I * d / 4096, down = fmt == 1 ? 4 * d : I * d / 4096;
+    const uint64_t sup = fmt == 1 ? 4 * Is : Is * d / 4096, sdown = fmt == 1 ? 4 * d : Is * d / 4096;
+    const struct {
+        const void* p;
+        uint64_t bytes;
+    } in[] = {{c.x, rows}, {c.residual, rows}, {c.w_g, 2 * E * d}, {c.bias, 4 * E},
+              {c.w_gate, E * I * d * size}, {c.w_up, E * I * d * size}, {c.w_down, E * I * d * size},
+              {c.ws_gate, Is * d * size}, {c.ws_up, Is * d * size}, {c.ws_down, Is * d * size},
+              {c.s_gate, E * up}, {c.s_up, E * up}, {c.s_down, E * down},
+              {c.ss_gate, sup}, {c.ss_up, sup}, {c.ss_down, sdown}};
+    for (const auto& i : in) {
+        if (overlap(workspace, need, i.p, i.bytes)) return MOE_ERR_INVALID_ARG;
+        const bool in_place = i.p == c.residual && c.residual == c.y;
+        if (!in_place && overlap(c.y, rows, i.p, i.bytes)) return MOE_ERR_INVALID_ARG;
+    }
+    if (overlap(c.y, rows, workspace, need)) return MOE_ERR_INVALID_ARG;
     if (!tc_available()) return MOE_ERR_UNSUPPORTED;
     return launch_few(s, fmt, c, workspace, (cudaStream_t)stream) == cudaSuccess ? MOE_OK
                                                                                  : MOE_ERR_CUDA;

@@ -284,6 +284,12 @@ cudaError_t launch_route_backward(const moe_shape& s, RouteBackwardArgs a, cudaS
 
 int device_sm_count();
 
+// [p, p + n) and [q, q + m) share a byte (NULL shares none)
+inline bool overlap(const void* p, uint64_t n, const void* q, uint64_t m) {
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    return p && q && a < b + m && b < a + n;
+}
+
 // norm.cu: RMS norm (x, residual -> s, y, codes and scales) and its backward pass
 // (d_y, x = s, d_s -> d_x, d_weight by way of part [rmsnorm_backward_blocks][d])
 struct NormArgs {

@@ -29,12 +29,6 @@ moe_status check_norm(int64_t rows, int64_t cols, int32_t dtype, float eps) {
     return check_sizes(rows, cols);
 }
 
-// [p, p + n) and [q, q + m) share a byte
-bool overlap(const void* p, uint64_t n, const void* q, uint64_t m) {
-    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-    return p && q && a < b + m && b < a + n;
-}
-
 }  // namespace
 
 extern "C" {
@@ -110,8 +104,14 @@ moe_status moe_rmsnorm_backward(int64_t rows, int64_t cols, int32_t dtype, const
     if (overlap(d_x, n, weight, wn) || overlap(d_x, n, d_weight, dn) ||
         overlap(d_weight, dn, weight, wn))
         return MOE_ERR_INVALID_ARG;
-    if (d_weight && (!good(workspace) || ws_bytes < moe_rmsnorm_workspace_bytes(rows, cols)))
-        return MOE_ERR_WORKSPACE;
+    if (d_weight) {
+        const size_t need = moe_rmsnorm_workspace_bytes(rows, cols);
+        if (!good(workspace) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+        for (const void* p : {d_y, s, d_s, (const void*)d_x})
+            if (overlap(workspace, need, p, n)) return MOE_ERR_INVALID_ARG;
+        if (overlap(workspace, need, weight, wn) || overlap(workspace, need, d_weight, dn))
+            return MOE_ERR_INVALID_ARG;
+    }
     NormArgs a{};
     a.rows = rows;
     a.d = (int)cols;
