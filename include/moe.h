@@ -573,9 +573,12 @@ moe_status moe_forward_few_fp8_blocks(const moe_shape *shape, const void *x, con
  * weight [cols] has the rows' dtype.  residual, s, y and codes may be NULL, not
  * both y and codes; codes and scales [rows] (fp32) go together.  s may be x or
  * residual itself, and y may be x; other overlaps are not allowed.  All
- * pointers 16-byte aligned.  The squares are summed in fp32: rows whose mean
- * square plus eps is a normal fp32 number, and with codes whose products
- * s * weight are finite ones.  eps is finite and not negative.
+ * pointers 16-byte aligned.  The squares are summed in fp32 before they are
+ * divided: rows whose SUM of squares is finite (magnitudes below 1.8e19 /
+ * sqrt(cols); past that y is 0) and whose mean square plus eps is a normal fp32
+ * number; with codes, rows whose products s * weight are finite and whose largest
+ * is a normal number or so small that scales is 2^-126.  eps is finite and not
+ * negative.
  * A row with a NaN or an infinity spoils no other row.
  * Limits: rows < 2^31, 1 <= cols <= 16384 (any width; multiples of 16 bytes are
  * fastest).  rows == 0 is a no-op.  No workspace.
@@ -597,7 +600,7 @@ size_t moe_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
  * is then the gradient of x and of the residual alike.  d_x or d_weight may be
  * NULL, not both; the workspace is needed for d_weight alone, and overlaps no
  * array.  d_x may be d_y, d_s or s itself.  Sums go in a fixed order (no atomics): the same bits on
- * every run.  Limits and alignment as in moe_rmsnorm; with rows == 0 d_weight
+ * every run.  Limits, range and alignment as in moe_rmsnorm; with rows == 0 d_weight
  * is zeroed if it is not NULL, and the other arrays may all be NULL.
  */
 moe_status moe_rmsnorm_backward(int64_t rows, int64_t cols, int32_t dtype, const void *d_y,
