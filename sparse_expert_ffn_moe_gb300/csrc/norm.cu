@@ -897,8 +897,11 @@ cudaError_t backward(const NormArgs& a, const BackPlan& p, cudaStream_t st) {
     do {                                                                                     \
         if (p.warps) return go(rmsnorm_backward_ring_kernel<T, 2, AL, true>);                \
         if (p.per_thread == 2) return go(rmsnorm_backward_ring_kernel<T, 2, AL, false>);     \
-        if (p.per_thread == 4) return go(rmsnorm_backward_ring_kernel<T, 4, AL, false>);     \
-        return go(rmsnorm_backward_ring_kernel<T, 5, AL, false>);                            \
+        /* whole bf16 vectors of the widest row: 2048, four a thread */                      \
+        if (p.per_thread == 4 || (AL && V == 8))                                             \
+            return go(rmsnorm_backward_ring_kernel<T, 4, AL, false>);                        \
+        if constexpr (!(AL && V == 8))                                                       \
+            return go(rmsnorm_backward_ring_kernel<T, 5, AL, false>);                        \
     } while (0)
     if (vec) MOE_RING(true);
     MOE_RING(false);
