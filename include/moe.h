@@ -529,13 +529,16 @@ moe_status moe_combine_backward(const moe_shape *shape, const void *d_y,
  *   y = residual + SharedExpert(x) + sum_j w_j Expert_{i_j}(x)     (fp32, rounded once)
  * The first launch scores, the second chooses the experts, streams every picked
  * expert's weights once and joins.  Arguments, router rules and layouts are those
- * of moe_forward, moe_forward_fp8 and moe_forward_fp8_blocks; shape->dtype must be
- * MOE_BF16 (and d, inter, inter_shared multiples of 128 for 8-bit weights), T at
- * most 16, else MOE_ERR_UNSUPPORTED.  residual [T][d] may be NULL; y may be the
- * residual itself, and else y and the workspace overlap nothing that is read.  The intermediates are finer than moe_forward's: sums,
- * expert outputs and the combine stay in fp32, h is read as planes of 16 (bf16
- * weights) or 12 bits (8-bit weights), x exactly -- with 8-bit weights down to
- * 2^-21 of the token's largest value.
+ * of moe_forward, moe_forward_fp8 and moe_forward_fp8_blocks; the scores are summed
+ * in another order than moe_route's, so where two keys tie to fp32's last places
+ * another expert may be picked than by those calls.  shape->dtype must be MOE_BF16
+ * (and d, inter, inter_shared multiples of 128 for 8-bit weights), T at most 16,
+ * else MOE_ERR_UNSUPPORTED.  residual [T][d] may be NULL; y may be the residual
+ * itself, and but for that y and the workspace overlap nothing that is read.
+ * The intermediates are finer than moe_forward's: sums, expert outputs and the
+ * combine stay in fp32, h is read as planes of 16 (bf16 weights) or 12 bits (8-bit
+ * weights), x exactly -- with 8-bit weights its values of at least 2^-13 of the
+ * token's largest, and smaller ones to within 2^-21 of that largest.
  * The same bits on every run.  No call waits for a part of the grid that is not
  * running, so calls on several streams (each with its own workspace) may overlap.
  * A token whose row is not finite shows it and spoils no other token.  Graph

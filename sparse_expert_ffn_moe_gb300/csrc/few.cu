@@ -32,9 +32,11 @@
 // alone, so a column that is not wanted costs nothing and spoils nothing, NaN
 // included), and h of the group's tokens.  Precision: bf16 experts take x as it is and
 // h as two bf16 planes (hi, remainder: within 2^-16).  8-bit experts take x as two
-// E4M3 planes, the second 16 times finer, with a power of two as the row's scale,
-// which holds a bf16 value exactly down to 2^-21 of the row's largest; and h as three
-// such planes with a scale per 128 values (within 2^-12, beside a code's own 2^-4).
+// E4M3 planes, the second 16 times finer, with a power of two as the row's scale: a bf16
+// value of at least 2^-13 of the row's largest is held exactly (its code is a normal number,
+// whose remainder the second plane has the bits for), a smaller one to within 2^-21 of the
+// row's largest; and h as three such planes with a scale per 128 values (within 2^-12,
+// beside a code's own 2^-4).
 // Planes are further columns, their sums are joined in fp32.
 //
 // Sums of parts go to buffers, and whoever finishes a tile's last part adds them in
@@ -373,8 +375,8 @@ __device__ __forceinline__ float score_of(const FewArgs& a, int t, int e) {
     return s;
 }
 
-// A key as an integer of the same order: -0 as +0, NaN above all numbers or below them by
-// its sign, so that every pick is one of the experts and none is picked twice.
+// A key as an integer of the same order: -0 as +0, and NaN, which a sum makes the one positive
+// NaN, above all numbers, so that every pick is one of the experts and none is picked twice.
 __device__ __forceinline__ uint32_t ordered(float key) {
     const uint32_t b = __float_as_uint(key + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
@@ -393,8 +395,8 @@ __device__ __forceinline__ float pick_weight(const FewArgs& a, float s, int e, i
 }
 
 // A warp's K rounds: lane j gets the j-th pick.  A lane has the experts lane, lane + 32, ...; its
-// best one that is not taken (0: none; a key of 0, a NaN of all ones, was stored as 1).  The
-// first eight stay in registers, more are read again after each pick.
+// best one that is not taken (0: none).  The first eight stay in registers, more are read again
+// after each pick.
 __device__ __forceinline__ int rounds(uint32_t* key, int E, int K, int lane) {
     uint32_t k8[8], best = 0u;
     int at = 0;
@@ -602,7 +604,8 @@ __device__ __forceinline__ void choose(const FewArgs& a, Ctl* ctl, uint32_t* key
         const int e = i % a.E;
         const float s = score_of(a, i / a.E, e), b = a.bias ? __ldg(a.bias + e) : 0.0f;
         scores[i] = s;
-        keys[i] = max(ordered(a.sigmoid ? 1.0f / (1.0f + expf(-s)) + b : s + b), 1u);  // 0: taken
+        // 0 stands for a taken one
+        keys[i] = max(ordered(a.sigmoid ? 1.0f / (1.0f + expf(-s)) + b : s + b), 1u);
     }
     __syncthreads();
     if constexpr (ONE) choose_one(a, ctl, keys, scores);

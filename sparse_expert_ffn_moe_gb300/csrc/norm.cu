@@ -14,6 +14,10 @@
 // aligned vectors that cover them; those at the ends are stored by element, by one
 // warp of the row.
 //
+// Of the instances, eight spill 8 to 56 bytes a thread: those of a warp a row that are held to
+// 32 or 40 registers, for the blocks an SM that hides the loads' latency, and the backward
+// ring of ragged bf16 rows of 5121 to 16376 elements.
+//
 // Measured (GB300, a CUDA graph's time a call; floor: the bytes at the measured copy's
 // 6788 GB/s): 16384 x 7168 bf16 with residual, both outputs 152 us (floor 156), one array in
 // and out 69 (69); 131072 x 512 78 (79); 20011 x 2049 fp32 57 (48), 100000 x 777 bf16 with
@@ -363,8 +367,10 @@ rmsnorm_block_kernel(const T* x, const T* residual, const T* __restrict__ weight
         }
     }
     // A block's reduction carries the maximum even where nobody asks for it: the few steps longer
-    // between a row's loads and its stores keep the memory busier (16384 x 7168 bf16, one array
-    // in and one out: 69 us against 74; no other form differs).
+    // between a row's loads and its stores keep the memory busier (bf16, one array in and one
+    // out, 117 M elements: rows of 4608 67.6 us against 72.2, 6144 67.8 and 70.4, 7168 68.4 and
+    // 72.8, 10240 68.2 and 73.0; 16384 75.0 and 74.5; narrower rows, fp32 and a residual the same
+    // either way).
     team_reduce<WARP ? 32 : 0, CODES || !WARP ? kMax : kAlone>(sum, top, red);
     const float r = rsqrtf(fmaf(sum, 1.0f / (float)d, eps));
     const float most = top * r;
@@ -646,7 +652,7 @@ __device__ __forceinline__ void open(const typename Raw<T, W>::type& v, float (&
     else unpack(v, f, (const T*)nullptr);
 }
 
-// Rows too wide for a ring of three (fp32 rows of more than 8192): straight from memory, twice
+// Rows too wide for a ring of three (fp32 rows past 9384 elements): straight from memory, twice
 // -- the second time from L2 -- by element where vectors do not tile them.
 template <typename T, int W, int EPT>
 __global__ void __launch_bounds__(1024)
@@ -792,7 +798,9 @@ cudaError_t forward(const NormArgs& a, cudaStream_t st) {
     if (nv <= kWarpVecs / 2) return go_blocks<T, 2, AL, true>(a, nv, st);
     if (nv <= kWarpVecs && a.rows > 8 * 152) return go_blocks<T, 4, AL, true>(a, nv, st);
     // Two vectors a thread, so that registers allow four blocks of 512; four a thread where a
-    // row is one array in and one out (16384 x 7168 bf16: 69 us against 75; with a residual 135
+    // row is one array in and one out (117 M elements of bf16: rows of 4608 67.6 us against 69.1,
+    // 5120 68.0 and 70.3, 7168 68.4 and 74.2, 8192 68.1 and 71.6; 59 M of fp32: 2304 68.5 and
+    // 67.0, 2880 68.5 and 69.1, 3584 68.5 and 70.0, 4096 68.4 and 68.3; with a residual 135
     // against 134).
     if (AL && !a.residual && !a.codes && nv > kBlockThreads && nv <= 2 * kBlockThreads)
         return go_blocks<T, 4, AL>(a, nv, st);
