@@ -38,32 +38,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr float kTinySum = 1e-18f;
 constexpr int kStages = 2;  // tiles a warp holds: one at hand, one on its way
 
-// ---- two fp32 values in a 64-bit register: one instruction works on both -----
-typedef uint64_t f2;
-__device__ __forceinline__ f2 pack2(float lo, float hi) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
-__device__ __forceinline__ void unpack2(f2 v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 __device__ __forceinline__ float ex2(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -212,8 +186,7 @@ __device__ __forceinline__ void copy_tile(float* dst, const float* src, int64_t 
     const uint32_t d = ptx::smem_u32(dst);
     const int whole = n > 0 ? (head + n) / 4 : 0;
     auto copy = [&](int i) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i * 16), "l"(g + i * 16)
-                     : "memory");
+        copy_async(d + i * 16, g + i * 16);
     };
     int i = lane;
     for (; i + 96 < whole; i += 128) {
@@ -229,7 +202,7 @@ __device__ __forceinline__ void copy_tile(float* dst, const float* src, int64_t 
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d + f * 4), "l"(g + f * 4)
                          : "memory");
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    copy_commit();
 }
 
 // n floats of a tile to dst + at, by the lanes; src is as far from a multiple of 16
@@ -300,7 +273,7 @@ struct Ring {
                 issue(cur + kStages);
             }
             ++cur;
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            copy_wait<kStages - 1>();
             __syncwarp();
         }
         return slot(i) + (L::kVec == 4 ? 0 : (int)((int64_t)(first + i * stride) * E & 3));

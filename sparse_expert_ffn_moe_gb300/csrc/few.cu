@@ -789,31 +789,14 @@ __device__ __forceinline__ void load_cols(uint32_t at, uint32_t (&v)[N]) {
     }
 }
 
-// ---- two fp32 values in a 64-bit register: one instruction works on both -----
-typedef uint64_t f2;
-__device__ __forceinline__ f2 pack2(float lo, float hi) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ f2 pack2(uint32_t lo, uint32_t hi) {
+// pairs of fp32 values from and to what tensor memory's loads give
+__device__ __forceinline__ f2 pack_bits(uint32_t lo, uint32_t hi) {
     return pack2(__uint_as_float(lo), __uint_as_float(hi));
 }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 template <int N>
-__device__ __forceinline__ void unpack2(const f2 (&v)[N / 2], float (&f)[N]) {
+__device__ __forceinline__ void unpack_pairs(const f2 (&v)[N / 2], float (&f)[N]) {
 #pragma unroll
-    for (int t = 0; t < N / 2; ++t)
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(f[2 * t]), "=f"(f[2 * t + 1]) : "l"(v[t]));
+    for (int t = 0; t < N / 2; ++t) unpack2(v[t], f[2 * t], f[2 * t + 1]);
 }
 
 // A down unit's bf16 sums: hi and lo plane, W columns each.
@@ -848,9 +831,9 @@ __device__ __forceinline__ void add_down(uint32_t at, const float* hs, const flo
             const float2 q = *reinterpret_cast<const float2*>(hs + 16 * i + 2 * t);
             f2 h = pack2(q.x, q.y);
             if constexpr (FMT == 2) h = mul2(h, pack2(bs[i], bs[i]));
-            const f2 mid = fma2(pack2(c[i][2 * W + 2 * t], c[i][2 * W + 2 * t + 1]), finer,
-                                pack2(c[i][W + 2 * t], c[i][W + 2 * t + 1]));
-            s[t] = fma2(fma2(mid, finer, pack2(c[i][2 * t], c[i][2 * t + 1])), h, s[t]);
+            const f2 mid = fma2(pack_bits(c[i][2 * W + 2 * t], c[i][2 * W + 2 * t + 1]), finer,
+                                pack_bits(c[i][W + 2 * t], c[i][W + 2 * t + 1]));
+            s[t] = fma2(fma2(mid, finer, pack_bits(c[i][2 * t], c[i][2 * t + 1])), h, s[t]);
         }
     }
 }
@@ -1081,8 +1064,8 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
             return __shfl_sync(0xffffffffu, good, 0) != 0;
         };
         const auto joined = [](const auto& v, int t) {  // x's two planes, tokens 2 t and 2 t + 1
-            return fma2(pack2(v[NT + 2 * t], v[NT + 2 * t + 1]), pack2(0.0625f, 0.0625f),
-                        pack2(v[2 * t], v[2 * t + 1]));
+            return fma2(pack_bits(v[NT + 2 * t], v[NT + 2 * t + 1]), pack2(0.0625f, 0.0625f),
+                        pack_bits(v[2 * t], v[2 * t + 1]));
         };
         // a K tile's block scale: all of a warp's rows have the same, a lane holds every 32nd
         struct BlockScales {
@@ -1177,12 +1160,12 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
 #pragma unroll
                         for (int t = 0; t < NT / 2; ++t) {
                             if constexpr (FMT) sums2[t] = joined(v, t);
-                            else sums2[t] = pack2(v[2 * t], v[2 * t + 1]);
+                            else sums2[t] = pack_bits(v[2 * t], v[2 * t + 1]);
                         }
                     }
                     if (!ok) break;
                     float s[NT];
-                    unpack2(sums2, s);
+                    unpack_pairs(sums2, s);
                     int c = 0;
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
@@ -1263,7 +1246,7 @@ few_experts_kernel(const __grid_constant__ FewArgs a) {
                         ok = ptx::named_bar_and(1, 128, ok);
                     }
                     if (!ok) break;
-                    if constexpr (FMT) unpack2(sums2, s);
+                    if constexpr (FMT) unpack_pairs(sums2, s);
                     if (col < a.d) {
 #pragma unroll
                         for (int t = 0; t < NT; ++t)

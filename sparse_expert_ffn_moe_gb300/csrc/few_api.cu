@@ -10,8 +10,6 @@ using namespace moe;
 
 namespace {
 
-bool good(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
-
 moe_status check_few(const moe_shape* shape) {
     const moe_status st = check_shape(shape);
     if (st != MOE_OK) return st;
@@ -21,8 +19,8 @@ moe_status check_few(const moe_shape* shape) {
 // what both kinds of call check and enqueue; c has the weights
 moe_status run(const moe_shape& s, int fmt, const FewCall& c, void* workspace, size_t ws_bytes,
                void* stream) {
-    if (!good(c.x) || !good(c.w_g) || !good(c.y) || ((uintptr_t)c.residual & 15u) ||
-        ((uintptr_t)c.bias & 3u))
+    if (!good(c.x) || !good(c.w_g) || !good(c.y) || !good_or_null(c.residual) ||
+        !good_or_null(c.bias, 4))
         return MOE_ERR_INVALID_ARG;
     const bool shared = s.inter_shared > 0;
     const void* routed[] = {c.w_gate, c.w_up, c.w_down};

@@ -284,6 +284,11 @@ cudaError_t launch_route_backward(const moe_shape& s, RouteBackwardArgs a, cudaS
 
 int device_sm_count();
 
+// p is a multiple of `to`; and present; or absent
+inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+inline bool good(const void* p, uintptr_t to = 16) { return p && aligned(p, to); }
+inline bool good_or_null(const void* p, uintptr_t to = 16) { return aligned(p, to); }
+
 // [p, p + n) and [q, q + m) share a byte (NULL shares none)
 inline bool overlap(const void* p, uint64_t n, const void* q, uint64_t m) {
     const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;

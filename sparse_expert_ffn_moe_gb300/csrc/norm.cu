@@ -479,13 +479,6 @@ rmsnorm_backward_kernel(const T* d_y, const T* s, const T* __restrict__ weight, 
 // Blocks that stay for many rows copy the next ones to shared memory while they work on one
 // (cp.async: neither registers nor barriers hold the copies up).  Used where blocks have to
 // stay, for the sums of d_w over rows, and for rows that 16-byte vectors do not tile.
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 constexpr int kDepth = 3;  // rows in a ring
 
 constexpr size_t kRingSmem = 220 * 1024;  // of an SM, for the rings of its blocks

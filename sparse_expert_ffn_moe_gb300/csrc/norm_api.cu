@@ -13,9 +13,6 @@ namespace {
 
 constexpr int64_t kMaxCols = 16384;
 
-bool good(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
-bool good_or_null(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 moe_status check_sizes(int64_t rows, int64_t cols) {

@@ -13,13 +13,7 @@ namespace {
 
 constexpr int32_t kMaxSeqs = 1 << 20;
 
-bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
-
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
-// present and aligned / absent or aligned
-bool good(const void* p, uintptr_t to) { return p && aligned(p, to); }
-bool good_or_null(const void* p, uintptr_t to) { return aligned(p, to); }
 
 // Error block (the record at its start, the ticket of the last block at
 // kTicket), then the shares of the loss and the partial rows.
